@@ -8,7 +8,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflashopt.so")
-SOURCES = [os.path.join(CSRC, "flashopt_kernels.hip"), os.path.join(CSRC, "flashopt_api.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in ("flashopt_kernels.hip", "flashopt_grad.hip",
+                                                 "flashopt_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",

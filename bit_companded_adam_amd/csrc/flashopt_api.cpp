@@ -5,9 +5,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 
@@ -194,6 +196,7 @@ flashopt_status adamw_scalars(const flashopt_adamw_args *a, StepScalars &sc)
     if (!(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0)) return FLASHOPT_EINVAL;
     if (!(a->eps >= 0.0) || !std::isfinite(a->eps)) return FLASHOPT_EINVAL;
     if (!std::isfinite(a->weight_decay)) return FLASHOPT_EINVAL;
+    if (!aligned(a->grad_scale, 4)) return FLASHOPT_EALIGN;
     const double t = static_cast<double>(a->step);
     sc.blk = state_layout(a->state_layout, a->master_bits, true);
     sc.cwd = static_cast<float>(1.0 - a->lr * a->weight_decay);
@@ -221,6 +224,8 @@ flashopt_status adamw_scalars(const flashopt_adamw_args *a, StepScalars &sc)
         sc.rbc1 = r;
     }
     sc.unit_bc = (sc.bc1 == 1.0f ? 1 : 0) | (sc.bc2 == 1.0f ? 2 : 0);
+    sc.grad_scale = a->grad_scale;
+    sc.gs = 1.0f;
     sc.lr2 = sc.lr * 0x1p32f;
     sc.eps2 = sc.eps * 0x1p32f;
     sc.kv = static_cast<float>(255.0 * std::sqrt(static_cast<double>(sc.bc2)) * 0x1p-32);
@@ -279,6 +284,7 @@ flashopt_status sgd_scalars(const flashopt_sgd_args *a, SgdScalars &sc)
     if (!(a->momentum > 0.0) || !std::isfinite(a->momentum)) return FLASHOPT_EINVAL;
     if (!std::isfinite(a->dampening) || !std::isfinite(a->weight_decay)) return FLASHOPT_EINVAL;
     if (a->nesterov && a->dampening != 0.0) return FLASHOPT_EINVAL;
+    if (!aligned(a->grad_scale, 4)) return FLASHOPT_EALIGN;
     if (a->state_layout != FLASHOPT_STATE_STREAMS && a->state_layout != FLASHOPT_STATE_BLOCKED)
         return FLASHOPT_EINVAL;
     if (a->state_layout == FLASHOPT_STATE_BLOCKED && a->fp32_states) return FLASHOPT_EINVAL;
@@ -290,6 +296,8 @@ flashopt_status sgd_scalars(const flashopt_sgd_args *a, SgdScalars &sc)
     sc.has_wd = a->weight_decay != 0.0 ? 1 : 0;
     sc.first = a->step == 1 ? 1 : 0;
     sc.nesterov = a->nesterov;
+    sc.grad_scale = a->grad_scale;
+    sc.gs = 1.0f;
     return FLASHOPT_OK;
 }
 
@@ -450,13 +458,14 @@ bool same_variant(const flashopt_adamw_args &a, const flashopt_adamw_plan_info &
 {
     return info.master_bits == a.master_bits && info.companded == a.companded &&
            info.fp32_states == a.fp32_states && info.param_fp32 == a.param_fp32 &&
-           info.state_layout == a.state_layout;
+           info.state_layout == a.state_layout && info.grad_scaled == (a.grad_scale != nullptr);
 }
 
 bool same_variant(const flashopt_sgd_args &a, const flashopt_sgd_plan_info &info)
 {
     return info.master_bits == a.master_bits && info.companded == a.companded &&
-           info.fp32_states == a.fp32_states && info.state_layout == a.state_layout;
+           info.fp32_states == a.fp32_states && info.state_layout == a.state_layout &&
+           info.grad_scaled == (a.grad_scale != nullptr);
 }
 
 // The launch-time checks shared by both plan kinds: counts, then the buffer.
@@ -481,6 +490,125 @@ bool valid_variant(int master_bits, int companded, int fp32_states)
 bool valid_layout(int layout, int fp32_states)
 {
     return layout == FLASHOPT_STATE_STREAMS || (layout == FLASHOPT_STATE_BLOCKED && fp32_states == 0);
+}
+
+// ---- gradient norm and clipping
+
+using flashopt::GradDesc;
+using flashopt::GradSums;
+
+size_t grad_table_bytes(int n)
+{
+    const size_t b = sizeof(GradDesc) * static_cast<size_t>(n) + sizeof(int32_t) * (static_cast<size_t>(n) + 1);
+    return (b + 15) & ~static_cast<size_t>(15);
+}
+
+int64_t grad_chunks(int64_t numel)
+{
+    return numel / flashopt::kGradChunk + (numel % flashopt::kGradChunk != 0);
+}
+
+// Validation of a gradient list; total = its chunks.
+flashopt_status check_grads(const flashopt_grad *grads, int n, int64_t &total)
+{
+    total = 0;
+    if (n < 0 || (n > 0 && !grads)) return FLASHOPT_EINVAL;
+    for (int i = 0; i < n; ++i) {
+        const flashopt_grad &g = grads[i];
+        if (g.numel < 0 || (g.fp32 != 0 && g.fp32 != 1)) return FLASHOPT_EINVAL;
+        if (g.numel == 0) continue;
+        if (!g.data) return FLASHOPT_EINVAL;
+        if (!aligned(g.data, g.fp32 ? 4 : 2)) return FLASHOPT_EALIGN;
+        total += grad_chunks(g.numel);
+        if (total > INT32_MAX) return FLASHOPT_EINVAL;
+    }
+    return FLASHOPT_OK;
+}
+
+// Whether two gradients of a list share memory: clipping would then scale
+// the shared elements twice, in an order that nothing fixes.
+flashopt_status check_disjoint(const flashopt_grad *grads, int n)
+{
+    struct Range { uintptr_t first, last; };
+    std::unique_ptr<Range[]> r(new (std::nothrow) Range[static_cast<size_t>(n) + 1]);
+    if (!r) return FLASHOPT_EHIP;
+    int k = 0;
+    for (int i = 0; i < n; ++i) {
+        if (grads[i].numel == 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i].data);
+        r[k++] = Range{a, a + static_cast<uintptr_t>(grads[i].numel) * (grads[i].fp32 ? 4u : 2u)};
+    }
+    std::sort(r.get(), r.get() + k, [](const Range &a, const Range &b) { return a.first < b.first; });
+    for (int i = 1; i < k; ++i)
+        if (r[i].first < r[i - 1].last) return FLASHOPT_EINVAL;
+    return FLASHOPT_OK;
+}
+
+// Descriptors, then n + 1 chunk starts.
+void fill_grad_table(const flashopt_grad *grads, int n, GradDesc *desc, int32_t *start)
+{
+    int32_t acc = 0;
+    for (int i = 0; i < n; ++i) {
+        desc[i] = GradDesc{grads[i].data, grads[i].numel, grads[i].fp32, 0};
+        start[i] = acc;
+        acc += static_cast<int32_t>(grad_chunks(grads[i].numel));
+    }
+    start[n] = acc;
+}
+
+// The arguments that a norm and a clip share, after the list's.
+flashopt_status check_norm(double max_norm, const float *out)
+{
+    if (!(max_norm >= 0.0) || !out) return FLASHOPT_EINVAL;     // NaN fails, infinity passes
+    return aligned(out, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
+}
+
+flashopt_status grad_call(const flashopt_grad *grads, int n, double max_norm, bool clip, float *out,
+                          void *workspace, size_t ws_bytes, void *stream)
+{
+    int64_t total = 0;
+    flashopt_status cs = check_grads(grads, n, total);
+    if (cs != FLASHOPT_OK) return cs;
+    if ((cs = check_norm(max_norm, out)) != FLASHOPT_OK) return cs;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (total == 0) return hip_status(flashopt::launch_grad_empty(max_norm, out, st));
+    if (clip && (cs = check_disjoint(grads, n)) != FLASHOPT_OK) return cs;
+    if (!workspace || ws_bytes < flashopt_grad_workspace_bytes(n)) return FLASHOPT_EWORKSPACE;
+    if (!aligned(workspace, 16)) return FLASHOPT_EALIGN;
+    GradSums *sums = static_cast<GradSums *>(workspace);
+    const int32_t chunks = static_cast<int32_t>(total);
+    if (n <= flashopt::kGradArgTensors) {
+        GradDesc desc[flashopt::kGradArgTensors];
+        int32_t start[flashopt::kGradArgTensors + 1];
+        fill_grad_table(grads, n, desc, start);
+        return hip_status(flashopt::launch_grad_args(desc, start, n, chunks, max_norm, clip, sums, out, st));
+    }
+    GradDesc *table = reinterpret_cast<GradDesc *>(sums + 1);
+    const flashopt_status ss = stage_copy(table, grad_table_bytes(n), st, [&](void *host) {
+        GradDesc *d = static_cast<GradDesc *>(host);
+        fill_grad_table(grads, n, d, reinterpret_cast<int32_t *>(d + n));
+    });
+    if (ss != FLASHOPT_OK) return ss;
+    return hip_status(flashopt::launch_grad_table(table, reinterpret_cast<const int32_t *>(table + n), n,
+                                                  chunks, max_norm, clip, sums, out, st));
+}
+
+flashopt_status grad_plan_call(const flashopt_grad_plan_info *info, void *plan, double max_norm,
+                               bool clip, float *out, void *stream)
+{
+    if (!info) return FLASHOPT_EINVAL;
+    const flashopt_status cs = check_norm(max_norm, out);
+    if (cs != FLASHOPT_OK) return cs;
+    const flashopt_status lc = plan_launch_checks(info->n_tensors, info->total_chunks, plan);
+    if (lc != FLASHOPT_OK) return lc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (info->total_chunks == 0) return hip_status(flashopt::launch_grad_empty(max_norm, out, st));
+    if (clip && info->overlap) return FLASHOPT_EINVAL;
+    GradSums *sums = static_cast<GradSums *>(plan);
+    const GradDesc *table = reinterpret_cast<const GradDesc *>(sums + 1);
+    return hip_status(flashopt::launch_grad_table(
+        table, reinterpret_cast<const int32_t *>(table + info->n_tensors), info->n_tensors,
+        info->total_chunks, max_norm, clip, sums, out, st));
 }
 
 // Host image of the allocation-free step's scalar block and chunk table:
@@ -575,7 +703,7 @@ flashopt_status flashopt_adamw_step(const flashopt_tensor *tensors, int n_tensor
                                 int32_t total, hipStream_t st) {
                                 return flashopt::launch_adamw_step(
                                     reinterpret_cast<const StepScalars *>(h), d, cs, n_tensors,
-                                    total, kernel_format(*a), states, st);
+                                    total, kernel_format(*a), states, sc.grad_scale != nullptr, st);
                             });
 }
 
@@ -623,7 +751,8 @@ flashopt_status flashopt_adamw_step_noalloc(const flashopt_tensor *tensors, int 
     const int32_t *d_start = reinterpret_cast<const int32_t *>(d_desc + n_tensors);
     return hip_status(flashopt::launch_adamw_step(reinterpret_cast<const StepScalars *>(base), d_desc,
                                                   d_start, n_tensors, acc, kernel_format(*a),
-                                                  states_of(a->fp32_states, a->companded), st));
+                                                  states_of(a->fp32_states, a->companded),
+                                                  sc.grad_scale != nullptr, st));
 }
 
 size_t flashopt_adamw_plan_bytes(int n_tensors)
@@ -645,6 +774,7 @@ flashopt_status flashopt_adamw_plan(const flashopt_tensor *tensors, int n_tensor
     out.fp32_states = a->fp32_states;
     out.param_fp32 = a->param_fp32;
     out.state_layout = a->state_layout;
+    out.grad_scaled = a->grad_scale != nullptr;
     const flashopt_status ps = make_plan(tensors, n_tensors, a->master_bits, a->fp32_states == 0, true,
                                          a->state_layout == FLASHOPT_STATE_BLOCKED, sc, plan,
                                          plan_bytes, out, stream);
@@ -668,7 +798,8 @@ flashopt_status flashopt_adamw_plan_launch(const flashopt_adamw_plan_info *info,
     if (!info) return FLASHOPT_EINVAL;
     if (!valid_variant(info->master_bits, info->companded, info->fp32_states) ||
         (info->param_fp32 != 0 && info->param_fp32 != 1) || (info->param_fp32 && info->master_bits != 0) ||
-        !valid_layout(info->state_layout, info->fp32_states))
+        !valid_layout(info->state_layout, info->fp32_states) ||
+        (info->grad_scaled != 0 && info->grad_scaled != 1))
         return FLASHOPT_EINVAL;
     const flashopt_status lc = plan_launch_checks(info->n_tensors, info->total_chunks, plan);
     if (lc != FLASHOPT_OK || info->total_chunks == 0) return lc;
@@ -680,6 +811,7 @@ flashopt_status flashopt_adamw_plan_launch(const flashopt_adamw_plan_info *info,
                                                   p.start, info->n_tensors, info->total_chunks,
                                                   kernel_format(a),
                                                   states_of(info->fp32_states, info->companded),
+                                                  info->grad_scaled != 0,
                                                   static_cast<hipStream_t>(stream)));
 }
 
@@ -707,7 +839,7 @@ flashopt_status flashopt_sgd_step(const flashopt_tensor *tensors, int n_tensors,
                                 int32_t total, hipStream_t st) {
                                 return flashopt::launch_sgd_step(
                                     reinterpret_cast<const SgdScalars *>(h), d, cs, n_tensors, total,
-                                    a->master_bits, states, st);
+                                    a->master_bits, states, sc.grad_scale != nullptr, st);
                             });
 }
 
@@ -729,6 +861,7 @@ flashopt_status flashopt_sgd_plan(const flashopt_tensor *tensors, int n_tensors,
     out.companded = a->companded;
     out.fp32_states = a->fp32_states;
     out.state_layout = a->state_layout;
+    out.grad_scaled = a->grad_scale != nullptr;
     const flashopt_status ps = make_plan(tensors, n_tensors, a->master_bits, a->fp32_states == 0, false,
                                          a->state_layout == FLASHOPT_STATE_BLOCKED, sc, plan,
                                          plan_bytes, out, stream);
@@ -751,7 +884,8 @@ flashopt_status flashopt_sgd_plan_launch(const flashopt_sgd_plan_info *info, con
 {
     if (!info) return FLASHOPT_EINVAL;
     if (!valid_variant(info->master_bits, info->companded, info->fp32_states) ||
-        !valid_layout(info->state_layout, info->fp32_states))
+        !valid_layout(info->state_layout, info->fp32_states) ||
+        (info->grad_scaled != 0 && info->grad_scaled != 1))
         return FLASHOPT_EINVAL;
     const flashopt_status lc = plan_launch_checks(info->n_tensors, info->total_chunks, plan);
     if (lc != FLASHOPT_OK || info->total_chunks == 0) return lc;
@@ -760,6 +894,7 @@ flashopt_status flashopt_sgd_plan_launch(const flashopt_sgd_plan_info *info, con
                                                 p.start, info->n_tensors, info->total_chunks,
                                                 info->master_bits,
                                                 states_of(info->fp32_states, info->companded),
+                                                info->grad_scaled != 0,
                                                 static_cast<hipStream_t>(stream)));
 }
 
@@ -776,6 +911,70 @@ flashopt_status flashopt_sgd_step_tensor(const flashopt_tensor *tensor,
     return hip_status(flashopt::launch_sgd_tensor(device_descriptor(*tensor), sc, a->master_bits,
                                                   states_of(a->fp32_states, a->companded),
                                                   static_cast<hipStream_t>(stream)));
+}
+
+size_t flashopt_grad_workspace_bytes(int n_tensors)
+{
+    if (n_tensors <= 0) return 0;
+    return sizeof(GradSums) + (n_tensors > flashopt::kGradArgTensors ? grad_table_bytes(n_tensors) : 0);
+}
+
+flashopt_status flashopt_grad_norm(const flashopt_grad *grads, int n_tensors, double max_norm,
+                                   float *out, void *workspace, size_t ws_bytes, void *stream)
+{
+    return grad_call(grads, n_tensors, max_norm, false, out, workspace, ws_bytes, stream);
+}
+
+flashopt_status flashopt_grad_clip(const flashopt_grad *grads, int n_tensors, double max_norm,
+                                   float *out, void *workspace, size_t ws_bytes, void *stream)
+{
+    return grad_call(grads, n_tensors, max_norm, true, out, workspace, ws_bytes, stream);
+}
+
+size_t flashopt_grad_plan_bytes(int n_tensors)
+{
+    return n_tensors <= 0 ? 0 : sizeof(GradSums) + grad_table_bytes(n_tensors);
+}
+
+flashopt_status flashopt_grad_plan(const flashopt_grad *grads, int n_tensors, void *plan,
+                                   size_t plan_bytes, flashopt_grad_plan_info *info, void *stream)
+{
+    if (!info) return FLASHOPT_EINVAL;
+    int64_t total = 0;
+    const flashopt_status cs = check_grads(grads, n_tensors, total);
+    if (cs != FLASHOPT_OK) return cs;
+    flashopt_grad_plan_info out{};
+    out.n_tensors = n_tensors;
+    out.total_chunks = static_cast<int32_t>(total);
+    if (n_tensors > 0) {
+        const size_t need = flashopt_grad_plan_bytes(n_tensors);
+        if (!plan || plan_bytes < need) return FLASHOPT_EWORKSPACE;
+        if (!aligned(plan, 16)) return FLASHOPT_EALIGN;
+        const flashopt_status ds = check_disjoint(grads, n_tensors);
+        if (ds == FLASHOPT_EHIP) return ds;
+        out.overlap = ds != FLASHOPT_OK;
+        const flashopt_status ss = stage_copy(plan, need, static_cast<hipStream_t>(stream), [&](void *host) {
+            GradSums *sums = static_cast<GradSums *>(host);
+            std::memset(sums, 0, sizeof(GradSums));
+            GradDesc *d = reinterpret_cast<GradDesc *>(sums + 1);
+            fill_grad_table(grads, n_tensors, d, reinterpret_cast<int32_t *>(d + n_tensors));
+        });
+        if (ss != FLASHOPT_OK) return ss;
+    }
+    *info = out;
+    return FLASHOPT_OK;
+}
+
+flashopt_status flashopt_grad_plan_norm(const flashopt_grad_plan_info *info, void *plan, double max_norm,
+                                        float *out, void *stream)
+{
+    return grad_plan_call(info, plan, max_norm, false, out, stream);
+}
+
+flashopt_status flashopt_grad_plan_clip(const flashopt_grad_plan_info *info, void *plan, double max_norm,
+                                        float *out, void *stream)
+{
+    return grad_plan_call(info, plan, max_norm, true, out, stream);
 }
 
 }  // extern "C"

@@ -74,6 +74,8 @@ struct StepScalars {
     int fast;           // 1 when eps and lr keep the short routes exact (see adamw_scalars)
     int unit_bc;        // bit 0: bc1 is exactly 1, bit 1: bc2 is exactly 1 (later in training)
     StateLayout blk;    // the state layout
+    float gs;           // the value at grad_scale, which the kernels fill in
+    const float *grad_scale;   // device factor on every gradient, or NULL
 };
 // The list step kernels (AdamW and FlashSGD) read their scalars from device
 // memory: a block of kScalarsBytes at the start of the staged table (the
@@ -93,6 +95,8 @@ struct SgdScalars {
     int first;      // step == 1: the buffer is set to the gradient
     int nesterov;
     StateLayout blk;    // the state layout (no v parts)
+    float gs;           // as in StepScalars
+    const float *grad_scale;
 };
 static_assert(sizeof(SgdScalars) <= kScalarsBytes, "scalar block");
 
@@ -116,17 +120,52 @@ hipError_t launch_reconstruct(const uint16_t *param, const void *rho, int64_t n,
                               int master_bits, float *master, hipStream_t stream);
 // scalars / tensors / chunk_start are device pointers into the staged
 // table; chunk_start has n_tensors + 1 entries.  master_bits: 24 | 32 | 0
-// (no split) | kParamF32 (AdamW only); states: one of kStates*.
+// (no split) | kParamF32 (AdamW only); states: one of kStates*; scaled: the
+// scalars hold a grad_scale.
 hipError_t launch_adamw_step(const StepScalars *scalars, const DevTensor *tensors,
                              const int32_t *chunk_start, int n_tensors, int32_t total_chunks,
-                             int master_bits, int states, hipStream_t stream);
+                             int master_bits, int states, bool scaled, hipStream_t stream);
 hipError_t launch_sgd_step(const SgdScalars *scalars, const DevTensor *tensors,
                            const int32_t *chunk_start, int n_tensors, int32_t total_chunks,
-                           int master_bits, int states, hipStream_t stream);
+                           int master_bits, int states, bool scaled, hipStream_t stream);
 // One tensor, its descriptor passed in the kernel arguments (no workspace).
 hipError_t launch_adamw_tensor(const DevTensor &d, const StepScalars &sc, int master_bits,
                                int states, hipStream_t stream);
 hipError_t launch_sgd_tensor(const DevTensor &d, const SgdScalars &sc, int master_bits,
                              int states, hipStream_t stream);
+
+
+// ---- gradient norm and clipping (flashopt_grad.hip)
+
+// One gradient of a list; the chunk table counts kGradChunk elements (two or
+// four 16-byte loads of a 256-thread workgroup).
+struct GradDesc {
+    void *data;
+    int64_t numel;
+    int32_t fp32;      // 0: bf16, 1: fp32
+    int32_t pad;
+};
+static_assert(sizeof(GradDesc) == 24, "descriptor layout");
+constexpr int kGradChunk = 4096;
+// Workgroups of a launch at most: eight to a CU, which all run at once.
+constexpr int kGradPartials = 2048;
+// Lists up to this length travel in the kernel arguments.
+constexpr int kGradArgTensors = 64;
+
+// The head of a norm's workspace or plan: how many workgroups of the launch
+// in flight have stored their partial sum (zero between launches), and the
+// partial sums.
+struct GradSums {
+    uint32_t finished;
+    uint32_t pad[31];
+    double partial[kGradPartials];
+};
+static_assert(sizeof(GradSums) % 128 == 0, "table alignment");
+
+hipError_t launch_grad_args(const GradDesc *desc, const int32_t *start, int n, int32_t total,
+                            double max_norm, bool clip, GradSums *sums, float *out, hipStream_t st);
+hipError_t launch_grad_table(const GradDesc *desc, const int32_t *start, int n, int32_t total,
+                             double max_norm, bool clip, GradSums *sums, float *out, hipStream_t st);
+hipError_t launch_grad_empty(double max_norm, float *out, hipStream_t st);
 
 }  // namespace flashopt

@@ -1010,7 +1010,8 @@ __device__ __forceinline__ float reconstruct_perm(const uint32_t (&pw)[W], const
 // Element j of a unit: the master theta (reconstructed, or the bf16 value
 // itself without a split), and the new moments m1 = b1 m0 + (1 - b1) g and
 // v1 = b2 v0 + ((1 - b2) g) g from the dequantized (or fp32) old ones.
-template <int MB, int ST, int N>
+// SCALED multiplies the gradient by sc.gs first (one fp32 rounding).
+template <int MB, int ST, int N, bool SCALED>
 __device__ __forceinline__ void element_moments(const UnitIn<MB, ST, N> &in, int j,
                                                 const StepScalars &sc, const float *s_mu,
                                                 const float *s_vu, float ms, float vs,
@@ -1025,6 +1026,7 @@ __device__ __forceinline__ void element_moments(const UnitIn<MB, ST, N> &in, int
         else theta = reconstruct_perm<MB>(in.pw, in.rw, j);
         g = (j & 1) ? bf16_hi(in.gw[j >> 1]) : bf16_lo(in.gw[j >> 1]);
     }
+    if constexpr (SCALED) g = g * sc.gs;
     float m0, v0;
     if constexpr (ST == kStatesFp32) {
         m0 = __uint_as_float(in.mf[j]);
@@ -1049,7 +1051,7 @@ __device__ __forceinline__ void element_moments(const UnitIn<MB, ST, N> &in, int
 // rounded division and sqrt, and encode and split with the NaN-safe element
 // routines.  The variance codes, fp32 moments and the group scales do not
 // depend on these paths and are produced by the caller.
-template <int MB, int ST, int N>
+template <int MB, int ST, int N, bool SCALED>
 __device__ __forceinline__ void unit_exact(const ChunkPtrs &c, uint32_t r, int cnt,
                                            const StepScalars &sc, const float *s_mu,
                                            const float *s_vu, uint32_t sm,
@@ -1069,7 +1071,7 @@ __device__ __forceinline__ void unit_exact(const ChunkPtrs &c, uint32_t r, int c
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         float theta, m, v;
-        element_moments<MB, ST, N>(in, j, sc, s_mu, s_vu, ms, vs, theta, m, v);
+        element_moments<MB, ST, N, SCALED>(in, j, sc, s_mu, s_vu, ms, vs, theta, m, v);
         const float thd = theta * sc.cwd;
         const float mhat = m / sc.bc1;
         const float vhat = v / sc.bc2;
@@ -1191,7 +1193,7 @@ __device__ __forceinline__ void update_terms(const float (&m1)[N], const float (
 // this for the same unit.  FULL units use straight-line streaming stores; at
 // the ragged end of a tensor stores are masked per element and groups padded
 // with zeros.
-template <int MB, int ST, int N, bool FULL>
+template <int MB, int ST, int N, bool FULL, bool SCALED>
 __device__ __forceinline__ void step_finish(const ChunkPtrs &c, uint32_t r, int cnt, int lane,
                                             const UnitIn<MB, ST, N> &in, const StepScalars &sc,
                                             const float *s_mu, const float *s_vu)
@@ -1208,7 +1210,7 @@ __device__ __forceinline__ void step_finish(const ChunkPtrs &c, uint32_t r, int 
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         float theta;
-        element_moments<MB, ST, N>(in, j, sc, s_mu, s_vu, ms, vs, theta, m1[j], v1[j]);
+        element_moments<MB, ST, N, SCALED>(in, j, sc, s_mu, s_vu, ms, vs, theta, m1[j], v1[j]);
         thd[j] = theta * sc.cwd;
         vbits = max(vbits, __float_as_uint(v1[j]));
     }
@@ -1289,7 +1291,7 @@ __device__ __forceinline__ void step_finish(const ChunkPtrs &c, uint32_t r, int 
         // is recomputed from its inputs in memory with the generic
         // operations; nothing has been stored yet, and the group scales
         // above are already exact
-        unit_exact<MB, ST, N>(c, r, cnt, sc, s_mu, s_vu, sm_out, mo, po, ro);
+        unit_exact<MB, ST, N, SCALED>(c, r, cnt, sc, s_mu, s_vu, sm_out, mo, po, ro);
     }
 
     // ---- stores
@@ -1337,7 +1339,7 @@ __device__ __forceinline__ void step_finish(const ChunkPtrs &c, uint32_t r, int 
 // master re-split.
 // There is no division: only non-finite values need the element-wise
 // NaN-safe encoders, which run on the same registers.
-template <int MB, int ST, int N, bool FULL>
+template <int MB, int ST, int N, bool FULL, bool SCALED>
 __device__ __forceinline__ void sgd_finish(const ChunkPtrs &c, uint32_t r, int cnt, int lane,
                                            const UnitIn<MB, ST, N> &in, const SgdScalars &sc,
                                            const float *s_mu)
@@ -1355,6 +1357,7 @@ __device__ __forceinline__ void sgd_finish(const ChunkPtrs &c, uint32_t r, int c
         if constexpr (MB == 0) theta = (j & 1) ? bf16_hi(in.pw[j >> 1]) : bf16_lo(in.pw[j >> 1]);
         else theta = reconstruct_perm<MB>(in.pw, in.rw, j);
         float d = (j & 1) ? bf16_hi(in.gw[j >> 1]) : bf16_lo(in.gw[j >> 1]);
+        if constexpr (SCALED) d = d * sc.gs;
         if (sc.has_wd) {
             const float decay = sc.wd * theta;
             d = d + decay;
@@ -1542,14 +1545,20 @@ __device__ __forceinline__ void build_tables(const TableEntries &e, float *s_mu,
 // the two 256-entry dequantization tables in LDS.  The step's scalars are read from the
 // staged table (scalar loads, uniform across the wavefront), not from the
 // kernel arguments, so that a captured launch steps with whatever scalars
-// were written there before it runs.
-template <int MB, int ST>
+// were written there before it runs.  SCALED kernels (clipping by the global
+// norm, loss scaling) read the factor on the gradients from device memory as
+// well, so a norm computed earlier on the stream reaches the step without
+// the host and without a second pass over the gradients; they are kernels of
+// their own because each instruction per element costs the unscaled step
+// 0.5-0.8% of its time.
+template <int MB, int ST, bool SCALED>
 __global__ void __launch_bounds__(kBlockThreads)
 adamw_step_kernel(const StepScalars *__restrict__ scalars, const DevTensor *__restrict__ tensors,
                   const int32_t *__restrict__ chunk_start, int n_tensors, int32_t chunk_base,
                   int32_t chunk_end)
 {
-    const StepScalars sc = *scalars;
+    StepScalars sc = *scalars;
+    if constexpr (SCALED) sc.gs = *sc.grad_scale;
     constexpr int kN = unit_elems(MB, ST);
     constexpr int kUnits = kLaneElems / kN;
     __shared__ float s_mu[256];
@@ -1564,20 +1573,21 @@ adamw_step_kernel(const StepScalars *__restrict__ scalars, const DevTensor *__re
         [&](const ChunkPtrs &cp, int u) { load_chunk_unit<MB, ST, kN>(cp, u, lane, r, cnt, in); },
         [&] { build_tables<ST, true>(te, s_mu, s_vu); },
         [&](const ChunkPtrs &cp) {
-            if (cp.rem == kChunkElems) step_finish<MB, ST, kN, true>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
-            else step_finish<MB, ST, kN, false>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
+            if (cp.rem == kChunkElems) step_finish<MB, ST, kN, true, SCALED>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
+            else step_finish<MB, ST, kN, false, SCALED>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
         });
 }
 
 // The fused FlashSGD step (same grid and tables, momentum only; scalars read
 // from the staged table like the AdamW step's).
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 __global__ void __launch_bounds__(kBlockThreads)
 sgd_step_kernel(const SgdScalars *__restrict__ scalars, const DevTensor *__restrict__ tensors,
                 const int32_t *__restrict__ chunk_start, int n_tensors, int32_t chunk_base,
                 int32_t chunk_end)
 {
-    const SgdScalars sc = *scalars;
+    SgdScalars sc = *scalars;
+    if constexpr (SCALED) sc.gs = *sc.grad_scale;
     constexpr int kN = unit_elems(MB, ST);
     constexpr int kUnits = kLaneElems / kN;
     __shared__ float s_mu[256];
@@ -1591,17 +1601,18 @@ sgd_step_kernel(const SgdScalars *__restrict__ scalars, const DevTensor *__restr
         [&](const ChunkPtrs &cp, int u) { load_chunk_unit<MB, ST, kN, false>(cp, u, lane, r, cnt, in); },
         [&] { build_tables<ST, false>(te, s_mu, nullptr); },
         [&](const ChunkPtrs &cp) {
-            if (cp.rem == kChunkElems) sgd_finish<MB, ST, kN, true>(cp, r, cnt, lane, in, sc, s_mu);
-            else sgd_finish<MB, ST, kN, false>(cp, r, cnt, lane, in, sc, s_mu);
+            if (cp.rem == kChunkElems) sgd_finish<MB, ST, kN, true, SCALED>(cp, r, cnt, lane, in, sc, s_mu);
+            else sgd_finish<MB, ST, kN, false, SCALED>(cp, r, cnt, lane, in, sc, s_mu);
         });
 }
 
 // Single-tensor forms (the descriptor travels in the kernel arguments, no
 // chunk table).
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 __global__ void __launch_bounds__(kBlockThreads)
 adamw_tensor_kernel(DevTensor d, StepScalars sc, int32_t chunk_base, int32_t chunk_end)
 {
+    if constexpr (SCALED) sc.gs = *sc.grad_scale;
     constexpr int kN = unit_elems(MB, ST);
     constexpr int kUnits = kLaneElems / kN;
     __shared__ float s_mu[256];
@@ -1616,15 +1627,16 @@ adamw_tensor_kernel(DevTensor d, StepScalars sc, int32_t chunk_base, int32_t chu
         [&](const ChunkPtrs &cp, int u) { load_chunk_unit<MB, ST, kN>(cp, u, lane, r, cnt, in); },
         [&] { build_tables<ST, true>(te, s_mu, s_vu); },
         [&](const ChunkPtrs &cp) {
-            if (cp.rem == kChunkElems) step_finish<MB, ST, kN, true>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
-            else step_finish<MB, ST, kN, false>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
+            if (cp.rem == kChunkElems) step_finish<MB, ST, kN, true, SCALED>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
+            else step_finish<MB, ST, kN, false, SCALED>(cp, r, cnt, lane, in, sc, s_mu, s_vu);
         });
 }
 
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 __global__ void __launch_bounds__(kBlockThreads)
 sgd_tensor_kernel(DevTensor d, SgdScalars sc, int32_t chunk_base, int32_t chunk_end)
 {
+    if constexpr (SCALED) sc.gs = *sc.grad_scale;
     constexpr int kN = unit_elems(MB, ST);
     constexpr int kUnits = kLaneElems / kN;
     __shared__ float s_mu[256];
@@ -1638,8 +1650,8 @@ sgd_tensor_kernel(DevTensor d, SgdScalars sc, int32_t chunk_base, int32_t chunk_
         [&](const ChunkPtrs &cp, int u) { load_chunk_unit<MB, ST, kN, false>(cp, u, lane, r, cnt, in); },
         [&] { build_tables<ST, false>(te, s_mu, nullptr); },
         [&](const ChunkPtrs &cp) {
-            if (cp.rem == kChunkElems) sgd_finish<MB, ST, kN, true>(cp, r, cnt, lane, in, sc, s_mu);
-            else sgd_finish<MB, ST, kN, false>(cp, r, cnt, lane, in, sc, s_mu);
+            if (cp.rem == kChunkElems) sgd_finish<MB, ST, kN, true, SCALED>(cp, r, cnt, lane, in, sc, s_mu);
+            else sgd_finish<MB, ST, kN, false, SCALED>(cp, r, cnt, lane, in, sc, s_mu);
         });
 }
 
@@ -1776,46 +1788,47 @@ hipError_t launch_units(Kernel kernel, int32_t total_chunks, hipStream_t st, Arg
     return hipSuccess;
 }
 
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 hipError_t step_variant(const DevTensor *tensors, const int32_t *chunk_start, int n_tensors,
                         int32_t total_chunks, const StepScalars *scalars, hipStream_t st)
 {
-    return launch_units<MB, ST>(adamw_step_kernel<MB, ST>, total_chunks, st, scalars, tensors,
+    return launch_units<MB, ST>(adamw_step_kernel<MB, ST, SCALED>, total_chunks, st, scalars, tensors,
                                 chunk_start, n_tensors);
 }
 
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 hipError_t sgd_variant(const DevTensor *tensors, const int32_t *chunk_start, int n_tensors,
                        int32_t total_chunks, const SgdScalars *scalars, hipStream_t st)
 {
-    return launch_units<MB, ST>(sgd_step_kernel<MB, ST>, total_chunks, st, scalars, tensors,
+    return launch_units<MB, ST>(sgd_step_kernel<MB, ST, SCALED>, total_chunks, st, scalars, tensors,
                                 chunk_start, n_tensors);
 }
 
 // The (master_bits, states) instantiations of one step kernel family: nine,
-// plus the three fp32-parameter ones where the family has them.
-template <template <int, int> class K, typename Sc>
+// plus the three fp32-parameter ones where the family has them, each with
+// and without a factor on the gradients.
+template <template <int, int, bool> class K, bool SCALED, typename Sc>
 hipError_t dispatch(int master_bits, int states, const DevTensor *tensors,
                     const int32_t *chunk_start, int n_tensors, int32_t total_chunks,
                     const Sc &sc, hipStream_t st)
 {
     switch (master_bits * 4 + states) {
-    case 24 * 4 + kStatesCompanded: return K<24, kStatesCompanded>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case 24 * 4 + kStatesLinear: return K<24, kStatesLinear>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case 24 * 4 + kStatesFp32: return K<24, kStatesFp32>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case 32 * 4 + kStatesCompanded: return K<32, kStatesCompanded>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case 32 * 4 + kStatesLinear: return K<32, kStatesLinear>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case 32 * 4 + kStatesFp32: return K<32, kStatesFp32>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case kStatesCompanded: return K<0, kStatesCompanded>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case kStatesLinear: return K<0, kStatesLinear>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-    case kStatesFp32: return K<0, kStatesFp32>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 24 * 4 + kStatesCompanded: return K<24, kStatesCompanded, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 24 * 4 + kStatesLinear: return K<24, kStatesLinear, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 24 * 4 + kStatesFp32: return K<24, kStatesFp32, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 32 * 4 + kStatesCompanded: return K<32, kStatesCompanded, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 32 * 4 + kStatesLinear: return K<32, kStatesLinear, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case 32 * 4 + kStatesFp32: return K<32, kStatesFp32, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case kStatesCompanded: return K<0, kStatesCompanded, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case kStatesLinear: return K<0, kStatesLinear, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+    case kStatesFp32: return K<0, kStatesFp32, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
     default: break;
     }
-    if constexpr (K<0, kStatesFp32>::kFp32Params) {
+    if constexpr (K<0, kStatesFp32, SCALED>::kFp32Params) {
         switch (master_bits * 4 + states) {
-        case kParamF32 * 4 + kStatesCompanded: return K<kParamF32, kStatesCompanded>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-        case kParamF32 * 4 + kStatesLinear: return K<kParamF32, kStatesLinear>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
-        case kParamF32 * 4 + kStatesFp32: return K<kParamF32, kStatesFp32>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+        case kParamF32 * 4 + kStatesCompanded: return K<kParamF32, kStatesCompanded, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+        case kParamF32 * 4 + kStatesLinear: return K<kParamF32, kStatesLinear, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
+        case kParamF32 * 4 + kStatesFp32: return K<kParamF32, kStatesFp32, SCALED>::run(tensors, chunk_start, n_tensors, total_chunks, sc, st);
         default: break;
         }
     }
@@ -1823,44 +1836,44 @@ hipError_t dispatch(int master_bits, int states, const DevTensor *tensors,
 }
 
 // List launches: the scalars are a device pointer into the staged table.
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 struct AdamWLaunch {
     static constexpr bool kFp32Params = true;
     static hipError_t run(const DevTensor *t, const int32_t *cs, int n, int32_t total,
                           const StepScalars *scalars, hipStream_t st)
     {
-        return step_variant<MB, ST>(t, cs, n, total, scalars, st);
+        return step_variant<MB, ST, SCALED>(t, cs, n, total, scalars, st);
     }
 };
 
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 struct SgdLaunch {
     static constexpr bool kFp32Params = false;
     static hipError_t run(const DevTensor *t, const int32_t *cs, int n, int32_t total,
                           const SgdScalars *scalars, hipStream_t st)
     {
-        return sgd_variant<MB, ST>(t, cs, n, total, scalars, st);
+        return sgd_variant<MB, ST, SCALED>(t, cs, n, total, scalars, st);
     }
 };
 
 // Single-tensor launches: t points to a host descriptor passed by value.
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 struct AdamWTensorLaunch {
     static constexpr bool kFp32Params = true;
     static hipError_t run(const DevTensor *t, const int32_t *, int, int32_t total,
                           const StepScalars &sc, hipStream_t st)
     {
-        return launch_units<MB, ST>(adamw_tensor_kernel<MB, ST>, total, st, *t, sc);
+        return launch_units<MB, ST>(adamw_tensor_kernel<MB, ST, SCALED>, total, st, *t, sc);
     }
 };
 
-template <int MB, int ST>
+template <int MB, int ST, bool SCALED>
 struct SgdTensorLaunch {
     static constexpr bool kFp32Params = false;
     static hipError_t run(const DevTensor *t, const int32_t *, int, int32_t total,
                           const SgdScalars &sc, hipStream_t st)
     {
-        return launch_units<MB, ST>(sgd_tensor_kernel<MB, ST>, total, st, *t, sc);
+        return launch_units<MB, ST>(sgd_tensor_kernel<MB, ST, SCALED>, total, st, *t, sc);
     }
 };
 
@@ -1899,20 +1912,22 @@ hipError_t scratch_address(void **ptr)
 
 hipError_t launch_adamw_step(const StepScalars *scalars, const DevTensor *tensors,
                              const int32_t *chunk_start, int n_tensors, int32_t total_chunks,
-                             int master_bits, int states, hipStream_t st)
+                             int master_bits, int states, bool scaled, hipStream_t st)
 {
     if (total_chunks <= 0) return hipSuccess;
-    return dispatch<AdamWLaunch>(master_bits, states, tensors, chunk_start, n_tensors,
-                                 total_chunks, scalars, st);
+    return (scaled ? dispatch<AdamWLaunch, true, const StepScalars *>
+                   : dispatch<AdamWLaunch, false, const StepScalars *>)(
+        master_bits, states, tensors, chunk_start, n_tensors, total_chunks, scalars, st);
 }
 
 hipError_t launch_sgd_step(const SgdScalars *scalars, const DevTensor *tensors,
                            const int32_t *chunk_start, int n_tensors, int32_t total_chunks,
-                           int master_bits, int states, hipStream_t st)
+                           int master_bits, int states, bool scaled, hipStream_t st)
 {
     if (total_chunks <= 0) return hipSuccess;
-    return dispatch<SgdLaunch>(master_bits, states, tensors, chunk_start, n_tensors,
-                               total_chunks, scalars, st);
+    return (scaled ? dispatch<SgdLaunch, true, const SgdScalars *>
+                   : dispatch<SgdLaunch, false, const SgdScalars *>)(
+        master_bits, states, tensors, chunk_start, n_tensors, total_chunks, scalars, st);
 }
 
 hipError_t launch_adamw_tensor(const DevTensor &d, const StepScalars &sc, int master_bits,
@@ -1920,8 +1935,9 @@ hipError_t launch_adamw_tensor(const DevTensor &d, const StepScalars &sc, int ma
 {
     const int64_t chunks = (d.numel + kChunkElems - 1) / kChunkElems;
     if (chunks <= 0) return hipSuccess;
-    return dispatch<AdamWTensorLaunch>(master_bits, states, &d, nullptr, 1,
-                                       static_cast<int32_t>(chunks), sc, st);
+    return (sc.grad_scale ? dispatch<AdamWTensorLaunch, true, StepScalars>
+                          : dispatch<AdamWTensorLaunch, false, StepScalars>)(
+        master_bits, states, &d, nullptr, 1, static_cast<int32_t>(chunks), sc, st);
 }
 
 hipError_t launch_sgd_tensor(const DevTensor &d, const SgdScalars &sc, int master_bits,
@@ -1929,8 +1945,9 @@ hipError_t launch_sgd_tensor(const DevTensor &d, const SgdScalars &sc, int maste
 {
     const int64_t chunks = (d.numel + kChunkElems - 1) / kChunkElems;
     if (chunks <= 0) return hipSuccess;
-    return dispatch<SgdTensorLaunch>(master_bits, states, &d, nullptr, 1,
-                                     static_cast<int32_t>(chunks), sc, st);
+    return (sc.grad_scale ? dispatch<SgdTensorLaunch, true, SgdScalars>
+                          : dispatch<SgdTensorLaunch, false, SgdScalars>)(
+        master_bits, states, &d, nullptr, 1, static_cast<int32_t>(chunks), sc, st);
 }
 
 }  // namespace flashopt

@@ -9,8 +9,10 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -36,7 +38,10 @@ EXPORTS = ("flashopt_quantize", "flashopt_dequantize", "flashopt_split",
            "flashopt_abi_version", "flashopt_adamw_step_noalloc", "flashopt_adamw_plan_bytes",
            "flashopt_adamw_plan", "flashopt_adamw_plan_set_step", "flashopt_adamw_plan_launch",
            "flashopt_sgd_plan_bytes", "flashopt_sgd_plan", "flashopt_sgd_plan_set_step",
-           "flashopt_sgd_plan_launch", "flashopt_blocked_state_bytes")
+           "flashopt_sgd_plan_launch", "flashopt_blocked_state_bytes",
+           "flashopt_grad_workspace_bytes", "flashopt_grad_norm", "flashopt_grad_clip",
+           "flashopt_grad_plan_bytes", "flashopt_grad_plan", "flashopt_grad_plan_norm",
+           "flashopt_grad_plan_clip")
 
 
 class FlashoptError(RuntimeError):
@@ -58,14 +63,14 @@ class flashopt_adamw_args(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
                 ("master_bits", ctypes.c_int), ("companded", ctypes.c_int),
                 ("fp32_states", ctypes.c_int), ("param_fp32", ctypes.c_int),
-                ("state_layout", ctypes.c_int)]
+                ("state_layout", ctypes.c_int), ("grad_scale", ctypes.c_void_p)]
 
 
 class flashopt_adamw_plan_info(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("total_chunks", ctypes.c_int32),
                 ("master_bits", ctypes.c_int32), ("companded", ctypes.c_int32),
                 ("fp32_states", ctypes.c_int32), ("param_fp32", ctypes.c_int32),
-                ("state_layout", ctypes.c_int32)]
+                ("state_layout", ctypes.c_int32), ("grad_scaled", ctypes.c_int32)]
 
 
 class flashopt_sgd_args(ctypes.Structure):
@@ -73,13 +78,25 @@ class flashopt_sgd_args(ctypes.Structure):
                 ("dampening", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("step", ctypes.c_int64), ("master_bits", ctypes.c_int),
                 ("companded", ctypes.c_int), ("fp32_states", ctypes.c_int),
-                ("nesterov", ctypes.c_int), ("state_layout", ctypes.c_int)]
+                ("nesterov", ctypes.c_int), ("state_layout", ctypes.c_int),
+                ("grad_scale", ctypes.c_void_p)]
 
 
 class flashopt_sgd_plan_info(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("total_chunks", ctypes.c_int32),
                 ("master_bits", ctypes.c_int32), ("companded", ctypes.c_int32),
-                ("fp32_states", ctypes.c_int32), ("state_layout", ctypes.c_int32)]
+                ("fp32_states", ctypes.c_int32), ("state_layout", ctypes.c_int32),
+                ("grad_scaled", ctypes.c_int32)]
+
+
+class flashopt_grad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("fp32", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class flashopt_grad_plan_info(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("total_chunks", ctypes.c_int32),
+                ("overlap", ctypes.c_int32)]
 
 
 _lib = None
@@ -131,6 +148,16 @@ def lib() -> ctypes.CDLL:
         L.flashopt_sgd_plan_launch.argtypes = [ctypes.POINTER(flashopt_sgd_plan_info), vp, vp]
         L.flashopt_blocked_state_bytes.argtypes = [i64, i, i]
         L.flashopt_blocked_state_bytes.restype = ctypes.c_size_t
+        grads, info, dbl = ctypes.POINTER(flashopt_grad), ctypes.POINTER(flashopt_grad_plan_info), ctypes.c_double
+        L.flashopt_grad_workspace_bytes.argtypes = [i]
+        L.flashopt_grad_workspace_bytes.restype = ctypes.c_size_t
+        L.flashopt_grad_norm.argtypes = [grads, i, dbl, vp, vp, ctypes.c_size_t, vp]
+        L.flashopt_grad_clip.argtypes = [grads, i, dbl, vp, vp, ctypes.c_size_t, vp]
+        L.flashopt_grad_plan_bytes.argtypes = [i]
+        L.flashopt_grad_plan_bytes.restype = ctypes.c_size_t
+        L.flashopt_grad_plan.argtypes = [grads, i, vp, ctypes.c_size_t, info, vp]
+        L.flashopt_grad_plan_norm.argtypes = [info, vp, dbl, vp, vp]
+        L.flashopt_grad_plan_clip.argtypes = [info, vp, dbl, vp, vp]
         L.flashopt_status_str.argtypes = [i]
         L.flashopt_status_str.restype = ctypes.c_char_p
         L.flashopt_abi_version.argtypes = []
@@ -139,7 +166,9 @@ def lib() -> ctypes.CDLL:
                      "flashopt_adamw_step_tensor", "flashopt_sgd_step_tensor",
                      "flashopt_adamw_step_noalloc", "flashopt_adamw_plan",
                      "flashopt_adamw_plan_set_step", "flashopt_adamw_plan_launch",
-                     "flashopt_sgd_plan", "flashopt_sgd_plan_set_step", "flashopt_sgd_plan_launch"):
+                     "flashopt_sgd_plan", "flashopt_sgd_plan_set_step", "flashopt_sgd_plan_launch",
+                     "flashopt_grad_norm", "flashopt_grad_clip", "flashopt_grad_plan",
+                     "flashopt_grad_plan_norm", "flashopt_grad_plan_clip"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -399,14 +428,26 @@ class TensorState:
 
 def make_args(step: int, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0,
               master_bits=24, companded=True, quantize_states=True,
-              param_fp32=False, state_layout="streams") -> flashopt_adamw_args:
+              param_fp32=False, state_layout="streams", grad_scale=None) -> flashopt_adamw_args:
     """master_bits 24 | 32 | None (no split); quantize_states False: fp32 m, v;
     param_fp32: fp32 parameters and gradients (needs master_bits None);
-    state_layout "streams" | "blocked"."""
+    state_layout "streams" | "blocked"; grad_scale: a device fp32 tensor whose
+    first element multiplies the gradients."""
     return flashopt_adamw_args(lr, betas[0], betas[1], eps, weight_decay, step,
                                0 if master_bits is None else master_bits, int(companded),
                                0 if quantize_states else 1, int(param_fp32),
-                               STATE_LAYOUTS[state_layout])
+                               STATE_LAYOUTS[state_layout], _scale_ptr(grad_scale))
+
+
+def _scale_ptr(grad_scale, device=None):
+    """Address of a grad_scale (None: none), after its checks."""
+    if grad_scale is None:
+        return None
+    if grad_scale.dtype != torch.float32 or not grad_scale.is_cuda or grad_scale.numel() < 1:
+        raise ValueError("grad_scale must be an fp32 device tensor")
+    if device is not None and grad_scale.device != device:
+        raise ValueError(f"grad_scale is on {grad_scale.device}, the parameters on {device}")
+    return grad_scale.data_ptr()
 
 
 def flashopt_adamw_workspace_bytes(n_tensors: int) -> int:
@@ -488,6 +529,154 @@ def flashopt_sgd_plan_launch(info: flashopt_sgd_plan_info, plan: torch.Tensor, s
            "flashopt_sgd_plan_launch")
 
 
+# --------------------------------------------- gradient norm and clipping
+
+def _stream_context(stream, device):
+    """Allocations and torch operations inside go to `stream` (None: the
+    current stream, nothing to do)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def grad_array(grads):
+    """(ctypes array of flashopt_grad, device) of a list of contiguous bf16
+    and fp32 device tensors (device None for an empty list)."""
+    words, device = array("q"), None
+    for g in grads:
+        wide = g.dtype == torch.float32
+        if not wide and g.dtype != torch.bfloat16:
+            raise ValueError(f"gradients must be bf16 or fp32, got {g.dtype}")
+        if not g.is_cuda:
+            raise ValueError("gradients must be device tensors")
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+        if device is None:
+            device = g.device
+        elif g.device != device:
+            raise ValueError(f"all gradients must be on one device, got {device} and {g.device}")
+        words.extend((g.data_ptr(), g.numel(), int(wide)))
+    n = len(words) // 3
+    return (flashopt_grad * n).from_buffer(words) if n else (flashopt_grad * 0)(), device
+
+
+def flashopt_grad_workspace_bytes(n_tensors: int) -> int:
+    return lib().flashopt_grad_workspace_bytes(n_tensors)
+
+
+# One zeroed workspace per device and stream: launches on one stream are
+# ordered, and each leaves its workspace ready for the next.  A captured
+# launch gets one of its own (replays may run next to anything else).
+_grad_workspaces = {}
+
+
+def _grad_workspace(n: int, device, stream) -> torch.Tensor:
+    need = max(16, flashopt_grad_workspace_bytes(n))
+    with _stream_context(stream, device):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(need, dtype=torch.uint8, device=device)
+        key = (device, torch.cuda.current_stream().cuda_stream)
+        ws = _grad_workspaces.get(key)
+        if ws is None or ws.numel() < need:
+            ws = _grad_workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+        return ws
+
+
+def _grad_out(out, device, stream) -> torch.Tensor:
+    if out is None:
+        with _stream_context(stream, device):
+            return torch.empty(2, dtype=torch.float32, device=device)
+    _buf(out, "out", device, (4,), 2, float32=True)
+    return out
+
+
+def _grad_call(name, grads, max_norm, out, workspace, stream):
+    arr, device = grads if isinstance(grads, tuple) else grad_array(grads)
+    if device is None:
+        device = out.device if out is not None else torch.device("cuda", torch.cuda.current_device())
+    dev = getattr(stream, "device", None)
+    if dev is not None and dev != device:
+        raise ValueError(f"stream is on {dev}, the gradients on {device}")
+    with torch.cuda.device(device):
+        out = _grad_out(out, device, stream)
+        ws = _grad_workspace(len(arr), device, stream) if workspace is None else workspace
+        if ws.device != device:
+            raise ValueError(f"workspace is on {ws.device}, the gradients on {device}")
+        _check(getattr(lib(), name)(arr, len(arr), max_norm, out.data_ptr(), _dev(ws, "workspace"),
+                                    ws.numel() * ws.element_size(), _stream(stream)), name)
+    return out
+
+
+def flashopt_grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None, stream=None):
+    """Global norm of a list of bf16 / fp32 gradients: a device fp32 tensor
+    [norm, scale], scale = min(1, max_norm / (norm + 1e-6)).  out[1:] is a
+    grad_scale for the steps.  A workspace passed in must have been zeroed
+    before its first use."""
+    return _grad_call("flashopt_grad_norm", grads, max_norm, out, workspace, stream)
+
+
+def flashopt_grad_clip(grads, max_norm: float, out=None, workspace=None, stream=None):
+    """flashopt_grad_norm, then every gradient multiplied by the scale in
+    place; returns [norm, scale]."""
+    return _grad_call("flashopt_grad_clip", grads, max_norm, out, workspace, stream)
+
+
+def flashopt_grad_plan_bytes(n_tensors: int) -> int:
+    return lib().flashopt_grad_plan_bytes(n_tensors)
+
+
+def flashopt_grad_plan(grads, plan: torch.Tensor, stream=None) -> flashopt_grad_plan_info:
+    """Stage the table of a grad_array (or of a list of tensors) into `plan`."""
+    arr = grads if isinstance(grads, ctypes.Array) else grad_array(grads)[0]
+    info = flashopt_grad_plan_info()
+    _check(lib().flashopt_grad_plan(arr, len(arr), _dev(plan, "plan"),
+                                    plan.numel() * plan.element_size(), ctypes.byref(info),
+                                    _stream(stream)), "flashopt_grad_plan")
+    return info
+
+
+def flashopt_grad_plan_norm(info, plan: torch.Tensor, max_norm: float, out: torch.Tensor, stream=None):
+    _check(lib().flashopt_grad_plan_norm(ctypes.byref(info), _dev(plan, "plan"), max_norm,
+                                         _buf(out, "out", plan.device, (4,), 2, float32=True),
+                                         _stream(stream)), "flashopt_grad_plan_norm")
+
+
+def flashopt_grad_plan_clip(info, plan: torch.Tensor, max_norm: float, out: torch.Tensor, stream=None):
+    _check(lib().flashopt_grad_plan_clip(ctypes.byref(info), _dev(plan, "plan"), max_norm,
+                                         _buf(out, "out", plan.device, (4,), 2, float32=True),
+                                         _stream(stream)), "flashopt_grad_plan_clip")
+
+
+class GradPlan:
+    """Norm and clipping of a fixed list of gradient buffers, of any length,
+    with the table staged once: norm() and clip() enqueue kernels only and can
+    be recorded into a graph.  The plan keeps references to the gradients;
+    launches of one plan must be ordered with each other."""
+
+    def __init__(self, grads, stream=None):
+        self.grads = list(grads)
+        arr, device = grad_array(self.grads)
+        self.device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(self.device), _stream_context(stream, self.device):
+            self.buffer = torch.empty(max(16, flashopt_grad_plan_bytes(len(arr))), dtype=torch.uint8,
+                                      device=self.device)
+            self.info = flashopt_grad_plan(arr, self.buffer, stream)
+
+    def norm(self, max_norm: float = float("inf"), out=None, stream=None) -> torch.Tensor:
+        with torch.cuda.device(self.device):
+            out = _grad_out(out, self.device, stream)
+            flashopt_grad_plan_norm(self.info, self.buffer, max_norm, out, stream)
+        return out
+
+    def clip(self, max_norm: float, out=None, stream=None) -> torch.Tensor:
+        with torch.cuda.device(self.device):
+            out = _grad_out(out, self.device, stream)
+            flashopt_grad_plan_clip(self.info, self.buffer, max_norm, out, stream)
+        return out
+
+
 class StepPlan:
     """The capture-safe list step of a FlashAdamW or FlashSGD over fixed
     gradient buffers (flashopt_adamw_plan / flashopt_sgd_plan): launch()
@@ -495,25 +684,27 @@ class StepPlan:
     graph, and set_step(t), called outside any capture before a launch or
     replay, writes the scalars of step t that it uses.  The plan keeps
     references to the gradient tensors (their addresses are in its table)
-    and does not change the optimizer's step counts."""
+    and to grad_scale, and does not change the optimizer's step counts."""
 
-    def __init__(self, opt, grads, step: int, stream=None):
+    def __init__(self, opt, grads, step: int, stream=None, grad_scale=None):
         grads = list(grads)
         if len(grads) != len(opt.states):
             raise ValueError(f"{len(grads)} gradients for {len(opt.states)} parameters")
         self.opt = opt
         self.grads = grads
+        self.grad_scale = grad_scale
+        _scale_ptr(grad_scale, opt.device)
         self._bytes, self._plan, self._set, self._launch = opt._plan_calls
         desc = descriptor_array(opt.states, grads)
         with torch.cuda.device(opt.device):
             self.buffer = torch.empty(max(16, self._bytes(len(desc))), dtype=torch.uint8,
                                       device=opt.device or "cuda")
-            self.info = self._plan(desc, opt._args(step), self.buffer, stream)
+            self.info = self._plan(desc, opt._args(step, grad_scale), self.buffer, stream)
         self.t = step
 
     def set_step(self, t: int, stream=None):
         with torch.cuda.device(self.opt.device):
-            self._set(self.info, self.opt._args(t), self.buffer, stream)
+            self._set(self.info, self.opt._args(t, self.grad_scale), self.buffer, stream)
         self.t = t
 
     def launch(self, stream=None):
@@ -550,11 +741,16 @@ class _Stepper:
             self._workspaces[key] = ws
         return ws
 
-    def step(self, grads, stream=None):
+    def step(self, grads, stream=None, grad_scale=None, max_norm=None):
         """One launch over every tensor; grads[i] is the bf16 gradient of
         tensor i.  The descriptor table is rebuilt (and the grads validated)
         whenever a grad's address, size, dtype, device or contiguity differs
-        from the previous step's; no reference to the grads is kept."""
+        from the previous step's; no reference to the grads is kept.
+
+        grad_scale: a device fp32 tensor whose first element multiplies every
+        gradient as it is loaded.  max_norm: the step is clipped by the global
+        norm of grads (flashopt_grad_norm first, its scale the grad_scale) and
+        [norm, scale] is returned."""
         grads = list(grads)
         if len(grads) != len(self.states):
             raise ValueError(f"{len(grads)} gradients for {len(self.states)} parameters")
@@ -563,19 +759,28 @@ class _Stepper:
             self._desc = descriptor_array(self.states, grads)
             self._key = key
         self._check_stream(stream)
+        _scale_ptr(grad_scale, self.device)
+        out = None
+        if max_norm is not None:
+            if grad_scale is not None:
+                raise ValueError("grad_scale and max_norm exclude each other")
+            out = flashopt_grad_norm(grads, max_norm, stream=stream)
+            grad_scale = out[1:]
         self.t += 1
         self.ts = [self.t] * len(self.states)
         with torch.cuda.device(self.device):    # the library launches on the current device
-            self._list_step(self._desc, self.t, stream)
+            self._list_step(self._desc, self.t, stream, grad_scale)
+        return out
 
-    def step_tensor(self, i: int, grad: torch.Tensor, stream=None):
+    def step_tensor(self, i: int, grad: torch.Tensor, stream=None, grad_scale=None):
         desc = self.states[i].descriptor(grad)
         self._check_stream(stream)
+        _scale_ptr(grad_scale, self.device)
         self.ts[i] += 1
         with torch.cuda.device(self.device):
-            self._tensor_step(desc, self.ts[i], stream)
+            self._tensor_step(desc, self.ts[i], stream, grad_scale)
 
-    def step_tensors(self, indices, grads, stream=None):
+    def step_tensors(self, indices, grads, stream=None, grad_scale=None):
         """Step a subset of the tensors (indices, each at most once) with one
         list launch per distinct step count: the same results as
         step_tensor() on each, in fewer launches."""
@@ -584,6 +789,7 @@ class _Stepper:
             raise ValueError("indices must be distinct and match the gradients")
         descs = [self.states[i].descriptor(g) for i, g in zip(indices, grads)]
         self._check_stream(stream)
+        _scale_ptr(grad_scale, self.device)
         by_t = {}
         for i, d in zip(indices, descs):
             self.ts[i] += 1
@@ -591,12 +797,12 @@ class _Stepper:
         with torch.cuda.device(self.device):
             for t, ds in by_t.items():
                 arr = (flashopt_tensor * len(ds))(*ds)
-                self._list_step(arr, t, stream)
+                self._list_step(arr, t, stream, grad_scale)
 
-    def plan(self, grads, step: int, stream=None) -> "StepPlan":
+    def plan(self, grads, step: int, stream=None, grad_scale=None) -> "StepPlan":
         """A capture-safe list step over these gradient buffers, with the
         scalars of `step` staged (StepPlan)."""
-        return StepPlan(self, grads, step, stream)
+        return StepPlan(self, grads, step, stream, grad_scale)
 
     def _check_stream(self, stream):
         dev = getattr(stream, "device", None)
@@ -703,29 +909,29 @@ class FlashAdamW(_Stepper):
         self._init_common()
         self._workspace_bytes = max(16, flashopt_adamw_workspace_bytes(len(self.states)))
 
-    def _list_step(self, desc, t, stream):
-        flashopt_adamw_step(desc, make_args(t, **self.hp), self.workspace(stream), stream)
+    def _list_step(self, desc, t, stream, grad_scale=None):
+        flashopt_adamw_step(desc, self._args(t, grad_scale), self.workspace(stream), stream)
 
-    def _args(self, t):
-        return make_args(t, **self.hp)
+    def _args(self, t, grad_scale=None):
+        return make_args(t, grad_scale=grad_scale, **self.hp)
 
     # (a tuple of plain functions: looked up on an instance, they stay unbound)
     _plan_calls = (flashopt_adamw_plan_bytes, flashopt_adamw_plan, flashopt_adamw_plan_set_step,
                    flashopt_adamw_plan_launch)
 
-    def _tensor_step(self, desc, t, stream):
-        flashopt_adamw_step_tensor(desc, make_args(t, **self.hp), stream)
+    def _tensor_step(self, desc, t, stream, grad_scale=None):
+        flashopt_adamw_step_tensor(desc, self._args(t, grad_scale), stream)
 
 
 # --------------------------------------------------------------- FlashSGD
 
 def make_sgd_args(step: int, lr=1e-2, momentum=0.9, dampening=0.0, weight_decay=0.0,
                   nesterov=False, master_bits=24, companded=True,
-                  quantize_states=True, state_layout="streams") -> flashopt_sgd_args:
+                  quantize_states=True, state_layout="streams", grad_scale=None) -> flashopt_sgd_args:
     return flashopt_sgd_args(lr, momentum, dampening, weight_decay, step,
                              0 if master_bits is None else master_bits, int(companded),
                              0 if quantize_states else 1, int(nesterov),
-                             STATE_LAYOUTS[state_layout])
+                             STATE_LAYOUTS[state_layout], _scale_ptr(grad_scale))
 
 
 def flashopt_sgd_workspace_bytes(n_tensors: int) -> int:
@@ -764,14 +970,14 @@ class FlashSGD(_Stepper):
         self._init_common()
         self._workspace_bytes = max(16, flashopt_sgd_workspace_bytes(len(self.states)))
 
-    def _list_step(self, desc, t, stream):
-        flashopt_sgd_step(desc, make_sgd_args(t, **self.hp), self.workspace(stream), stream)
+    def _list_step(self, desc, t, stream, grad_scale=None):
+        flashopt_sgd_step(desc, self._args(t, grad_scale), self.workspace(stream), stream)
 
-    def _args(self, t):
-        return make_sgd_args(t, **self.hp)
+    def _args(self, t, grad_scale=None):
+        return make_sgd_args(t, grad_scale=grad_scale, **self.hp)
 
     _plan_calls = (flashopt_sgd_plan_bytes, flashopt_sgd_plan, flashopt_sgd_plan_set_step,
                    flashopt_sgd_plan_launch)
 
-    def _tensor_step(self, desc, t, stream):
-        flashopt_sgd_step_tensor(desc, make_sgd_args(t, **self.hp), stream)
+    def _tensor_step(self, desc, t, stream, grad_scale=None):
+        flashopt_sgd_step_tensor(desc, self._args(t, grad_scale), stream)

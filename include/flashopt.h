@@ -51,7 +51,7 @@
 extern "C" {
 #endif
 
-#define FLASHOPT_ABI_VERSION 8
+#define FLASHOPT_ABI_VERSION 9
 
 typedef enum {
     FLASHOPT_OK = 0,
@@ -187,6 +187,12 @@ typedef struct {
                                  update is stored unchanged; needs
                                  master_bits 0 (rho unused)                   */
     int state_layout;         /* FLASHOPT_STATE_STREAMS | FLASHOPT_STATE_BLOCKED */
+    const float *grad_scale;  /* NULL, or a DEVICE fp32 that every gradient is
+                                 multiplied by as it is loaded (one fp32
+                                 rounding, not rounded back to bf16): a clipping
+                                 factor (flashopt_grad_norm's out + 1) or a loss
+                                 scale.  Read when the step runs; it must not
+                                 change until then                            */
 } flashopt_adamw_args;
 
 /* Bytes of a FLASHOPT_STATE_BLOCKED state buffer for a tensor of numel
@@ -209,6 +215,7 @@ size_t flashopt_adamw_workspace_bytes(const flashopt_tensor *tensors, int n_tens
  *                                                 the linear specs if !companded;
  *                                                 fp32 states are read as is)
  *   theta = reconstruct(param, rho)             (the bf16 param if master_bits 0)
+ *   g *= *grad_scale                            (with a grad_scale)
  *   theta *= 1 - lr*wd;  m1 = b1 m0 + (1-b1) g;  v1 = b2 v0 + ((1-b2) g) g
  *   mhat = m1 / (1 - b1^t);  vhat = v1 / (1 - b2^t)
  *   theta -= (lr mhat) / (sqrt(vhat) + eps)     (the page's order, "Standard
@@ -236,7 +243,8 @@ size_t flashopt_adamw_workspace_bytes(const flashopt_tensor *tensors, int n_tens
  * m_codes, m_scales, v_codes or v_scales,
  * step < 1, lr < 0, beta outside
  * [0, 1), eps < 0, non-finite weight_decay, more than 2^31 - 1 chunks of
- * 1024 elements in total), EALIGN, EWORKSPACE, EHIP. */
+ * 1024 elements in total), EALIGN (also a grad_scale that is not 4-byte
+ * aligned), EWORKSPACE, EHIP. */
 flashopt_status flashopt_adamw_step(const flashopt_tensor *tensors, int n_tensors,
                                     const flashopt_adamw_args *args,
                                     void *workspace, size_t workspace_bytes,
@@ -277,8 +285,9 @@ flashopt_status flashopt_adamw_step_noalloc(const flashopt_tensor *tensors, int 
  *   must stay where they are for as long as the plan is launched.
  * flashopt_adamw_plan_set_step(info, args, plan, stream): enqueues one
  *   128-byte host-to-device copy of the scalars of args (any step and
- *   hyper-parameters; master_bits, companded, fp32_states, param_fp32 and
- *   state_layout must equal the plan's, else EINVAL).
+ *   hyper-parameters; master_bits, companded, fp32_states, param_fp32,
+ *   state_layout and whether there is a grad_scale must equal the plan's,
+ *   else EINVAL; the address of grad_scale may change).
  * flashopt_adamw_plan_launch(info, plan, stream): enqueues the step kernel
  *   only.  It copies nothing, allocates nothing and does not synchronize, so
  *   it can be captured into a graph; a launch or graph replay steps with the
@@ -299,6 +308,7 @@ typedef struct {
     int32_t fp32_states;
     int32_t param_fp32;
     int32_t state_layout;
+    int32_t grad_scaled;      /* args.grad_scale was not NULL                 */
 } flashopt_adamw_plan_info;
 flashopt_status flashopt_adamw_plan(const flashopt_tensor *tensors, int n_tensors,
                                     const flashopt_adamw_args *args, void *plan,
@@ -334,6 +344,7 @@ typedef struct {
     int nesterov;             /* 0 | 1                                        */
     int state_layout;         /* FLASHOPT_STATE_STREAMS | FLASHOPT_STATE_BLOCKED
                                  (the blocked buffer without the v parts)     */
+    const float *grad_scale;  /* as in flashopt_adamw_args                    */
 } flashopt_sgd_args;
 
 /* Device workspace bytes that flashopt_sgd_step needs for this list. */
@@ -359,8 +370,8 @@ flashopt_status flashopt_sgd_step(const flashopt_tensor *tensors, int n_tensors,
  * flashopt_adamw_plan calls above: flashopt_sgd_plan stages the scalars of
  * args and the tables into `plan` (flashopt_sgd_plan_bytes(n) bytes) and
  * fills *info; flashopt_sgd_plan_set_step rewrites the scalars (any step and
- * hyper-parameters; master_bits, companded, fp32_states and state_layout
- * must equal the plan's); flashopt_sgd_plan_launch enqueues the kernel only
+ * hyper-parameters; master_bits, companded, fp32_states, state_layout and
+ * whether there is a grad_scale must equal the plan's); flashopt_sgd_plan_launch enqueues the kernel only
  * and can be captured into a graph.
  * Errors: as flashopt_sgd_step (EWORKSPACE for a NULL or short plan; EINVAL
  * also for a NULL info or a variant mismatch). */
@@ -372,6 +383,7 @@ typedef struct {
     int32_t companded;
     int32_t fp32_states;
     int32_t state_layout;
+    int32_t grad_scaled;
 } flashopt_sgd_plan_info;
 flashopt_status flashopt_sgd_plan(const flashopt_tensor *tensors, int n_tensors,
                                   const flashopt_sgd_args *args, void *plan, size_t plan_bytes,
@@ -397,6 +409,74 @@ flashopt_status flashopt_adamw_step_tensor(const flashopt_tensor *tensor,
                                            const flashopt_adamw_args *args, void *stream);
 flashopt_status flashopt_sgd_step_tensor(const flashopt_tensor *tensor,
                                          const flashopt_sgd_args *args, void *stream);
+
+/* One gradient of flashopt_grad_norm / flashopt_grad_clip. */
+typedef struct {
+    void *data;               /* [numel] bf16, or fp32; aligned to its element
+                                 (2 or 4 bytes)                               */
+    int64_t numel;            /* >= 0                                         */
+    int32_t fp32;             /* 0: bf16, 1: fp32                             */
+    int32_t reserved;         /* 0                                            */
+} flashopt_grad;
+
+/* Device workspace bytes of flashopt_grad_norm / flashopt_grad_clip.  The
+ * caller ZEROES the workspace once, before its first use; every call leaves
+ * it ready for the next.  Calls that share a workspace must be ordered (one
+ * stream); calls that may overlap, captured graphs among them, need one
+ * each.  Returns 0 for n_tensors <= 0. */
+size_t flashopt_grad_workspace_bytes(int n_tensors);
+
+/* The global norm of a list of gradients, bf16 and fp32 mixed, in one pass
+ * and one kernel launch:
+ *   out[0] = norm  = sqrt(sum over the list of g^2)
+ *   out[1] = scale = min(1, max_norm / (norm + 1e-6))
+ * Squares and sums are fp64, added in an order that depends only on the list;
+ * norm and scale are rounded to fp32 once.  A NaN gradient gives a NaN norm
+ * and scale, an infinite one norm inf and scale 0 (NaN for an infinite
+ * max_norm).  An empty list has norm 0.
+ *   max_norm  >= 0; infinity: the norm only, scale 1
+ *   out       DEVICE fp32[2], written; out + 1 is a grad_scale for the steps
+ * A list of at most 64 tensors travels in the kernel arguments, and the call
+ * can be captured into a graph.  A longer one is staged through a pinned
+ * buffer of the library (see flashopt_adamw_step) and must not be captured:
+ * use a plan.
+ * Errors: EINVAL (n_tensors < 0, NULL grads/out, numel < 0, NULL data with
+ * numel > 0, fp32 not 0 or 1, max_norm negative or NaN, more than 2^31 - 1
+ * chunks of 4096 elements), EALIGN (data not aligned to its element, out to
+ * 4, workspace to 16 bytes), EWORKSPACE, EHIP. */
+flashopt_status flashopt_grad_norm(const flashopt_grad *grads, int n_tensors, double max_norm,
+                                   float *out, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* flashopt_grad_norm, then every gradient multiplied by the scale in place
+ * (the fp32 product rounded to the gradient's type, bf16 to nearest even);
+ * two launches.  With a scale of 1 the gradients are not touched.  A step
+ * given out + 1 as its grad_scale does without this pass.
+ * Errors: as flashopt_grad_norm; EINVAL also when two gradients overlap. */
+flashopt_status flashopt_grad_clip(const flashopt_grad *grads, int n_tensors, double max_norm,
+                                   float *out, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* The capture-safe forms for lists of any length, with the contract of the
+ * flashopt_adamw_plan calls: flashopt_grad_plan stages the list's table into
+ * `plan` (16-byte aligned, flashopt_grad_plan_bytes(n) bytes, zeroed by this
+ * call's own copy) and fills *info; flashopt_grad_plan_norm and _clip only
+ * enqueue kernels, with max_norm in their arguments (a captured launch keeps
+ * it).  Launches that share a plan must be ordered.
+ * Errors: as above (EWORKSPACE: plan NULL or too small; EINVAL also for a
+ * NULL info, and from _clip for a list with overlapping gradients). */
+size_t flashopt_grad_plan_bytes(int n_tensors);
+typedef struct {
+    int32_t n_tensors;        /* tensors in the plan's table                  */
+    int32_t total_chunks;     /* their 4096-element chunks                    */
+    int32_t overlap;          /* some gradients overlap: norm only            */
+} flashopt_grad_plan_info;
+flashopt_status flashopt_grad_plan(const flashopt_grad *grads, int n_tensors, void *plan,
+                                   size_t plan_bytes, flashopt_grad_plan_info *info, void *stream);
+flashopt_status flashopt_grad_plan_norm(const flashopt_grad_plan_info *info, void *plan,
+                                        double max_norm, float *out, void *stream);
+flashopt_status flashopt_grad_plan_clip(const flashopt_grad_plan_info *info, void *plan,
+                                        double max_norm, float *out, void *stream);
 
 /* Static string naming a status code. */
 const char *flashopt_status_str(flashopt_status status);
