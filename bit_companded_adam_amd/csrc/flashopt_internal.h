@@ -137,8 +137,8 @@ hipError_t launch_sgd_tensor(const DevTensor &d, const SgdScalars &sc, int maste
 
 // ---- gradient norm and clipping (flashopt_grad.hip)
 
-// One gradient of a list; the chunk table counts kGradChunk elements (two or
-// four 16-byte loads of a 256-thread workgroup).
+// One gradient of a list; the chunk table counts kGradChunk elements (four or
+// eight 16-byte loads of each of a workgroup's 256 threads).
 struct GradDesc {
     void *data;
     int64_t numel;
@@ -146,9 +146,10 @@ struct GradDesc {
     int32_t pad;
 };
 static_assert(sizeof(GradDesc) == 24, "descriptor layout");
-constexpr int kGradChunk = 4096;
-// Workgroups of a launch at most: eight to a CU, which all run at once.
-constexpr int kGradPartials = 2048;
+constexpr int kGradChunk = 8192;
+// Workgroups of a norm at most: two of 1024 threads to a CU, which all run at
+// once.  Fewer and larger, because each ends in two atomics that take turns.
+constexpr int kGradPartials = 512;
 // Lists up to this length travel in the kernel arguments.
 constexpr int kGradArgTensors = 64;
 

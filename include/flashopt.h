@@ -442,7 +442,7 @@ size_t flashopt_grad_workspace_bytes(int n_tensors);
  * use a plan.
  * Errors: EINVAL (n_tensors < 0, NULL grads/out, numel < 0, NULL data with
  * numel > 0, fp32 not 0 or 1, max_norm negative or NaN, more than 2^31 - 1
- * chunks of 4096 elements), EALIGN (data not aligned to its element, out to
+ * chunks of 8192 elements), EALIGN (data not aligned to its element, out to
  * 4, workspace to 16 bytes), EWORKSPACE, EHIP. */
 flashopt_status flashopt_grad_norm(const flashopt_grad *grads, int n_tensors, double max_norm,
                                    float *out, void *workspace, size_t workspace_bytes,
@@ -468,7 +468,7 @@ flashopt_status flashopt_grad_clip(const flashopt_grad *grads, int n_tensors, do
 size_t flashopt_grad_plan_bytes(int n_tensors);
 typedef struct {
     int32_t n_tensors;        /* tensors in the plan's table                  */
-    int32_t total_chunks;     /* their 4096-element chunks                    */
+    int32_t total_chunks;     /* their 8192-element chunks                    */
     int32_t overlap;          /* some gradients overlap: norm only            */
 } flashopt_grad_plan_info;
 flashopt_status flashopt_grad_plan(const flashopt_grad *grads, int n_tensors, void *plan,
