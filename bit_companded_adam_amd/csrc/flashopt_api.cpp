@@ -611,6 +611,45 @@ flashopt_status grad_plan_call(const flashopt_grad_plan_info *info, void *plan, 
         info->total_chunks, max_norm, clip, sums, out, st));
 }
 
+// ---- MXFP4
+
+using flashopt::MxMatrix;
+
+// A matrix's size, element type and row stride (an output's rows may not
+// overlap), then its address.
+flashopt_status check_size(int64_t rows, int64_t cols)
+{
+    return rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX ? FLASHOPT_EINVAL : FLASHOPT_OK;
+}
+
+flashopt_status check_matrix(const MxMatrix &x, int fp32, bool written)
+{
+    if (check_size(x.rows, x.cols) != FLASHOPT_OK || (fp32 != 0 && fp32 != 1)) return FLASHOPT_EINVAL;
+    if (x.row_stride < (written ? x.cols : 0) || x.row_stride > (int64_t{1} << 40)) return FLASHOPT_EINVAL;
+    if (x.rows == 0 || x.cols == 0) return FLASHOPT_OK;
+    if (!x.data) return FLASHOPT_EINVAL;
+    return aligned(x.data, x.fp32 ? 4 : 2) ? FLASHOPT_OK : FLASHOPT_EALIGN;
+}
+
+// Codes and scales of a rows x cols matrix (a pair that is empty may be NULL).
+flashopt_status check_codes(const void *codes, const void *scales, int64_t rows, int64_t cols)
+{
+    if (check_size(rows, cols) != FLASHOPT_OK) return FLASHOPT_EINVAL;
+    if (rows == 0 || cols == 0) return FLASHOPT_OK;
+    if (!codes || !scales) return FLASHOPT_EINVAL;
+    return aligned(codes, 16) && aligned(scales, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
+}
+
+// Workgroups of a quantization: tiles of 128 rows by 256 columns, whose
+// work-items a dispatch counts in 32 bits.
+bool quantizable(int64_t rows, int64_t cols)
+{
+    return ((rows + 127) / 128) * ((cols + 255) / 256) < (int64_t{1} << 24);
+}
+
+// The part of a buffer of codes that scales follow in: 16-byte rounded.
+size_t rounded(size_t bytes) { return (bytes + 15) & ~static_cast<size_t>(15); }
+
 // Host image of the allocation-free step's scalar block and chunk table:
 // built under the mutex and copied (pageable hipMemcpyAsync, which has
 // consumed the buffer when it returns) into the device scratch array.
@@ -975,6 +1014,93 @@ flashopt_status flashopt_grad_plan_clip(const flashopt_grad_plan_info *info, voi
                                         float *out, void *stream)
 {
     return grad_plan_call(info, plan, max_norm, true, out, stream);
+}
+
+size_t flashopt_mx_code_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || check_size(rows, cols) != FLASHOPT_OK) return 0;
+    return static_cast<size_t>(rows) * static_cast<size_t>(flashopt::mx_padded(cols) / 2);
+}
+
+size_t flashopt_mx_scale_bytes(int64_t rows, int64_t cols)
+{
+    return flashopt_mx_code_bytes(rows, cols) / 16;
+}
+
+flashopt_status flashopt_mx_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols, int64_t row_stride,
+                                     void *codes, void *scales, void *codes_t, void *scales_t, void *stream)
+{
+    const MxMatrix in{const_cast<void *>(x), rows, cols, row_stride, x_fp32 != 0};
+    flashopt_status cs = check_matrix(in, x_fp32, false);
+    if (cs != FLASHOPT_OK || rows == 0 || cols == 0) return cs;
+    if ((!codes && !codes_t) || (!codes != !scales) || (!codes_t != !scales_t) || !quantizable(rows, cols))
+        return FLASHOPT_EINVAL;
+    if (codes && (cs = check_codes(codes, scales, rows, cols)) != FLASHOPT_OK) return cs;
+    if (codes_t && (cs = check_codes(codes_t, scales_t, cols, rows)) != FLASHOPT_OK) return cs;
+    return hip_status(flashopt::launch_mx_quantize(
+        in, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), static_cast<uint8_t *>(codes_t),
+        static_cast<uint8_t *>(scales_t), static_cast<hipStream_t>(stream)));
+}
+
+flashopt_status flashopt_mx_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                                       void *out, int out_fp32, int64_t row_stride, void *stream)
+{
+    const MxMatrix o{out, rows, cols, row_stride, out_fp32 != 0};
+    flashopt_status cs = check_matrix(o, out_fp32, true);
+    if (cs != FLASHOPT_OK || rows == 0 || cols == 0) return cs;
+    if ((cs = check_codes(codes, scales, rows, cols)) != FLASHOPT_OK) return cs;
+    return hip_status(flashopt::launch_mx_dequantize(static_cast<const uint8_t *>(codes),
+                                                     static_cast<const uint8_t *>(scales), o,
+                                                     static_cast<hipStream_t>(stream)));
+}
+
+flashopt_status flashopt_mx_product(const void *a_codes, const void *a_scales, const void *b_codes,
+                                    const void *b_scales, int64_t m, int64_t n, int64_t k, void *out,
+                                    int out_fp32, int64_t row_stride, void *stream)
+{
+    const MxMatrix o{out, m, n, row_stride, out_fp32 != 0};
+    flashopt_status cs = check_matrix(o, out_fp32, true);
+    if (cs != FLASHOPT_OK) return cs;
+    if ((cs = check_size(m, k)) != FLASHOPT_OK) return cs;
+    if (m == 0 || n == 0) return FLASHOPT_OK;
+    if ((cs = check_codes(a_codes, a_scales, m, k)) != FLASHOPT_OK) return cs;
+    if ((cs = check_codes(b_codes, b_scales, n, k)) != FLASHOPT_OK) return cs;
+    return hip_status(flashopt::launch_mx_product(
+        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales),
+        static_cast<const uint8_t *>(b_codes), static_cast<const uint8_t *>(b_scales), k, o,
+        static_cast<hipStream_t>(stream)));
+}
+
+size_t flashopt_mx_linear_workspace_bytes(int64_t m, int64_t k)
+{
+    return rounded(flashopt_mx_code_bytes(m, k)) + rounded(flashopt_mx_scale_bytes(m, k));
+}
+
+flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t k, int64_t x_stride,
+                                   const void *w_codes, const void *w_scales, int64_t n, void *out,
+                                   int out_fp32, int64_t out_stride, void *workspace, size_t ws_bytes,
+                                   void *stream)
+{
+    const MxMatrix in{const_cast<void *>(x), m, k, x_stride, x_fp32 != 0};
+    const MxMatrix o{out, m, n, out_stride, out_fp32 != 0};
+    flashopt_status cs = check_matrix(in, x_fp32, false);
+    if (cs != FLASHOPT_OK) return cs;
+    if ((cs = check_matrix(o, out_fp32, true)) != FLASHOPT_OK) return cs;
+    if (m == 0 || n == 0) return FLASHOPT_OK;
+    if (!quantizable(m, k)) return FLASHOPT_EINVAL;
+    if ((cs = check_codes(w_codes, w_scales, n, k)) != FLASHOPT_OK) return cs;
+    const size_t need = flashopt_mx_linear_workspace_bytes(m, k);
+    if (need > 0 && (!workspace || ws_bytes < need)) return FLASHOPT_EWORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return FLASHOPT_EALIGN;
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + rounded(flashopt_mx_code_bytes(m, k));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (k > 0) {
+        const hipError_t e = flashopt::launch_mx_quantize(in, codes, scales, nullptr, nullptr, st);
+        if (e != hipSuccess) return hip_status(e);
+    }
+    return hip_status(flashopt::launch_mx_product(codes, scales, static_cast<const uint8_t *>(w_codes),
+                                                  static_cast<const uint8_t *>(w_scales), k, o, st));
 }
 
 }  // extern "C"

@@ -169,4 +169,25 @@ hipError_t launch_grad_table(const GradDesc *desc, const int32_t *start, int n, 
                              double max_norm, bool clip, GradSums *sums, float *out, hipStream_t st);
 hipError_t launch_grad_empty(double max_norm, float *out, hipStream_t st);
 
+// ---- MXFP4 (flashopt_mx.hip)
+
+// Elements of a padded row.
+__host__ __device__ inline int64_t mx_padded(int64_t cols) { return (cols + 127) / 128 * 128; }
+
+// A plain row-major matrix, its rows row_stride elements apart.
+struct MxMatrix {
+    void *data;
+    int64_t rows, cols, row_stride;
+    bool fp32;         // or bf16
+};
+
+hipError_t launch_mx_quantize(const MxMatrix &x, uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
+                              uint8_t *scales_t, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, const MxMatrix &out,
+                                hipStream_t stream);
+// out = A B^T with A of out.rows and B of out.cols rows.
+hipError_t launch_mx_product(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
+                             const uint8_t *b_scales, int64_t inner, const MxMatrix &out,
+                             hipStream_t stream);
+
 }  // namespace flashopt

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from array import array
 
@@ -41,7 +42,9 @@ EXPORTS = ("flashopt_quantize", "flashopt_dequantize", "flashopt_split",
            "flashopt_sgd_plan_launch", "flashopt_blocked_state_bytes",
            "flashopt_grad_workspace_bytes", "flashopt_grad_norm", "flashopt_grad_clip",
            "flashopt_grad_plan_bytes", "flashopt_grad_plan", "flashopt_grad_plan_norm",
-           "flashopt_grad_plan_clip")
+           "flashopt_grad_plan_clip", "flashopt_mx_code_bytes", "flashopt_mx_scale_bytes",
+           "flashopt_mx_quantize", "flashopt_mx_dequantize", "flashopt_mx_product",
+           "flashopt_mx_linear_workspace_bytes", "flashopt_mx_linear")
 
 
 class FlashoptError(RuntimeError):
@@ -158,6 +161,14 @@ def lib() -> ctypes.CDLL:
         L.flashopt_grad_plan.argtypes = [grads, i, vp, ctypes.c_size_t, info, vp]
         L.flashopt_grad_plan_norm.argtypes = [info, vp, dbl, vp, vp]
         L.flashopt_grad_plan_clip.argtypes = [info, vp, dbl, vp, vp]
+        for name, args in (("flashopt_mx_code_bytes", [i64, i64]), ("flashopt_mx_scale_bytes", [i64, i64]),
+                           ("flashopt_mx_linear_workspace_bytes", [i64, i64])):
+            getattr(L, name).argtypes, getattr(L, name).restype = args, ctypes.c_size_t
+        L.flashopt_mx_quantize.argtypes = [vp, i, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.flashopt_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i, i64, vp]
+        L.flashopt_mx_product.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i, i64, vp]
+        L.flashopt_mx_linear.argtypes = [vp, i, i64, i64, i64, vp, vp, i64, vp, i, i64, vp,
+                                         ctypes.c_size_t, vp]
         L.flashopt_status_str.argtypes = [i]
         L.flashopt_status_str.restype = ctypes.c_char_p
         L.flashopt_abi_version.argtypes = []
@@ -168,7 +179,8 @@ def lib() -> ctypes.CDLL:
                      "flashopt_adamw_plan_set_step", "flashopt_adamw_plan_launch",
                      "flashopt_sgd_plan", "flashopt_sgd_plan_set_step", "flashopt_sgd_plan_launch",
                      "flashopt_grad_norm", "flashopt_grad_clip", "flashopt_grad_plan",
-                     "flashopt_grad_plan_norm", "flashopt_grad_plan_clip"):
+                     "flashopt_grad_plan_norm", "flashopt_grad_plan_clip", "flashopt_mx_quantize",
+                     "flashopt_mx_dequantize", "flashopt_mx_product", "flashopt_mx_linear"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -981,3 +993,233 @@ class FlashSGD(_Stepper):
 
     def _tensor_step(self, desc, t, stream, grad_scale=None):
         flashopt_sgd_step_tensor(desc, self._args(t, grad_scale), stream)
+
+
+# --------------------------------------------------------------- MXFP4
+
+MX_BLOCK = 128          # rows of codes are padded to whole blocks of this many elements
+
+
+def flashopt_mx_code_bytes(rows: int, cols: int) -> int:
+    return lib().flashopt_mx_code_bytes(rows, cols)
+
+
+def flashopt_mx_scale_bytes(rows: int, cols: int) -> int:
+    return lib().flashopt_mx_scale_bytes(rows, cols)
+
+
+class MXTensor:
+    """A rows x cols matrix in MXFP4: uint8 tensors of packed codes (two to a
+    byte, rows padded to 128 elements) and of E8M0 scales (one for 32)."""
+
+    __slots__ = ("codes", "scales", "rows", "cols")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        blocks = rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
+        for t, name, each in ((codes, "codes", 64), (scales, "scales", 4)):
+            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 device tensor")
+            if t.numel() < blocks * each:
+                raise ValueError(f"{name} holds {t.numel()} bytes, {blocks * each} needed")
+        if codes.device != scales.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "MXTensor":
+        blocks = (cols + MX_BLOCK - 1) // MX_BLOCK
+        return MXTensor(torch.empty((rows, 64 * blocks), dtype=torch.uint8, device=device),
+                        torch.empty((rows, 4 * blocks), dtype=torch.uint8, device=device), rows, cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def __repr__(self):
+        return f"MXTensor({self.rows} x {self.cols}, {self.device})"
+
+
+def _matrix(x: torch.Tensor, name: str):
+    """(address, fp32 flag, rows, cols, row stride) of a bf16 or fp32 device
+    matrix whose rows are contiguous."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {x.dim()} dimensions")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if x.dtype != torch.bfloat16 and x.dtype != torch.float32:
+        raise ValueError(f"{name} must be bf16 or fp32, got {x.dtype}")
+    rows, cols = x.shape
+    stride, inner = x.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return x.data_ptr(), int(x.dtype == torch.float32), rows, cols, stride if rows > 1 else cols
+
+
+def _same_device(device, *named):
+    for t, name in named:
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the input on {device}")
+
+
+def _out_matrix(out, rows, cols, dtype, device):
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out must be {rows} x {cols}, got {tuple(out.shape)}")
+    if rows > 1 and out.stride(0) < cols:
+        raise ValueError("out's rows overlap")
+    _same_device(device, (out, "out"))
+    return out
+
+
+def _mx_target(q, rows, cols, device):
+    if q is None:
+        return MXTensor.empty(rows, cols, device)
+    if (q.rows, q.cols) != (rows, cols):
+        raise ValueError(f"out is {q.rows} x {q.cols}, {rows} x {cols} needed")
+    _same_device(device, (q.codes, "out"))
+    return q
+
+
+def flashopt_mx_quantize(x: torch.Tensor, layout: str = "rows", out=None, stream=None):
+    """MXFP4 of a bf16 or fp32 matrix.  layout "rows": x with groups along its
+    rows; "cols": x transposed, groups along x's columns; "both": the pair of
+    them from one read.  out: an MXTensor (a pair for "both") to write to."""
+    ptr, wide, rows, cols, stride = _matrix(x, "x")
+    if layout not in ("rows", "cols", "both"):
+        raise ValueError("layout must be 'rows', 'cols' or 'both'")
+    dev = x.device
+    first, second = out if layout == "both" and out is not None else (out, out)
+    with torch.cuda.device(dev), _stream_context(stream, dev):
+        q = _mx_target(first, rows, cols, dev) if layout != "cols" else None
+        t = _mx_target(second, cols, rows, dev) if layout != "rows" else None
+        _check(lib().flashopt_mx_quantize(
+            ptr, wide, rows, cols, stride, *((q.codes.data_ptr(), q.scales.data_ptr()) if q else (None, None)),
+            *((t.codes.data_ptr(), t.scales.data_ptr()) if t else (None, None)), _stream(stream)),
+            "flashopt_mx_quantize")
+    return (q, t) if layout == "both" else (q or t)
+
+
+def flashopt_mx_dequantize(q: MXTensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """The bf16 or fp32 values of an MXTensor."""
+    with torch.cuda.device(q.device), _stream_context(stream, q.device):
+        out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
+        ptr, wide, rows, cols, stride = _matrix(out, "out")
+        _check(lib().flashopt_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, ptr, wide,
+                                            stride, _stream(stream)), "flashopt_mx_dequantize")
+    return out
+
+
+def flashopt_mx_product(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """a b^T of two MXTensors with the same number of columns, in bf16 or fp32."""
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+    dev = a.device
+    _same_device(dev, (b, "b"))
+    with torch.cuda.device(dev), _stream_context(stream, dev):
+        out = _out_matrix(out, a.rows, b.rows, dtype, dev)
+        ptr, wide, m, n, stride = _matrix(out, "out")
+        _check(lib().flashopt_mx_product(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+                                         b.scales.data_ptr(), m, n, a.cols, ptr, wide, stride,
+                                         _stream(stream)), "flashopt_mx_product")
+    return out
+
+
+def flashopt_mx_linear_workspace_bytes(m: int, k: int) -> int:
+    return lib().flashopt_mx_linear_workspace_bytes(m, k)
+
+
+def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, workspace=None, stream=None):
+    """x w^T of a bf16 or fp32 matrix, quantized on the way, and MXFP4 weights
+    (no gradients: mx_linear has them); in x's dtype unless given."""
+    ptr, wide, m, k, stride = _matrix(x, "x")
+    if k != w.cols:
+        raise ValueError(f"x has {k} columns, w {w.cols}")
+    dev = x.device
+    _same_device(dev, (w, "w"))
+    with torch.cuda.device(dev), _stream_context(stream, dev):
+        out = _out_matrix(out, m, w.rows, dtype or x.dtype, dev)
+        optr, owide, _, n, ostride = _matrix(out, "out")
+        if workspace is None:
+            workspace = torch.empty(68 * m * ((k + MX_BLOCK - 1) // MX_BLOCK) + 16, dtype=torch.uint8,
+                                    device=dev)
+        _same_device(dev, (workspace, "workspace"))
+        _check(lib().flashopt_mx_linear(ptr, wide, m, k, stride, w.codes.data_ptr(), w.scales.data_ptr(), n,
+                                        optr, owide, ostride, _dev(workspace, "workspace"),
+                                        workspace.numel() * workspace.element_size(), _stream(stream)),
+               "flashopt_mx_linear")
+    return out
+
+
+class MXWeight:
+    """A weight parameter (bf16 or fp32, [out, in]) with its MXFP4 copies:
+    `rows` for the forward product, `cols` (transposed) for the input's
+    gradient.  refresh() requantizes into the same buffers, after each step of
+    the optimizer."""
+
+    def __init__(self, param: torch.Tensor):
+        self.param = param
+        self.version = 0
+        self.rows, self.cols = flashopt_mx_quantize(param.detach(), "both")
+
+    def refresh(self, stream=None):
+        self.version += 1
+        flashopt_mx_quantize(self.param.detach(), "both", (self.rows, self.cols), stream)
+
+
+def _flat(x: torch.Tensor) -> torch.Tensor:
+    x = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+
+
+class _MXLinear(torch.autograd.Function):
+    """y = Q(x) Q(w)^T with straight-through gradients: dx = Q(dy) Q'(w) and
+    dw = Q'(dy)^T Q'(x), Q along rows and Q' along columns (the axis each
+    product sums over).  The activation is kept for the backward pass in
+    4 bits."""
+
+    @staticmethod
+    def forward(ctx, x, w, weight):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        if weight is None:
+            q = flashopt_mx_quantize(w, "both" if need_x else "rows")
+            w_rows, w_cols = q if need_x else (q, None)
+        else:
+            w_rows, w_cols = weight.rows, weight.cols
+        flat = _flat(x)
+        q = flashopt_mx_quantize(flat, "both" if need_w else "rows")
+        x_rows, x_cols = q if need_w else (q, None)
+        ctx.weight, ctx.version = weight, None if weight is None else weight.version
+        ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
+        ctx.kept = [None if t is None else (t.rows, t.cols) for t in (x_cols, w_cols if need_x else None)]
+        ctx.save_for_backward(*[part for t, k in zip((x_cols, w_cols), ctx.kept) if k
+                                for part in (t.codes, t.scales)])
+        y = flashopt_mx_product(x_rows, w_rows, x.dtype)
+        return y.view(*x.shape[:-1], w.shape[0])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        if ctx.weight is not None and ctx.weight.version != ctx.version:
+            raise RuntimeError("the MXWeight was refreshed between the forward and the backward pass")
+        saved = list(ctx.saved_tensors)
+        x_cols, w_cols = [None if k is None else MXTensor(saved.pop(0), saved.pop(0), *k) for k in ctx.kept]
+        need_x, need_w = ctx.needs_input_grad[:2]
+        flat = _flat(dy)
+        layout = "both" if need_x and need_w else "rows" if need_x else "cols"
+        q = flashopt_mx_quantize(flat, layout)
+        dy_rows, dy_cols = q if layout == "both" else (q, q)
+        dx = flashopt_mx_product(dy_rows, w_cols, ctx.x_dtype).view(ctx.x_shape) if need_x else None
+        dw = flashopt_mx_product(dy_cols, x_cols, ctx.w_dtype) if need_w else None
+        return dx, dw, None
+
+
+def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
+    """A linear layer in MXFP4 with gradients: x [..., in] and a weight
+    parameter [out, in] (quantized in the call) or an MXWeight (quantized when
+    it was last refreshed; the gradient goes to its param).  Work goes to the
+    current stream."""
+    w, held = (weight.param, weight) if isinstance(weight, MXWeight) else (weight, None)
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")
+    return _MXLinear.apply(x, w, held)

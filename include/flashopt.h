@@ -478,6 +478,67 @@ flashopt_status flashopt_grad_plan_norm(const flashopt_grad_plan_info *info, voi
 flashopt_status flashopt_grad_plan_clip(const flashopt_grad_plan_info *info, void *plan,
                                         double max_norm, float *out, void *stream);
 
+/* MXFP4: 4-bit E2M1 codes (0 .5 1 1.5 2 3 4 6 and their negatives) with one
+ * E8M0 scale byte, 2^(byte - 127), for each 32 elements along a row: weights,
+ * activations and output gradients for matrix products in 4 bits.  Storage of
+ * an R x C matrix, its rows padded to Cp = 128 ceil(C / 128) elements:
+ *   codes   R rows of Cp / 2 bytes, the even column in the low nibble
+ *   scales  R rows of Cp / 32 bytes
+ * Padding is code 0 and scale byte 0.  codes 16-byte aligned, scales 4-byte.
+ * Rows and columns: 0 to 2^31 - 1 (memory ends earlier).
+ *
+ * Bytes of an R x C matrix's codes and of its scales (0 for an empty one): */
+size_t flashopt_mx_code_bytes(int64_t rows, int64_t cols);
+size_t flashopt_mx_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantization of a row-major bf16 or fp32 matrix, rows row_stride elements
+ * apart.  Per group of 32: e = floor(log2 max|x|) - 2, at least -127; byte =
+ * e + 127 (0 for a group of zeros); codes = x / 2^e rounded half to even,
+ * saturated at 6.  A group with an infinity or NaN has byte 255, which stands
+ * for NaN, and codes 0.
+ *   codes, scales      of x, groups along its rows; or both NULL
+ *   codes_t, scales_t  of x transposed (cols x rows), groups along x's
+ *                      columns; or both NULL.  Both pairs come from one read
+ *   x                  aligned to its element; row_stride >= 0
+ * Errors: EINVAL (negative or too large sizes, x_fp32 not 0 or 1, NULL x, no
+ * or half an output pair, 2^24 tiles of 128 x 256 or more), EALIGN, EHIP.  An
+ * empty matrix is a no-op. */
+flashopt_status flashopt_mx_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols,
+                                     int64_t row_stride, void *codes, void *scales,
+                                     void *codes_t, void *scales_t, void *stream);
+
+/* The values codes and scales stand for, to bf16 or fp32 (both hold them
+ * exactly unless a scale above 2^125 overflows).  out: aligned to its
+ * element, row_stride >= cols.  Errors: as above. */
+flashopt_status flashopt_mx_dequantize(const void *codes, const void *scales, int64_t rows,
+                                       int64_t cols, void *out, int out_fp32, int64_t row_stride,
+                                       void *stream);
+
+/* out[i, j] = sum over k of a[i, k] b[j, k]: the product of an m x k and an
+ * n x k MXFP4 matrix, accumulated in fp32 by the matrix instructions and
+ * rounded once to out's type (bf16 to nearest even).  One launch.  A NaN scale
+ * makes its row's (or column's) outputs NaN.  k == 0 writes zeros.
+ * A linear layer y = x w^T of x [m, k] and w [n, k] is three of these:
+ *   y  = product(x, w)          groups along k
+ *   dx = product(dy, w_t)       w_t: w's transposed codes, groups along n
+ *   dw = product(dy_t, x_t)     groups along m
+ * Errors: EINVAL (sizes, out_fp32, row_stride < n, NULL), EALIGN, EHIP. */
+flashopt_status flashopt_mx_product(const void *a_codes, const void *a_scales,
+                                    const void *b_codes, const void *b_scales, int64_t m,
+                                    int64_t n, int64_t k, void *out, int out_fp32,
+                                    int64_t row_stride, void *stream);
+
+/* y = quantize(x) w^T for serving: x [m, k] bf16 or fp32, w [n, k] MXFP4 laid
+ * out once.  The result is that of flashopt_mx_quantize and
+ * flashopt_mx_product.
+ *   workspace  DEVICE, 16-byte aligned, holds x's codes until the call has run
+ * Errors: as those calls; EWORKSPACE. */
+size_t flashopt_mx_linear_workspace_bytes(int64_t m, int64_t k);
+flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t k,
+                                   int64_t x_stride, const void *w_codes, const void *w_scales,
+                                   int64_t n, void *out, int out_fp32, int64_t out_stride,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static string naming a status code. */
 const char *flashopt_status_str(flashopt_status status);
 
