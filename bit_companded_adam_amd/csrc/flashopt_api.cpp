@@ -640,6 +640,10 @@ flashopt_status check_codes(const void *codes, const void *scales, int64_t rows,
     return aligned(codes, 16) && aligned(scales, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
 }
 
+// Most elements that a product sums over: its kernels address 256 rows of
+// codes with 32-bit offsets.
+constexpr int64_t kMaxInner = int64_t{1} << 25;
+
 // Workgroups of a quantization: tiles of 128 rows by 256 columns, whose
 // work-items a dispatch counts in 32 bits.
 bool quantizable(int64_t rows, int64_t cols)
@@ -1062,6 +1066,7 @@ flashopt_status flashopt_mx_product(const void *a_codes, const void *a_scales, c
     flashopt_status cs = check_matrix(o, out_fp32, true);
     if (cs != FLASHOPT_OK) return cs;
     if ((cs = check_size(m, k)) != FLASHOPT_OK) return cs;
+    if (k > kMaxInner) return FLASHOPT_EINVAL;
     if (m == 0 || n == 0) return FLASHOPT_OK;
     if ((cs = check_codes(a_codes, a_scales, m, k)) != FLASHOPT_OK) return cs;
     if ((cs = check_codes(b_codes, b_scales, n, k)) != FLASHOPT_OK) return cs;
@@ -1086,6 +1091,7 @@ flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t
     flashopt_status cs = check_matrix(in, x_fp32, false);
     if (cs != FLASHOPT_OK) return cs;
     if ((cs = check_matrix(o, out_fp32, true)) != FLASHOPT_OK) return cs;
+    if (k > kMaxInner) return FLASHOPT_EINVAL;
     if (m == 0 || n == 0) return FLASHOPT_OK;
     if (!quantizable(m, k)) return FLASHOPT_EINVAL;
     if ((cs = check_codes(w_codes, w_scales, n, k)) != FLASHOPT_OK) return cs;

@@ -28,6 +28,7 @@ namespace {
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_packed __attribute__((aligned(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -35,45 +36,77 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = kBlockThreads;
 
+// Number b of nb workgroups renumbered so that each of the 8 XCDs (workgroup b
+// runs on XCD b % 8) takes one contiguous eighth of them.
+__device__ __forceinline__ uint32_t xcd_contiguous(uint32_t b, uint32_t nb)
+{
+    const uint32_t x = b % 8u, per = (nb + 7u) / 8u, full = nb % 8u;
+    return x * per + b / 8u - (full != 0u && x > full ? x - full : 0u);
+}
+
 __device__ __forceinline__ uint32_t umax32(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// fp32 -> bf16, round to nearest even (no NaN keeps its payload's low half:
-// the quiet bit is set).
-__device__ __forceinline__ uint32_t bf16_rne(float x)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// fp32 -> bf16, round to nearest even (v_cvt_pk_bf16_f32): one value, or two
+// to a word.
+__device__ __forceinline__ uint16_t bf16_rne(float x)
 {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
 // -------------------------------------------------------------- quantize
 
-// The scale byte of a group from its largest biased exponent E (255: the
-// group holds an infinity or NaN, and so does its scale), and 2^(127 - byte),
-// the exact reciprocal of the scale (0 for byte 255).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t e)
+// Group maxima are kept as bit patterns without their sign, whose order is
+// that of the magnitudes, infinities and NaN on top.  The scale 2^e as an fp32
+// pattern is the maximum's exponent field less two, not below zero: the
+// conversion instructions take their scale from the exponent field alone, so
+// field 0 is 2^-127.
+constexpr uint32_t kExponent = 0x7F800000u;
+__device__ __forceinline__ uint32_t scale_bits(uint32_t top)
 {
-    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-__device__ __forceinline__ float scale_recip(uint32_t byte)
-{
-    return __uint_as_float((byte == 255u ? 0u : 254u - byte) << 23);
+    return __builtin_elementwise_sub_sat(top & kExponent, 2u << 23);
 }
 
-// Two E2M1 codes in byte SEL of acc (v_cvt_scalef32_pk_fp4_f32: half to even,
-// saturating at 6).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+
+// Maximum over aligned groups of eight lanes.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x)
+{
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), CTRL,
+                                                             0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t max8(uint32_t x)
+{
+    x = umax32(x, dpp<0xB1>(x));       // lane ^ 1
+    x = umax32(x, dpp<0x4E>(x));       // lane ^ 2
+    return umax32(x, dpp<0x141>(x));   // the other four of the eight
+}
+
+// Two E2M1 codes in byte SEL of acc (half to even, saturating at 6), from
+// fp32 values or from a word of two bf16 ones.
 template <int SEL>
-__device__ __forceinline__ uint32_t codes2(uint32_t acc, float a, float b)
+__device__ __forceinline__ uint32_t codes2(uint32_t acc, uint32_t a, uint32_t b, uint32_t scale)
 {
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(acc, a, b, 1.0f, SEL);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(acc, __uint_as_float(a), __uint_as_float(b),
+                                                    __uint_as_float(scale), SEL);
 }
-
-__device__ __forceinline__ uint32_t codes8(const float (&y)[8])
+template <int SEL>
+__device__ __forceinline__ uint32_t codes2(uint32_t acc, uint32_t ab, uint32_t scale)
 {
-    uint32_t w = codes2<0>(0u, y[0], y[1]);
-    w = codes2<1>(w, y[2], y[3]);
-    w = codes2<2>(w, y[4], y[5]);
-    return codes2<3>(w, y[6], y[7]);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(acc, __builtin_bit_cast(bf16x2, ab),
+                                                     __uint_as_float(scale), SEL);
 }
 
 // A wavefront takes 32 rows by 256 columns, four columns to a lane: every
@@ -82,109 +115,197 @@ __device__ __forceinline__ uint32_t codes8(const float (&y)[8])
 constexpr int kLaneCols = 4;
 constexpr int kTileCols = 64 * kLaneCols;
 constexpr int kWaveRows = 32;
-constexpr int kTileRows = kWaveRows * (kThreads / kWaveLanes);
+constexpr int kQuantWaves = kThreads / kWaveLanes;
+constexpr int kTileRows = kWaveRows * kQuantWaves;
 
-// Four elements of a row as fp32 bit patterns; columns past the end are 0.
+// A lane's four values of one row, in the words they came in.
+template <bool F32>
+struct Four {
+    uint32_t w[F32 ? 4 : 2];
+};
+
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load4(const uint8_t *row, int64_t c, int64_t cols, uint32_t (&w)[4])
+__device__ __forceinline__ Four<F32> load4(const uint8_t *row, int64_t c, int64_t cols)
 {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = 0u;
+    Four<F32> f{};
     if constexpr (VEC) {
         if (c + 4 <= cols) {
             if constexpr (F32) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(row + c * 4);
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + c * 4));
+                f.w[0] = v.x; f.w[1] = v.y; f.w[2] = v.z; f.w[3] = v.w;
             } else {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(row + c * 2);
-                w[0] = v.x << 16; w[1] = v.x & 0xFFFF0000u;
-                w[2] = v.y << 16; w[3] = v.y & 0xFFFF0000u;
+                const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + c * 2));
+                f.w[0] = v.x; f.w[1] = v.y;
             }
-            return;
+            return f;
         }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (c + j >= cols) continue;
-        if constexpr (F32) w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
-        else w[j] = static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c + j]) << 16;
+        if constexpr (F32) f.w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
+        else f.w[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c + j]) << (16 * (j & 1));
+    }
+    return f;
+}
+
+// Magnitude patterns: word by word, and the largest of the four as fp32 bits
+// (for bf16 the low half holds other bits, which no use of it sees).
+template <bool F32>
+__device__ __forceinline__ Four<F32> magnitudes(const Four<F32> &f)
+{
+    Four<F32> m;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) m.w[i] = f.w[i] & (F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+    return m;
+}
+template <bool F32>
+__device__ __forceinline__ void raise(Four<F32> &a, const Four<F32> &b)
+{
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) a.w[i] = F32 ? umax32(a.w[i], b.w[i]) : max_u16(a.w[i], b.w[i]);
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t largest(const Four<F32> &m)
+{
+    if constexpr (F32) return umax32(umax32(m.w[0], m.w[1]), umax32(m.w[2], m.w[3]));
+    const uint32_t t = max_u16(m.w[0], m.w[1]);
+    return umax32(t, t << 16);
+}
+
+// The codes of a column's eight consecutive rows, in the order of the rows.
+template <bool F32>
+__device__ __forceinline__ uint32_t column_codes(const Four<F32> *f, int j, uint32_t scale)
+{
+    if constexpr (F32) {
+        uint32_t q = codes2<0>(0u, f[0].w[j], f[1].w[j], scale);
+        q = codes2<1>(q, f[2].w[j], f[3].w[j], scale);
+        q = codes2<2>(q, f[4].w[j], f[5].w[j], scale);
+        return codes2<3>(q, f[6].w[j], f[7].w[j], scale);
+    } else {
+        const int k = j >> 1;
+        const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+        uint32_t q = codes2<0>(0u, __builtin_amdgcn_perm(f[1].w[k], f[0].w[k], sel), scale);
+        q = codes2<1>(q, __builtin_amdgcn_perm(f[3].w[k], f[2].w[k], sel), scale);
+        q = codes2<2>(q, __builtin_amdgcn_perm(f[5].w[k], f[4].w[k], sel), scale);
+        return codes2<3>(q, __builtin_amdgcn_perm(f[7].w[k], f[6].w[k], sel), scale);
     }
 }
 
-__device__ __forceinline__ uint32_t exponent(uint32_t bits) { return (bits >> 23) & 0xFFu; }
-
-// Maximum over aligned groups of eight lanes.
-__device__ __forceinline__ uint32_t max8(uint32_t x)
-{
-    x = umax32(x, __shfl_xor(x, 1, kWaveLanes));
-    x = umax32(x, __shfl_xor(x, 2, kWaveLanes));
-    return umax32(x, __shfl_xor(x, 4, kWaveLanes));
-}
-
-// Codes of x along its rows (ROWS) and of its transpose (COLS), from one read.
+// Codes of x along its rows (ROWS) and of its transpose (COLS), from one
+// read.  A workgroup's four wavefronts take 128 rows, so that it writes 64
+// bytes of each column's codes and one word of its scales; those, and the
+// rows' scales, go through LDS to be stored in such pieces.
 template <bool F32, bool ROWS, bool COLS, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, int64_t row_bytes,
-                   uint32_t col_tiles, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                   uint32_t row_tiles, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t)
 {
+    __shared__ __align__(16) u32x4 s_codes[COLS ? kTileCols * kQuantWaves : 1];
+    __shared__ __align__(16) uint8_t s_scales_t[COLS ? kTileCols * kQuantWaves : 1];
+    __shared__ __align__(16) uint16_t s_rows[ROWS ? kTileRows * 64 : 1];
+    __shared__ __align__(16) uint8_t s_scales[ROWS ? kTileRows * (kTileCols / 32) : 1];
     const int lane = threadIdx.x & (kWaveLanes - 1);
-    const int wave = threadIdx.x / kWaveLanes;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / col_tiles) * kTileRows + wave * kWaveRows;
-    const int64_t c = static_cast<int64_t>(blockIdx.x % col_tiles) * kTileCols + lane * kLaneCols;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    // the tiles of one XCD are neighbours down the rows: two of them write
+    // the two halves of a line of codes_t
+    const uint32_t tile = xcd_contiguous(blockIdx.x, gridDim.x);
+    const int64_t tile_row = static_cast<int64_t>(tile % row_tiles) * kTileRows;
+    const int64_t tile_col = static_cast<int64_t>(tile / row_tiles) * kTileCols;
+    const int64_t row0 = tile_row + wave * kWaveRows, c = tile_col + lane * kLaneCols;
     const int64_t colsp = mx_padded(cols), rowsp = mx_padded(rows);
 
-    uint32_t w[kWaveRows][kLaneCols];
+    Four<F32> f[kWaveRows];
 #pragma unroll
     for (int r = 0; r < kWaveRows; ++r) {
-        if (row0 + r < rows) {
-            load4<F32, VEC>(x + (row0 + r) * row_bytes, c, cols, w[r]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kLaneCols; ++j) w[r][j] = 0u;
-        }
+        f[r] = Four<F32>{};
+        if (row0 + r < rows) f[r] = load4<F32, VEC>(x + (row0 + r) * row_bytes, c, cols);
     }
+    Four<F32> col_top{};
+#pragma unroll
+    for (int r = 0; r < kWaveRows; ++r) raise(col_top, magnitudes(f[r]));
+    // infinities and NaN are rare: the selects for them run only where the
+    // wavefront has seen one
+    const bool bad = __any(largest(col_top) >= kExponent);
+
     if constexpr (ROWS) {
 #pragma unroll
         for (int r = 0; r < kWaveRows; ++r) {
-            if (row0 + r >= rows) break;
-            const uint32_t e = max8(umax32(umax32(exponent(w[r][0]), exponent(w[r][1])),
-                                           umax32(exponent(w[r][2]), exponent(w[r][3]))));
-            const uint32_t b = scale_byte(e);
-            const float f = scale_recip(b);
-            uint32_t q = codes2<0>(0u, __uint_as_float(w[r][0]) * f, __uint_as_float(w[r][1]) * f);
-            q = codes2<1>(q, __uint_as_float(w[r][2]) * f, __uint_as_float(w[r][3]) * f);
-            if (b == 255u) q = 0u;
-            if (c < colsp) {
-                *reinterpret_cast<uint16_t *>(codes + (row0 + r) * (colsp / 2) + c / 2) =
-                    static_cast<uint16_t>(q);
-                if ((lane & 7) == 0)
-                    scales[(row0 + r) * (colsp / 32) + c / 32] = static_cast<uint8_t>(b);
+            // opaque, or the magnitudes above would be kept for this use and
+            // double the registers
+#pragma unroll
+            for (int i = 0; i < (F32 ? 4 : 2); ++i) asm volatile("" : "+v"(f[r].w[i]));
+            const uint32_t top = max8(largest(magnitudes(f[r])));
+            const uint32_t scale = scale_bits(top);
+            uint32_t q, b = scale >> 23;
+            if constexpr (F32) {
+                q = codes2<0>(0u, f[r].w[0], f[r].w[1], scale);
+                q = codes2<1>(q, f[r].w[2], f[r].w[3], scale);
+            } else {
+                q = codes2<0>(0u, f[r].w[0], scale);
+                q = codes2<1>(q, f[r].w[1], scale);
             }
+            if (bad && top >= kExponent) {
+                q = 0u;
+                b = 255u;
+            }
+            if ((lane & 7) == 0) s_scales[(wave * kWaveRows + r) * (kTileCols / 32) + lane / 8] = static_cast<uint8_t>(b);
+            s_rows[(wave * kWaveRows + r) * 64 + lane] = static_cast<uint16_t>(q);
+            __builtin_amdgcn_sched_barrier(0);        // row by row: fewer registers, more wavefronts
         }
     }
     if constexpr (COLS) {
 #pragma unroll
         for (int j = 0; j < kLaneCols; ++j) {
-            uint32_t e = 0u;
-#pragma unroll
-            for (int r = 0; r < kWaveRows; ++r) e = umax32(e, exponent(w[r][j]));
-            const uint32_t b = scale_byte(e);
-            const float f = scale_recip(b);
-            uint32_t q[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(w[8 * k + i][j]) * f;
-                q[k] = b == 255u ? 0u : codes8(y);
+            uint32_t top;
+            if constexpr (F32) top = col_top.w[j];
+            else top = (j & 1) ? col_top.w[j / 2] & 0xFFFF0000u : col_top.w[j / 2] << 16;
+            const uint32_t scale = scale_bits(top);
+            uint32_t b = scale >> 23;
+            u32x4 q{column_codes(&f[0], j, scale), column_codes(&f[8], j, scale), column_codes(&f[16], j, scale),
+                    column_codes(&f[24], j, scale)};
+            if (bad && top >= kExponent) {
+                q = u32x4{0u, 0u, 0u, 0u};
+                b = 255u;
             }
-            if (c + j < cols) {
-                *reinterpret_cast<u32x4 *>(codes_t + (c + j) * (rowsp / 2) + row0 / 2) =
-                    u32x4{q[0], q[1], q[2], q[3]};
-                scales_t[(c + j) * (rowsp / 32) + row0 / 32] = static_cast<uint8_t>(b);
-            }
+            const int col = lane * kLaneCols + j;
+            // 16-byte slots, the eight that share the banks turned by the
+            // lane so that eight lanes' stores fall on all of them
+            s_codes[(col * kQuantWaves + wave) ^ (lane & 7)] = q;
+            s_scales_t[col * kQuantWaves + wave] = static_cast<uint8_t>(b);
         }
+    }
+    __syncthreads();
+    if constexpr (ROWS) {
+#pragma unroll
+        for (int i = 0; i < kTileRows * 8 / kThreads; ++i) {
+            const int u = i * kThreads + threadIdx.x;
+            const int64_t row = tile_row + u / 8, byte = tile_col / 2 + (u % 8) * 16;
+            if (row < rows && byte < colsp / 2)
+                *reinterpret_cast<u32x4 *>(codes + row * (colsp / 2) + byte) =
+                    *reinterpret_cast<const u32x4 *>(&s_rows[u * 8]);
+        }
+        const int r = threadIdx.x;                // eight groups to a row of the tile, fours of them there or not
+        if (r < kTileRows && tile_row + r < rows) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(&s_scales[r * (kTileCols / 32)]);
+            uint8_t *p = scales + (tile_row + r) * (colsp / 32) + tile_col / 32;
+            *reinterpret_cast<uint32_t *>(p) = v.x;
+            if (tile_col + 128 < colsp) *reinterpret_cast<uint32_t *>(p + 4) = v.y;
+        }
+    }
+    if constexpr (COLS) {
+#pragma unroll
+        for (int i = 0; i < kQuantWaves; ++i) {
+            const int u = i * kThreads + threadIdx.x, col = u / kQuantWaves;
+            if (tile_col + col < cols)
+                *reinterpret_cast<u32x4 *>(codes_t + (tile_col + col) * (rowsp / 2) + tile_row / 2 +
+                                           (u % kQuantWaves) * 16) = s_codes[u ^ ((col / kLaneCols) & 7)];
+        }
+        const int col = threadIdx.x;
+        if (tile_col + col < cols)
+            *reinterpret_cast<uint32_t *>(scales_t + (tile_col + col) * (rowsp / 32) + tile_row / 32) =
+                *reinterpret_cast<const uint32_t *>(&s_scales_t[col * kQuantWaves]);
     }
 }
 
@@ -224,7 +345,7 @@ mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restric
             } else {
                 u32x4 p;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = bf16_rne(v[2 * k]) | (bf16_rne(v[2 * k + 1]) << 16);
+                for (int k = 0; k < 4; ++k) p[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
                 *reinterpret_cast<u32x4 *>(o + c * 2) = p;
             }
         } else {
@@ -232,7 +353,7 @@ mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restric
             for (int k = 0; k < 8; ++k) {
                 if (c + k >= cols) break;
                 if constexpr (F32) reinterpret_cast<float *>(o)[c + k] = v[k];
-                else reinterpret_cast<uint16_t *>(o)[c + k] = static_cast<uint16_t>(bf16_rne(v[k]));
+                else reinterpret_cast<uint16_t *>(o)[c + k] = bf16_rne(v[k]);
             }
         }
     }
@@ -259,8 +380,7 @@ __device__ __forceinline__ void store4(uint8_t *out, int64_t row_bytes, int64_t 
         if constexpr (F32) {
             *reinterpret_cast<f32x4 *>(o + n * 4) = f32x4{a, b, c, d};
         } else {
-            *reinterpret_cast<u32x2 *>(o + n * 2) =
-                u32x2{bf16_rne(a) | (bf16_rne(b) << 16), bf16_rne(c) | (bf16_rne(d) << 16)};
+            *reinterpret_cast<u32x2 *>(o + n * 2) = u32x2{bf16_pair(a, b), bf16_pair(c, d)};
         }
         return;
     }
@@ -269,7 +389,7 @@ __device__ __forceinline__ void store4(uint8_t *out, int64_t row_bytes, int64_t 
     for (int i = 0; i < 4; ++i) {
         if (n + i >= cols) break;
         if constexpr (F32) reinterpret_cast<float *>(o)[n + i] = v[i];
-        else reinterpret_cast<uint16_t *>(o)[n + i] = static_cast<uint16_t>(bf16_rne(v[i]));
+        else reinterpret_cast<uint16_t *>(o)[n + i] = bf16_rne(v[i]);
     }
 }
 
@@ -389,9 +509,11 @@ mx_skinny_kernel(MxIn a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t 
 // takes at one c then fall on all banks.  Two buffers: the copy of the next
 // step runs while this one is multiplied, one barrier a step.
 //
-// Scales go straight to registers, eight bytes of a row and step; the four
-// that a lane needs (groups 2 k + lane / 32) are gathered into one word with
-// a byte permutation, from which the instruction selects by an immediate.
+// Scales: each thread carries 16 bytes of one row, two steps' worth, through
+// a register to LDS.  (Loaded by the lanes that use them they cost 32 cache
+// lines an instruction, and set the time: 8192^3 took 485 us.)  The four that
+// a lane needs of a step's eight (groups 2 k + lane / 32) are gathered into
+// one word with a byte permutation, and the instruction selects its byte.
 typedef __attribute__((address_space(1))) const uint8_t g_u8;
 typedef __attribute__((address_space(3))) uint8_t l_u8;
 
@@ -403,7 +525,8 @@ struct Tile {
     static constexpr int kBytes = kRows * 128;             // one buffer
     static constexpr int kCopies = kRows / 8 / kWaves;     // DMA instructions of a wavefront and step
     static constexpr int kTN = BN / WN / 32, kTM = BM / WM / 32;
-    static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0, "tile");
+    static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 &&
+                      kRows <= kTileThreads, "tile");
 };
 
 // The tile of this workgroup: neighbours on one XCD (workgroup b runs on XCD
@@ -413,10 +536,7 @@ constexpr uint32_t kGroupM = 4;
 
 __device__ __forceinline__ void tile_of_block(uint32_t tiles_n, uint32_t tiles_m, uint32_t &tn, uint32_t &tm)
 {
-    const uint32_t nb = gridDim.x, b = blockIdx.x, x = b % 8u;
-    const uint32_t per = (nb + 7u) / 8u, full = nb % 8u;
-    uint32_t lb = x * per + b / 8u;
-    if (full != 0u && x > full) lb -= x - full;
+    const uint32_t lb = xcd_contiguous(blockIdx.x, gridDim.x);
     const uint32_t group = lb / (kGroupM * tiles_n), first = group * kGroupM;
     const uint32_t width = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
     const uint32_t in = lb - group * kGroupM * tiles_n;
@@ -431,6 +551,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
 {
     using T = Tile<BN, BM, WN, WM>;
     __shared__ __align__(128) uint8_t s_buf[2][T::kBytes];
+    __shared__ u32x4 s_scales[2][T::kRows];
     const int lane = threadIdx.x & (kWaveLanes - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int wn = wave % WN, wm = wave / WN;
@@ -439,53 +560,65 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
     const int64_t n0 = static_cast<int64_t>(tile_n) * BN, m0 = static_cast<int64_t>(tile_m) * BM;
     const uint32_t code_stride = static_cast<uint32_t>(kp / 2), scale_stride = static_cast<uint32_t>(kp / 32);
 
-    // this lane's rows of the copies, clamped to the matrices: a row past the
-    // end repeats the last one and is not stored
-    const uint8_t *src[T::kCopies];
-    const int slot_chunk = (lane & 7) ^ (lane >> 3);
+    // Addresses are a uniform base and a 32-bit offset of the lane (kp is at
+    // most 2^25, so 256 rows of codes span less than 4 GiB).  Rows are clamped
+    // to the matrices: a row past the end repeats the last one, unstored.
+    const uint8_t *b_codes = b.codes + n0 * code_stride, *a_codes = a.codes + m0 * code_stride;
+    const uint8_t *b_scales = b.scales + n0 * scale_stride, *a_scales = a.scales + m0 * scale_stride;
+    const int n_last = static_cast<int>(b.rows - n0 < BN ? b.rows - n0 : BN) - 1;
+    const int m_last = static_cast<int>(a.rows - m0 < BM ? a.rows - m0 : BM) - 1;
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;     // for rows 0 to 7 of 16; ^ 64 for 8 to 15
+    uint32_t src[T::kCopies];
 #pragma unroll
     for (int i = 0; i < T::kCopies; ++i) {
-        const int r = (wave * T::kCopies + i) * 8 + (lane >> 3);      // row of the buffer
-        const bool is_b = (wave * T::kCopies + i) * 8 < BN;
-        const MxIn &in = is_b ? b : a;
-        int64_t row = is_b ? n0 + r : m0 + r - BN;
-        if (row >= in.rows) row = in.rows - 1;
-        src[i] = in.codes + row * code_stride;
+        const int first = (wave * T::kCopies + i) * 8, r = (first < BN ? first : first - BN) + (lane >> 3);
+        const int last = first < BN ? n_last : m_last;
+        src[i] = static_cast<uint32_t>(r < last ? r : last) * code_stride;
     }
-    const uint8_t *scale_n[T::kTN], *scale_m[T::kTM];
-#pragma unroll
-    for (int i = 0; i < T::kTN; ++i) {
-        int64_t row = n0 + (wn * T::kTN + i) * 32 + (lane & 31);
-        if (row >= b.rows) row = b.rows - 1;
-        scale_n[i] = b.scales + row * scale_stride;
-    }
-#pragma unroll
-    for (int i = 0; i < T::kTM; ++i) {
-        int64_t row = m0 + (wm * T::kTM + i) * 32 + (lane & 31);
-        if (row >= a.rows) row = a.rows - 1;
-        scale_m[i] = a.scales + row * scale_stride;
-    }
+    // thread t carries the scales of buffer row t
+    const int srow = threadIdx.x < BN ? threadIdx.x : threadIdx.x - BN;
+    const int slast = threadIdx.x < BN ? n_last : m_last;
+    const uint8_t *s_src = (threadIdx.x < BN ? b_scales : a_scales) +
+                           static_cast<uint32_t>(srow < slast ? srow : slast) * scale_stride;
     const int g = lane >> 5;
     const uint32_t gather = g ? 0x07050301u : 0x06040200u;
 
-    const int64_t steps = (kp + 255) / 256;
+    const int steps = static_cast<int>((kp + 255) / 256);
     const bool half_end = (kp & 128) != 0;       // the last step has 128 elements
 
-    auto copy = [&](int64_t k, int buf) {
+    auto copy = [&](int k, int buf) {
         // the second half of a half step repeats the first: it is not used
-        const int chunk = (half_end && k == steps - 1) ? (slot_chunk & 3) : slot_chunk;
+        const uint32_t at = (half_end && k == steps - 1) ? (chunk & 48u) : chunk;
 #pragma unroll
         for (int i = 0; i < T::kCopies; ++i) {
-            const uint8_t *p = src[i] + k * 128 + chunk * 16;
-            uint8_t *l = &s_buf[buf][(wave * T::kCopies + i) * 1024];
-            __builtin_amdgcn_global_load_lds((g_u8 *)p, (l_u8 *)l, 16, 0, 0);
+            const int first = (wave * T::kCopies + i) * 8;
+            const uint8_t *base = (first < BN ? b_codes : a_codes) + static_cast<int64_t>(k) * 128;
+            const uint32_t turn = (half_end && k == steps - 1) ? 0u : (first & 8) * 8u;
+            uint8_t *l = &s_buf[buf][first * 128];
+            __builtin_amdgcn_global_load_lds((g_u8 *)(base + (src[i] + (at ^ turn))), (l_u8 *)l, 16, 0, 0);
         }
     };
-    auto scale_word = [&](const uint8_t *p, int64_t k) {
-        const uint32_t lo = *reinterpret_cast<const uint32_t *>(p + k * 8);
-        const uint32_t hi = *reinterpret_cast<const uint32_t *>(
-            p + k * 8 + ((half_end && k == steps - 1) ? 0 : 4));
-        return __builtin_amdgcn_perm(hi, lo, gather);
+    // the scales of steps 2 p and 2 p + 1: 16 bytes of a row, or what is left
+    auto load_scales = [&](int p) {
+        u32x4 v{0u, 0u, 0u, 0u};
+        if (threadIdx.x < T::kRows) {
+            const uint32_t at = static_cast<uint32_t>(p) * 16u;
+            if (at + 16u <= scale_stride) {
+                v = *reinterpret_cast<const u32x4_packed *>(s_src + at);
+            } else {
+#pragma unroll
+                for (uint32_t w = 0; w < 3; ++w)
+                    if (at + 4 * w < scale_stride) v[w] = *reinterpret_cast<const uint32_t *>(s_src + at + 4 * w);
+            }
+        }
+        return v;
+    };
+    auto store_scales = [&](int p, u32x4 v) {
+        if (threadIdx.x < T::kRows) s_scales[p & 1][threadIdx.x] = v;
+    };
+    auto scale_word = [&](int k, int row) {
+        const u32x2 v = *(reinterpret_cast<const u32x2 *>(&s_scales[(k >> 1) & 1][row]) + (k & 1));
+        return __builtin_amdgcn_perm(v.y, v.x, gather);
     };
 
     f32x16 acc[T::kTN][T::kTM];
@@ -498,7 +631,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
 
     uint32_t off[4];             // this lane's chunk of each quarter step
 #pragma unroll
-    for (int q = 0; q < 4; ++q) off[q] = (lane & 31) * 128 + (((2 * q + g) ^ (lane & 7)) << 4);
+    for (int q = 0; q < 4; ++q) off[q] = (lane & 31) * 128 + (((2 * q + g) ^ ((lane >> 1) & 7)) << 4);
 
     auto multiply = [&](int buf, const uint32_t (&sn)[T::kTN], const uint32_t (&sm)[T::kTM], auto quarter) {
         constexpr int q = decltype(quarter)::value;
@@ -515,17 +648,23 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
             for (int j = 0; j < T::kTM; ++j) acc[i][j] = mfma32<q>(vn[i], vm[j], acc[i][j], sn[i], sm[j]);
     };
 
-    if (steps > 0) copy(0, 0);
-    for (int64_t k = 0; k < steps; ++k) {
-        const int buf = static_cast<int>(k & 1);
+    u32x4 next_scales{0u, 0u, 0u, 0u};
+    if (steps > 0) {
+        store_scales(0, load_scales(0));
+        copy(0, 0);
+    }
+    for (int k = 0; k < steps; ++k) {
+        const int buf = k & 1;
+        __builtin_amdgcn_s_waitcnt(0);   // this wavefront's copies have reached LDS
+        __syncthreads();                 // everyone's have, and the other buffers are free
+        if (k & 1) store_scales((k >> 1) + 1, next_scales);
+        else if (k + 2 < steps) next_scales = load_scales((k >> 1) + 1);
+        if (k + 1 < steps) copy(k + 1, buf ^ 1);
         uint32_t sn[T::kTN], sm[T::kTM];
 #pragma unroll
-        for (int i = 0; i < T::kTN; ++i) sn[i] = scale_word(scale_n[i], k);
+        for (int i = 0; i < T::kTN; ++i) sn[i] = scale_word(k, (wn * T::kTN + i) * 32 + (lane & 31));
 #pragma unroll
-        for (int i = 0; i < T::kTM; ++i) sm[i] = scale_word(scale_m[i], k);
-        __builtin_amdgcn_s_waitcnt(0);   // this wavefront's copies have reached LDS
-        __syncthreads();                 // everyone's have, and the other buffer is free
-        if (k + 1 < steps) copy(k + 1, buf ^ 1);
+        for (int i = 0; i < T::kTM; ++i) sm[i] = scale_word(k, BN + (wm * T::kTM + i) * 32 + (lane & 31));
         multiply(buf, sn, sm, std::integral_constant<int, 0>{});
         multiply(buf, sn, sm, std::integral_constant<int, 1>{});
         if (!(half_end && k == steps - 1)) {
@@ -564,10 +703,10 @@ hipError_t quantize_layout(const MxMatrix &x, uint8_t *codes, uint8_t *scales, u
     constexpr int vec = F32 ? 16 : 8;
     if (aligned_to(p, vec) && row_bytes % vec == 0)
         hipLaunchKernelGGL((mx_quantize_kernel<F32, ROWS, COLS, true>), grid, dim3(kThreads), 0, st, p, x.rows,
-                           x.cols, row_bytes, col_tiles, codes, scales, codes_t, scales_t);
+                           x.cols, row_bytes, row_tiles, codes, scales, codes_t, scales_t);
     else
         hipLaunchKernelGGL((mx_quantize_kernel<F32, ROWS, COLS, false>), grid, dim3(kThreads), 0, st, p, x.rows,
-                           x.cols, row_bytes, col_tiles, codes, scales, codes_t, scales_t);
+                           x.cols, row_bytes, row_tiles, codes, scales, codes_t, scales_t);
     return hipGetLastError();
 }
 
