@@ -35,6 +35,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = kBlockThreads;
+constexpr unsigned kCus = 256;
 
 // Number b of nb workgroups renumbered so that each of the 8 XCDs (workgroup b
 // runs on XCD b % 8) takes one contiguous eighth of them.
@@ -524,19 +525,20 @@ struct Tile {
     static constexpr int kRows = BN + BM;                  // rows of B, then of A
     static constexpr int kBytes = kRows * 128;             // one buffer
     static constexpr int kCopies = kRows / 8 / kWaves;     // DMA instructions of a wavefront and step
+    static constexpr int kLds = 2 * kBytes + 2 * kRows * 16;
     static constexpr int kTN = BN / WN / 32, kTM = BM / WM / 32;
     static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 &&
                       kRows <= kTileThreads, "tile");
 };
 
-// The tile of this workgroup: neighbours on one XCD (workgroup b runs on XCD
-// b % 8) take neighbouring tiles, in columns of kGroupM tiles, so that the
-// 32 or so that run together share their rows in the XCD's L2.
+// Tile number t of a launch: neighbours on one XCD take neighbouring tiles,
+// in columns of kGroupM tiles, so that the 32 or so that run together share
+// their rows in the XCD's L2.
 constexpr uint32_t kGroupM = 4;
 
-__device__ __forceinline__ void tile_of_block(uint32_t tiles_n, uint32_t tiles_m, uint32_t &tn, uint32_t &tm)
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_n, uint32_t tiles_m, uint32_t &tn, uint32_t &tm)
 {
-    const uint32_t lb = xcd_contiguous(blockIdx.x, gridDim.x);
+    const uint32_t lb = xcd_contiguous(t, tiles_n * tiles_m);
     const uint32_t group = lb / (kGroupM * tiles_n), first = group * kGroupM;
     const uint32_t width = tiles_m - first < kGroupM ? tiles_m - first : kGroupM;
     const uint32_t in = lb - group * kGroupM * tiles_n;
@@ -550,52 +552,58 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
                int64_t row_bytes)
 {
     using T = Tile<BN, BM, WN, WM>;
+    constexpr int kTN = T::kTN, kTM = T::kTM;
     __shared__ __align__(128) uint8_t s_buf[2][T::kBytes];
     __shared__ u32x4 s_scales[2][T::kRows];
     const int lane = threadIdx.x & (kWaveLanes - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
-    const int wn = wave % WN, wm = wave / WN;
-    uint32_t tile_n, tile_m;
-    tile_of_block(tiles_n, tiles_m, tile_n, tile_m);
-    const int64_t n0 = static_cast<int64_t>(tile_n) * BN, m0 = static_cast<int64_t>(tile_m) * BM;
+    const int wn = wave % WN, wm = wave / WN, g = lane >> 5;
     const uint32_t code_stride = static_cast<uint32_t>(kp / 2), scale_stride = static_cast<uint32_t>(kp / 32);
-
-    // Addresses are a uniform base and a 32-bit offset of the lane (kp is at
-    // most 2^25, so 256 rows of codes span less than 4 GiB).  Rows are clamped
-    // to the matrices: a row past the end repeats the last one, unstored.
-    const uint8_t *b_codes = b.codes + n0 * code_stride, *a_codes = a.codes + m0 * code_stride;
-    const uint8_t *b_scales = b.scales + n0 * scale_stride, *a_scales = a.scales + m0 * scale_stride;
-    const int n_last = static_cast<int>(b.rows - n0 < BN ? b.rows - n0 : BN) - 1;
-    const int m_last = static_cast<int>(a.rows - m0 < BM ? a.rows - m0 : BM) - 1;
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;     // for rows 0 to 7 of 16; ^ 64 for 8 to 15
-    uint32_t src[T::kCopies];
-#pragma unroll
-    for (int i = 0; i < T::kCopies; ++i) {
-        const int first = (wave * T::kCopies + i) * 8, r = (first < BN ? first : first - BN) + (lane >> 3);
-        const int last = first < BN ? n_last : m_last;
-        src[i] = static_cast<uint32_t>(r < last ? r : last) * code_stride;
-    }
-    // thread t carries the scales of buffer row t
-    const int srow = threadIdx.x < BN ? threadIdx.x : threadIdx.x - BN;
-    const int slast = threadIdx.x < BN ? n_last : m_last;
-    const uint8_t *s_src = (threadIdx.x < BN ? b_scales : a_scales) +
-                           static_cast<uint32_t>(srow < slast ? srow : slast) * scale_stride;
-    const int g = lane >> 5;
-    const uint32_t gather = g ? 0x07050301u : 0x06040200u;
-
     const int steps = static_cast<int>((kp + 255) / 256);
     const bool half_end = (kp & 128) != 0;       // the last step has 128 elements
+    const uint32_t total = tiles_n * tiles_m;
 
+    // Where the copies of a tile come from: uniform bases and 32-bit offsets
+    // of the lane (kp is at most 2^25, so 256 rows of codes span at most
+    // 4 GiB).  Rows are clamped to the matrices: a row past the end repeats
+    // the last one, unstored.
+    int64_t n0, m0;
+    const uint8_t *b_codes, *a_codes, *scale_src;
+    uint32_t src[T::kCopies];
+    auto aim = [&](uint32_t t) {
+        uint32_t tile_n, tile_m;
+        tile_at(t, tiles_n, tiles_m, tile_n, tile_m);
+        n0 = static_cast<int64_t>(tile_n) * BN;
+        m0 = static_cast<int64_t>(tile_m) * BM;
+        b_codes = b.codes + n0 * code_stride;
+        a_codes = a.codes + m0 * code_stride;
+        const int n_last = static_cast<int>(b.rows - n0 < BN ? b.rows - n0 : BN) - 1;
+        const int m_last = static_cast<int>(a.rows - m0 < BM ? a.rows - m0 : BM) - 1;
+#pragma unroll
+        for (int i = 0; i < T::kCopies; ++i) {
+            const int first = (wave * T::kCopies + i) * 8, r = (first < BN ? first : first - BN) + (lane >> 3);
+            const int last = first < BN ? n_last : m_last;
+            src[i] = static_cast<uint32_t>(r < last ? r : last) * code_stride;
+        }
+        // thread t carries the scales of buffer row t
+        const bool of_b = threadIdx.x < BN;
+        const int r = of_b ? threadIdx.x : threadIdx.x - BN, last = of_b ? n_last : m_last;
+        scale_src = (of_b ? b.scales + n0 * scale_stride : a.scales + m0 * scale_stride) +
+                    static_cast<uint32_t>(r < last ? r : last) * scale_stride;
+    };
+    // slot s of row r holds chunk s ^ ((r / 2) & 7): for rows 0 to 7 of a
+    // copy's 16 here, for rows 8 to 15 with bit 2 of the chunk turned
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;
     auto copy = [&](int k, int buf) {
         // the second half of a half step repeats the first: it is not used
-        const uint32_t at = (half_end && k == steps - 1) ? (chunk & 48u) : chunk;
+        const bool half = half_end && k == steps - 1;
 #pragma unroll
         for (int i = 0; i < T::kCopies; ++i) {
             const int first = (wave * T::kCopies + i) * 8;
             const uint8_t *base = (first < BN ? b_codes : a_codes) + static_cast<int64_t>(k) * 128;
-            const uint32_t turn = (half_end && k == steps - 1) ? 0u : (first & 8) * 8u;
+            const uint32_t at = half ? (chunk & 48u) : (chunk ^ ((first & 8) * 8u));
             uint8_t *l = &s_buf[buf][first * 128];
-            __builtin_amdgcn_global_load_lds((g_u8 *)(base + (src[i] + (at ^ turn))), (l_u8 *)l, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((g_u8 *)(base + (src[i] + at)), (l_u8 *)l, 16, 0, 0);
         }
     };
     // the scales of steps 2 p and 2 p + 1: 16 bytes of a row, or what is left
@@ -604,86 +612,164 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
         if (threadIdx.x < T::kRows) {
             const uint32_t at = static_cast<uint32_t>(p) * 16u;
             if (at + 16u <= scale_stride) {
-                v = *reinterpret_cast<const u32x4_packed *>(s_src + at);
+                v = *reinterpret_cast<const u32x4_packed *>(scale_src + at);
             } else {
 #pragma unroll
                 for (uint32_t w = 0; w < 3; ++w)
-                    if (at + 4 * w < scale_stride) v[w] = *reinterpret_cast<const uint32_t *>(s_src + at + 4 * w);
+                    if (at + 4 * w < scale_stride) v[w] = *reinterpret_cast<const uint32_t *>(scale_src + at + 4 * w);
             }
         }
         return v;
     };
-    auto store_scales = [&](int p, u32x4 v) {
-        if (threadIdx.x < T::kRows) s_scales[p & 1][threadIdx.x] = v;
+    auto store_scales = [&](int set, u32x4 v) {
+        if (threadIdx.x < T::kRows) s_scales[set][threadIdx.x] = v;
     };
-    auto scale_word = [&](int k, int row) {
-        const u32x2 v = *(reinterpret_cast<const u32x2 *>(&s_scales[(k >> 1) & 1][row]) + (k & 1));
+    const uint32_t gather = g ? 0x07050301u : 0x06040200u;
+    auto scale_word = [&](int set, int k, int row) {
+        const u32x2 v = *(reinterpret_cast<const u32x2 *>(&s_scales[set][row]) + (k & 1));
         return __builtin_amdgcn_perm(v.y, v.x, gather);
     };
-
-    f32x16 acc[T::kTN][T::kTM];
-#pragma unroll
-    for (int i = 0; i < T::kTN; ++i)
-#pragma unroll
-        for (int j = 0; j < T::kTM; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
     uint32_t off[4];             // this lane's chunk of each quarter step
 #pragma unroll
     for (int q = 0; q < 4; ++q) off[q] = (lane & 31) * 128 + (((2 * q + g) ^ ((lane >> 1) & 7)) << 4);
-
-    auto multiply = [&](int buf, const uint32_t (&sn)[T::kTN], const uint32_t (&sm)[T::kTM], auto quarter) {
-        constexpr int q = decltype(quarter)::value;
-        u32x4 vn[T::kTN], vm[T::kTM];
+    struct Operands {
+        u32x4 n[kTN], m[kTM];
+    };
+    auto fetch = [&](int buf, int q, Operands &v) {
 #pragma unroll
-        for (int i = 0; i < T::kTN; ++i)
-            vn[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * T::kTN + i) * 4096 + off[q]]);
+        for (int i = 0; i < kTN; ++i)
+            v.n[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * kTN + i) * 4096 + off[q]]);
 #pragma unroll
-        for (int i = 0; i < T::kTM; ++i)
-            vm[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * T::kTM + i) * 4096 + off[q]]);
-#pragma unroll
-        for (int i = 0; i < T::kTN; ++i)
-#pragma unroll
-            for (int j = 0; j < T::kTM; ++j) acc[i][j] = mfma32<q>(vn[i], vm[j], acc[i][j], sn[i], sm[j]);
+        for (int i = 0; i < kTM; ++i)
+            v.m[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * kTM + i) * 4096 + off[q]]);
     };
 
-    u32x4 next_scales{0u, 0u, 0u, 0u};
-    if (steps > 0) {
-        store_scales(0, load_scales(0));
-        copy(0, 0);
-    }
-    for (int k = 0; k < steps; ++k) {
-        const int buf = k & 1;
-        __builtin_amdgcn_s_waitcnt(0);   // this wavefront's copies have reached LDS
-        __syncthreads();                 // everyone's have, and the other buffers are free
-        if (k & 1) store_scales((k >> 1) + 1, next_scales);
-        else if (k + 2 < steps) next_scales = load_scales((k >> 1) + 1);
-        if (k + 1 < steps) copy(k + 1, buf ^ 1);
-        uint32_t sn[T::kTN], sm[T::kTM];
+    f32x16 acc[kTN][kTM];
+    uint32_t sn[kTN], sm[kTM];
+    auto multiply = [&](const Operands &v, auto quarter) {
+        constexpr int q = decltype(quarter)::value;
 #pragma unroll
-        for (int i = 0; i < T::kTN; ++i) sn[i] = scale_word(k, (wn * T::kTN + i) * 32 + (lane & 31));
+        for (int i = 0; i < kTN; ++i)
 #pragma unroll
-        for (int i = 0; i < T::kTM; ++i) sm[i] = scale_word(k, BN + (wm * T::kTM + i) * 32 + (lane & 31));
-        multiply(buf, sn, sm, std::integral_constant<int, 0>{});
-        multiply(buf, sn, sm, std::integral_constant<int, 1>{});
-        if (!(half_end && k == steps - 1)) {
-            multiply(buf, sn, sm, std::integral_constant<int, 2>{});
-            multiply(buf, sn, sm, std::integral_constant<int, 3>{});
-        }
-    }
+            for (int j = 0; j < kTM; ++j) acc[i][j] = mfma32<q>(v.n[i], v.m[j], acc[i][j], sn[i], sm[j]);
+    };
 
-    // block element e of a lane: m = lane % 32, n = 8 (e / 4) + 4 (lane / 32) + e % 4
+    uint32_t t = blockIdx.x;
+    if (t >= total) return;
+    aim(t);
+    int buf = 0, set = 0;        // the buffers of the step and of its scales
+    store_scales(0, load_scales(0));
+    copy(0, 0);
+    while (true) {
+        const int64_t tile_n0 = n0, tile_m0 = m0;
+        const bool more = t + gridDim.x < total;
 #pragma unroll
-    for (int j = 0; j < T::kTM; ++j) {
-        const int64_t m = m0 + (wm * T::kTM + j) * 32 + (lane & 31);
-        if (m >= a.rows) continue;
+        for (int i = 0; i < kTN; ++i)
 #pragma unroll
-        for (int i = 0; i < T::kTN; ++i)
+            for (int j = 0; j < kTM; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                store4<F32, VEC>(out, row_bytes, m, n0 + (wn * T::kTN + i) * 32 + 2 * e + 4 * g, b.rows,
-                                 acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        u32x4 next_scales{0u, 0u, 0u, 0u};
+        for (int k = 0; k < steps; ++k, buf ^= 1) {
+            __builtin_amdgcn_s_waitcnt(0);   // this wavefront's copies have reached LDS
+            __syncthreads();                 // everyone's have, and the other buffers are free
+            Operands v[2];
+            fetch(buf, 0, v[0]);
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) sn[i] = scale_word(set, k, (wn * kTN + i) * 32 + (lane & 31));
+#pragma unroll
+            for (int i = 0; i < kTM; ++i) sm[i] = scale_word(set, k, BN + (wm * kTM + i) * 32 + (lane & 31));
+            const bool last = k == steps - 1;
+            if ((k & 1) && !last) store_scales(set ^ 1, next_scales);
+            if (!last) {
+                if (!(k & 1) && k + 2 < steps) next_scales = load_scales((k >> 1) + 1);
+                copy(k + 1, buf ^ 1);
+            } else if (more) {               // the next tile's first step, before this one is stored
+                aim(t + gridDim.x);
+                next_scales = load_scales(0);
+                copy(0, buf ^ 1);
+            }
+            fetch(buf, 1, v[1]);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(v[0], std::integral_constant<int, 0>{});
+            fetch(buf, 2, v[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(v[1], std::integral_constant<int, 1>{});
+            if (!(half_end && last)) {
+                fetch(buf, 3, v[1]);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(v[0], std::integral_constant<int, 2>{});
+                multiply(v[1], std::integral_constant<int, 3>{});
+            }
+            if ((k & 1) || last) set ^= 1;
+        }
+        if (more) store_scales(set, next_scales);
+        __syncthreads();                     // the last step's buffer is free
+
+        // Block element e of a lane is m = lane % 32, n = 8 (e / 4) +
+        // 4 (lane / 32) + e % 4: 16 bytes of a row at most, where a store of
+        // part of a line costs L2 as much as one of a whole line.  Each
+        // wavefront turns 32 rows at a time over in its part of that buffer
+        // and stores them in 16-byte pieces, whole lines of bf16.
+        constexpr int kEsz = F32 ? 4 : 2, kRowBytes = kTN * 32 * kEsz, kPitch = kRowBytes + 16;
+        static_assert(T::kWaves * 16 * kPitch <= T::kBytes, "staging");
+        uint8_t *stage = &s_buf[buf ^ 1][wave * (16 * kPitch)];
+        const int64_t n_first = tile_n0 + wn * (kTN * 32);
+#pragma unroll
+        for (int j = 0; j < 2 * kTM; ++j) {  // 16 rows: the lanes whose m is among them
+            if ((lane & 16) == (j & 1) * 16) {
+#pragma unroll
+                for (int i = 0; i < kTN; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const f32x16 &x = acc[i][j / 2];
+                        uint8_t *p = stage + (lane & 15) * kPitch + (i * 32 + 2 * e + 4 * g) * kEsz;
+                        if constexpr (F32) *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                        else *reinterpret_cast<u32x2 *>(p) = u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
+                    }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            constexpr int kPieces = kRowBytes / 16;
+#pragma unroll
+            for (int u0 = 0; u0 < 16 * kPieces; u0 += kWaveLanes) {
+                const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
+                const int64_t m = tile_m0 + (wm * kTM + j / 2) * 32 + (j & 1) * 16 + r;
+                const int64_t n = n_first + c * (16 / kEsz);
+                if (u < 16 * kPieces && m < a.rows && n < b.rows) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + c * 16);
+                    uint8_t *o = out + m * row_bytes + n * kEsz;
+                    if (VEC && n + 16 / kEsz <= b.rows) {
+                        *reinterpret_cast<u32x4 *>(o) = w;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 16 / kEsz; ++x) {
+                            if (n + x >= b.rows) break;
+                            if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
+                            else reinterpret_cast<uint16_t *>(o)[x] = static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
+                        }
+                    }
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        if (!more) return;
+        t += gridDim.x;
+    }
+}
+
+// out = 0, for a product over nothing.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads)
+mx_zero_kernel(int64_t rows, int64_t cols, uint8_t *__restrict__ out, int64_t row_bytes)
+{
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < rows * cols;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        uint8_t *o = out + i / cols * row_bytes;
+        if constexpr (F32) reinterpret_cast<float *>(o)[i % cols] = 0.0f;
+        else reinterpret_cast<uint16_t *>(o)[i % cols] = 0;
     }
 }
 
@@ -734,9 +820,13 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
 {
     const uint32_t tn = static_cast<uint32_t>((b.rows + BN - 1) / BN);
     const uint32_t tm = static_cast<uint32_t>((a.rows + BM - 1) / BM);
-    const uint64_t grid = static_cast<uint64_t>(tn) * tm;
-    if (grid * (WN * WM * kWaveLanes) > UINT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((mx_tile_kernel<F32, VEC, BN, BM, WN, WM>), dim3(static_cast<unsigned>(grid)),
+    const uint64_t total = static_cast<uint64_t>(tn) * tm;
+    if (total > UINT32_MAX / 2) return hipErrorInvalidValue;
+    // as many workgroups as run at once (their LDS decides), each taking tiles
+    // in turn; a multiple of the 8 XCDs
+    constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds);
+    const unsigned grid = total < kAtOnce ? static_cast<unsigned>(total) : kAtOnce;
+    hipLaunchKernelGGL((mx_tile_kernel<F32, VEC, BN, BM, WN, WM>), dim3(grid),
                        dim3(WN * WM * kWaveLanes), 0, st, a, b, kp, tn, tm, out, row_bytes);
     return hipGetLastError();
 }
@@ -793,8 +883,14 @@ hipError_t launch_mx_product(const uint8_t *a_codes, const uint8_t *a_scales, co
     const MxIn a{a_codes, a_scales, out.rows}, b{b_codes, b_scales, out.cols};
     const int64_t kp = mx_padded(inner), row_bytes = out.row_stride * (out.fp32 ? 4 : 2);
     uint8_t *p = static_cast<uint8_t *>(out.data);
-    const int need = out.fp32 ? 16 : 8;
-    const bool vec = aligned_to(p, need) && row_bytes % need == 0;
+    if (inner == 0) {
+        const int64_t blocks = (out.rows * out.cols + kThreads - 1) / kThreads;
+        const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)));
+        if (out.fp32) hipLaunchKernelGGL(mx_zero_kernel<true>, grid, dim3(kThreads), 0, st, out.rows, out.cols, p, row_bytes);
+        else hipLaunchKernelGGL(mx_zero_kernel<false>, grid, dim3(kThreads), 0, st, out.rows, out.cols, p, row_bytes);
+        return hipGetLastError();
+    }
+    const bool vec = aligned_to(p, 16) && row_bytes % 16 == 0;
     if (out.fp32) return vec ? product_type<true, true>(a, b, kp, p, row_bytes, st)
                              : product_type<true, false>(a, b, kp, p, row_bytes, st);
     return vec ? product_type<false, true>(a, b, kp, p, row_bytes, st)
