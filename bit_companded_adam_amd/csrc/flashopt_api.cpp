@@ -640,9 +640,9 @@ flashopt_status check_codes(const void *codes, const void *scales, int64_t rows,
     return aligned(codes, 16) && aligned(scales, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
 }
 
-// Most elements that a product sums over: its kernels address 256 rows of
-// codes with 32-bit offsets.
-constexpr int64_t kMaxInner = int64_t{1} << 25;
+// Most elements that a product sums over: its kernels multiply rows of a tile
+// by a row's bytes of codes in 24 bits.
+constexpr int64_t kMaxInner = (int64_t{1} << 25) - 128;
 
 // Workgroups of a quantization: tiles of 128 rows by 256 columns, whose
 // work-items a dispatch counts in 32 bits.

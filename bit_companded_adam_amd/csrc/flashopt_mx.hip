@@ -515,8 +515,26 @@ mx_skinny_kernel(MxIn a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t 
 // lines an instruction, and set the time: 8192^3 took 485 us.)  The four that
 // a lane needs of a step's eight (groups 2 k + lane / 32) are gathered into
 // one word with a byte permutation, and the instruction selects its byte.
-typedef __attribute__((address_space(1))) const uint8_t g_u8;
 typedef __attribute__((address_space(3))) uint8_t l_u8;
+
+// 16 bytes a lane from base + offset to LDS, the lanes' in order from byte
+// `to` on.  Written out because the compiler, which cannot tell the buffers
+// apart, would wait for the copy before any read of LDS; it has no register
+// result, and the kernel waits for it (vmcnt 0) ahead of the barrier that
+// publishes it.  M0 holds the LDS address; nothing else in a kernel that calls
+// this uses it (it is a reserved register, which an asm cannot name as
+// clobbered).
+__device__ __forceinline__ uint32_t lds_offset(const void *p)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((l_u8 *)p));
+}
+__device__ __forceinline__ void load_to_lds(const uint8_t *base, uint32_t offset, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(offset), "s"(base)
+                 : "memory");
+}
 
 template <int BN, int BM, int WN, int WM>
 struct Tile {
@@ -525,10 +543,20 @@ struct Tile {
     static constexpr int kRows = BN + BM;                  // rows of B, then of A
     static constexpr int kBytes = kRows * 128;             // one buffer
     static constexpr int kCopies = kRows / 8 / kWaves;     // DMA instructions of a wavefront and step
-    static constexpr int kLds = 2 * kBytes + 2 * kRows * 16;
     static constexpr int kTN = BN / WN / 32, kTM = BM / WM / 32;
+    // as LDS allows; the compiler keeps accumulators out of the AGPRs (moves
+    // around each pinned product) where it is held to this
+    static constexpr int kWavesPerSimd = BN * BM >= 128 * 128 ? 2 : 4;
+    // a wavefront's turned-over rows of out: so many at a time, 16 bytes of
+    // padding to a row
+    static constexpr int kStageRows(bool f32) { return f32 ? 4 : 8; }
+    static constexpr int kPitch(bool f32) { return kTN * 32 * (f32 ? 4 : 2) + 16; }
+    static constexpr int kLds(bool f32)
+    {
+        return 2 * kBytes + 2 * kRows * 16 + kWaves * kStageRows(f32) * kPitch(f32);
+    }
     static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 &&
-                      kRows <= kTileThreads, "tile");
+                      kRows <= kTileThreads && BN % (8 * kCopies) == 0 && BN % kWaveLanes == 0, "tile");
 };
 
 // Tile number t of a launch: neighbours on one XCD take neighbouring tiles,
@@ -548,6 +576,7 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_n, uint32_t t
 
 template <bool F32, bool VEC, int BN, int BM, int WN, int WM>
 __global__ void __launch_bounds__(WN *WM *kWaveLanes)
+    __attribute__((amdgpu_waves_per_eu(Tile<BN, BM, WN, WM>::kWavesPerSimd)))
 mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, uint8_t *__restrict__ out,
                int64_t row_bytes)
 {
@@ -555,6 +584,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
     constexpr int kTN = T::kTN, kTM = T::kTM;
     __shared__ __align__(128) uint8_t s_buf[2][T::kBytes];
     __shared__ u32x4 s_scales[2][T::kRows];
+    __shared__ __align__(16) uint8_t s_stage[T::kWaves][T::kStageRows(F32) * T::kPitch(F32)];
     const int lane = threadIdx.x & (kWaveLanes - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int wn = wave % WN, wm = wave / WN, g = lane >> 5;
@@ -563,201 +593,267 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
     const bool half_end = (kp & 128) != 0;       // the last step has 128 elements
     const uint32_t total = tiles_n * tiles_m;
 
-    // Where the copies of a tile come from: uniform bases and 32-bit offsets
-    // of the lane (kp is at most 2^25, so 256 rows of codes span at most
-    // 4 GiB).  Rows are clamped to the matrices: a row past the end repeats
-    // the last one, unstored.
-    int64_t n0, m0;
-    const uint8_t *b_codes, *a_codes, *scale_src;
-    uint32_t src[T::kCopies];
-    auto aim = [&](uint32_t t) {
+    // The copies run two steps ahead of the products, through the tiles in
+    // turn: tile pt, step pk is copied next.  A wavefront copies rows of one
+    // matrix only, and thread t the scales of buffer row t: uniform bases, and
+    // 32-bit offsets of the lane, row x stride (24 bits each, kp being below
+    // 2^25).  Rows are clamped to the matrix: a row past the end repeats the
+    // last one, unstored.
+    uint32_t pt = blockIdx.x;
+    int pk = 0;
+    const bool copy_b = wave * (8 * T::kCopies) < BN, scale_b = wave * kWaveLanes < BN;
+    const uint8_t *copy_base = nullptr, *scale_base = nullptr;
+    uint32_t src[T::kCopies], scale_src = 0;
+    // slot s of row r holds chunk s ^ ((r / 2) & 7): for rows 0 to 7 of 16
+    // here, for rows 8 to 15 with bit 2 of the chunk turned
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;
+    auto aim = [&] {
         uint32_t tile_n, tile_m;
-        tile_at(t, tiles_n, tiles_m, tile_n, tile_m);
-        n0 = static_cast<int64_t>(tile_n) * BN;
-        m0 = static_cast<int64_t>(tile_m) * BM;
-        b_codes = b.codes + n0 * code_stride;
-        a_codes = a.codes + m0 * code_stride;
+        tile_at(pt, tiles_n, tiles_m, tile_n, tile_m);
+        const int64_t n0 = static_cast<int64_t>(tile_n) * BN, m0 = static_cast<int64_t>(tile_m) * BM;
         const int n_last = static_cast<int>(b.rows - n0 < BN ? b.rows - n0 : BN) - 1;
         const int m_last = static_cast<int>(a.rows - m0 < BM ? a.rows - m0 : BM) - 1;
+        copy_base = copy_b ? b.codes + n0 * code_stride : a.codes + m0 * code_stride;
+        scale_base = scale_b ? b.scales + n0 * scale_stride : a.scales + m0 * scale_stride;
+        const int copy_last = copy_b ? n_last : m_last, scale_last = scale_b ? n_last : m_last;
+        const int first = wave * (8 * T::kCopies) - (copy_b ? 0 : BN) + (lane >> 3);
 #pragma unroll
         for (int i = 0; i < T::kCopies; ++i) {
-            const int first = (wave * T::kCopies + i) * 8, r = (first < BN ? first : first - BN) + (lane >> 3);
-            const int last = first < BN ? n_last : m_last;
-            src[i] = static_cast<uint32_t>(r < last ? r : last) * code_stride;
+            const int r = first + 8 * i;
+            src[i] = __umul24(r < copy_last ? r : copy_last, code_stride) + (chunk ^ ((i & 1) * 64u));
         }
-        // thread t carries the scales of buffer row t
-        const bool of_b = threadIdx.x < BN;
-        const int r = of_b ? threadIdx.x : threadIdx.x - BN, last = of_b ? n_last : m_last;
-        scale_src = (of_b ? b.scales + n0 * scale_stride : a.scales + m0 * scale_stride) +
-                    static_cast<uint32_t>(r < last ? r : last) * scale_stride;
+        const int r = static_cast<int>(threadIdx.x) - (scale_b ? 0 : BN);
+        scale_src = __umul24(r < scale_last ? r : scale_last, scale_stride);
     };
-    // slot s of row r holds chunk s ^ ((r / 2) & 7): for rows 0 to 7 of a
-    // copy's 16 here, for rows 8 to 15 with bit 2 of the chunk turned
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;
-    auto copy = [&](int k, int buf) {
-        // the second half of a half step repeats the first: it is not used
-        const bool half = half_end && k == steps - 1;
-#pragma unroll
-        for (int i = 0; i < T::kCopies; ++i) {
-            const int first = (wave * T::kCopies + i) * 8;
-            const uint8_t *base = (first < BN ? b_codes : a_codes) + static_cast<int64_t>(k) * 128;
-            const uint32_t at = half ? (chunk & 48u) : (chunk ^ ((first & 8) * 8u));
-            uint8_t *l = &s_buf[buf][first * 128];
-            __builtin_amdgcn_global_load_lds((g_u8 *)(base + (src[i] + at)), (l_u8 *)l, 16, 0, 0);
-        }
-    };
-    // the scales of steps 2 p and 2 p + 1: 16 bytes of a row, or what is left
-    auto load_scales = [&](int p) {
-        u32x4 v{0u, 0u, 0u, 0u};
-        if (threadIdx.x < T::kRows) {
-            const uint32_t at = static_cast<uint32_t>(p) * 16u;
-            if (at + 16u <= scale_stride) {
-                v = *reinterpret_cast<const u32x4_packed *>(scale_src + at);
-            } else {
-#pragma unroll
-                for (uint32_t w = 0; w < 3; ++w)
-                    if (at + 4 * w < scale_stride) v[w] = *reinterpret_cast<const uint32_t *>(scale_src + at + 4 * w);
-            }
-        }
-        return v;
-    };
-    auto store_scales = [&](int set, u32x4 v) {
-        if (threadIdx.x < T::kRows) s_scales[set][threadIdx.x] = v;
+    const uint32_t lds_to = lds_offset(s_buf) + wave * (T::kCopies * 1024);
+    // Copy i of step pk into a buffer.  In a half step the second half of a
+    // row, not used then, repeats the first.
+    auto copy = [&](int i, int buf) {
+        const bool half = half_end && pk == steps - 1;
+        const uint32_t back = half ? ((chunk ^ ((i & 1) * 64u)) & 64u) : 0u;
+        load_to_lds(copy_base, src[i] - back, lds_to + buf * T::kBytes + i * 1024);
     };
     const uint32_t gather = g ? 0x07050301u : 0x06040200u;
-    auto scale_word = [&](int set, int k, int row) {
-        const u32x2 v = *(reinterpret_cast<const u32x2 *>(&s_scales[set][row]) + (k & 1));
-        return __builtin_amdgcn_perm(v.y, v.x, gather);
+    auto scale_bytes = [&](int set, int k, int row) {
+        return *(reinterpret_cast<const u32x2 *>(&s_scales[set][row]) + (k & 1));
     };
 
-    uint32_t off[4];             // this lane's chunk of each quarter step
-#pragma unroll
-    for (int q = 0; q < 4; ++q) off[q] = (lane & 31) * 128 + (((2 * q + g) ^ ((lane >> 1) & 7)) << 4);
+    // this lane's chunk of the first quarter step; of quarter q: ^ 32 q
+    const uint32_t off = (lane & 31) * 128 + ((g ^ ((lane >> 1) & 7)) << 4);
     struct Operands {
         u32x4 n[kTN], m[kTM];
     };
     auto fetch = [&](int buf, int q, Operands &v) {
+        const uint32_t at = off ^ (32 * q);
 #pragma unroll
         for (int i = 0; i < kTN; ++i)
-            v.n[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * kTN + i) * 4096 + off[q]]);
+            v.n[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * kTN + i) * 4096 + at]);
 #pragma unroll
         for (int i = 0; i < kTM; ++i)
-            v.m[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * kTM + i) * 4096 + off[q]]);
+            v.m[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * kTM + i) * 4096 + at]);
     };
 
     f32x16 acc[kTN][kTM];
     uint32_t sn[kTN], sm[kTM];
-    auto multiply = [&](const Operands &v, auto quarter) {
-        constexpr int q = decltype(quarter)::value;
+    // One quarter's products; with COPY, the copies of step pk are issued
+    // between them, where they cost nothing.  Each block is pinned in its
+    // place: the compiler would sink products past the barrier and the
+    // branches after it, and hold all four quarters' operands.
+    auto multiply = [&](const Operands &v, auto quarter, auto with_copy, int to) {
+        constexpr int q = decltype(quarter)::value, kBlocks = kTN * kTM;
 #pragma unroll
-        for (int i = 0; i < kTN; ++i)
+        for (int x = 0; x < kBlocks; ++x) {
+            const int i = x / kTM, j = x % kTM;
+            acc[i][j] = mfma32<q>(v.n[i], v.m[j], acc[i][j], sn[i], sm[j]);
+            asm volatile("" : "+v"(acc[i][j]));
+            if constexpr (decltype(with_copy)::value) {
 #pragma unroll
-            for (int j = 0; j < kTM; ++j) acc[i][j] = mfma32<q>(v.n[i], v.m[j], acc[i][j], sn[i], sm[j]);
+                for (int c = x * T::kCopies / kBlocks; c < (x + 1) * T::kCopies / kBlocks; ++c) copy(c, to);
+            }
+        }
+    };
+    constexpr std::integral_constant<int, 0> q0{};
+    constexpr std::integral_constant<int, 1> q1{};
+    constexpr std::integral_constant<int, 2> q2{};
+    constexpr std::integral_constant<int, 3> q3{};
+    constexpr std::true_type with_copies{};
+    constexpr std::false_type alone{};
+
+    // After the copies of step pk: with the first of two steps, the scales of
+    // both go to a register (16 bytes, from a window that ends with the row, so
+    // nothing past it is read), and half a step on settle() moves them to LDS
+    // and back to their place.  Rows of less than 16 bytes, products over less
+    // than 512 elements, go there at once.  Past the last tile its last copies
+    // are repeated, unused.
+    u32x4 next_scales{0u, 0u, 0u, 0u};
+    uint32_t shift = 0;
+    bool pending = false;
+    int pset = 1, set = 0;       // sets of scales: the last one filled, the one in use
+    auto advance = [&] {
+        if (!(pk & 1)) {
+            pset ^= 1;
+            const uint8_t *row = scale_base + scale_src;
+            if (scale_stride >= 16u) {
+                const uint32_t at = static_cast<uint32_t>(pk) * 8u, end = scale_stride - 16u;
+                const uint32_t from = at < end ? at : end;
+                if (T::kRows == T::kTileThreads || threadIdx.x < T::kRows)
+                    next_scales = *reinterpret_cast<const u32x4_packed *>(row + from);
+                shift = (at - from) / 4u;
+                pending = true;
+            } else if (threadIdx.x < T::kRows) {
+                for (uint32_t w = 0; w < 16; w += 4)
+                    reinterpret_cast<uint32_t *>(&s_scales[pset][threadIdx.x])[w / 4] =
+                        w < scale_stride ? *reinterpret_cast<const uint32_t *>(row + w) : 0u;
+            }
+        }
+        copy_base += 128;
+        if (++pk == steps) {
+            if (pt + gridDim.x < total) {
+                pk = 0;
+                pt += gridDim.x;
+                aim();
+            } else {
+                --pk;
+                copy_base -= 128;
+            }
+        }
+    };
+    auto settle = [&] {
+        if (!pending) return;
+        u32x4 v = next_scales;
+        if (shift & 1) v = u32x4{v.y, v.z, v.w, v.w};
+        if (shift & 2) v = u32x4{v.z, v.w, v.w, v.w};
+        if (threadIdx.x < T::kRows) s_scales[pset][threadIdx.x] = v;
+        pending = false;
     };
 
     uint32_t t = blockIdx.x;
     if (t >= total) return;
-    aim(t);
-    int buf = 0, set = 0;        // the buffers of the step and of its scales
-    store_scales(0, load_scales(0));
-    copy(0, 0);
-    while (true) {
-        const int64_t tile_n0 = n0, tile_m0 = m0;
-        const bool more = t + gridDim.x < total;
+    aim();
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) copy(i, 0);
+    advance();
+    settle();
+    __builtin_amdgcn_s_waitcnt(0);       // this wavefront's copies have reached LDS
+    __syncthreads();                     // everyone's have
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) copy(i, 1);
+    advance();
+    Operands v[2];
+    fetch(0, 0, v[0]);
+    u32x2 next_n[kTN], next_m[kTM];      // scales of the step to come
+    auto fetch_scales = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < kTN; ++i) next_n[i] = scale_bytes(set, k, (wn * kTN + i) * 32 + (lane & 31));
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) next_m[i] = scale_bytes(set, k, BN + (wm * kTM + i) * 32 + (lane & 31));
+    };
+    fetch_scales(0);
+    int buf = 0;
+    for (; t < total; t += gridDim.x) {
 #pragma unroll
         for (int i = 0; i < kTN; ++i)
 #pragma unroll
             for (int j = 0; j < kTM; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-        u32x4 next_scales{0u, 0u, 0u, 0u};
+        // Each step starts with its first quarter and scales in registers.
+        // Half way through, its buffer has been read by everyone and the next
+        // one has landed: the only barrier, after which the copy two steps on
+        // starts and the next step's first quarter is fetched under the
+        // remaining products.
         for (int k = 0; k < steps; ++k, buf ^= 1) {
-            __builtin_amdgcn_s_waitcnt(0);   // this wavefront's copies have reached LDS
-            __syncthreads();                 // everyone's have, and the other buffers are free
-            Operands v[2];
-            fetch(buf, 0, v[0]);
 #pragma unroll
-            for (int i = 0; i < kTN; ++i) sn[i] = scale_word(set, k, (wn * kTN + i) * 32 + (lane & 31));
+            for (int i = 0; i < kTN; ++i) sn[i] = __builtin_amdgcn_perm(next_n[i].y, next_n[i].x, gather);
 #pragma unroll
-            for (int i = 0; i < kTM; ++i) sm[i] = scale_word(set, k, BN + (wm * kTM + i) * 32 + (lane & 31));
+            for (int i = 0; i < kTM; ++i) sm[i] = __builtin_amdgcn_perm(next_m[i].y, next_m[i].x, gather);
             const bool last = k == steps - 1;
-            if ((k & 1) && !last) store_scales(set ^ 1, next_scales);
-            if (!last) {
-                if (!(k & 1) && k + 2 < steps) next_scales = load_scales((k >> 1) + 1);
-                copy(k + 1, buf ^ 1);
-            } else if (more) {               // the next tile's first step, before this one is stored
-                aim(t + gridDim.x);
-                next_scales = load_scales(0);
-                copy(0, buf ^ 1);
-            }
+            // a half step's second half counts as zeros (a branch around its
+            // products would double the accumulators)
+            const uint32_t second = half_end && last ? 0u : 0xFFFFFFFFu;
             fetch(buf, 1, v[1]);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(v[0], std::integral_constant<int, 0>{});
+            multiply(v[0], q0, alone, 0);
             fetch(buf, 2, v[0]);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(v[1], std::integral_constant<int, 1>{});
-            if (!(half_end && last)) {
-                fetch(buf, 3, v[1]);
-                __builtin_amdgcn_sched_barrier(0);
-                multiply(v[0], std::integral_constant<int, 2>{});
-                multiply(v[1], std::integral_constant<int, 3>{});
-            }
+            multiply(v[1], q1, alone, 0);
+            fetch(buf, 3, v[1]);
+            __builtin_amdgcn_s_waitcnt(0);
+            settle();
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) v[0].n[i] &= second;
+            multiply(v[0], q2, with_copies, buf);
+            advance();
             if ((k & 1) || last) set ^= 1;
+            fetch(buf ^ 1, 0, v[0]);
+            fetch_scales(last ? 0 : k + 1);
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) v[1].n[i] &= second;
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(v[1], q3, alone, 0);
         }
-        if (more) store_scales(set, next_scales);
-        __syncthreads();                     // the last step's buffer is free
 
         // Block element e of a lane is m = lane % 32, n = 8 (e / 4) +
         // 4 (lane / 32) + e % 4: 16 bytes of a row at most, where a store of
         // part of a line costs L2 as much as one of a whole line.  Each
-        // wavefront turns 32 rows at a time over in its part of that buffer
-        // and stores them in 16-byte pieces, whole lines of bf16.
-        constexpr int kEsz = F32 ? 4 : 2, kRowBytes = kTN * 32 * kEsz, kPitch = kRowBytes + 16;
-        static_assert(T::kWaves * 16 * kPitch <= T::kBytes, "staging");
-        uint8_t *stage = &s_buf[buf ^ 1][wave * (16 * kPitch)];
-        const int64_t n_first = tile_n0 + wn * (kTN * 32);
+        // wavefront turns a few rows at a time over in LDS of its own and
+        // stores them in 16-byte pieces, whole lines of bf16; the next tile's
+        // copies run meanwhile.
+        constexpr int kEsz = F32 ? 4 : 2, kRowBytes = kTN * 32 * kEsz, kPitch = T::kPitch(F32);
+        constexpr int kR = T::kStageRows(F32), kPieces = kRowBytes / 16;
+        uint32_t tile_n, tile_m;
+        tile_at(t, tiles_n, tiles_m, tile_n, tile_m);
+        const int64_t m_first = static_cast<int64_t>(tile_m) * BM + wm * (kTM * 32);
+        const int64_t n_first = static_cast<int64_t>(tile_n) * BN + wn * (kTN * 32);
+        uint8_t *stage = s_stage[wave];
 #pragma unroll
-        for (int j = 0; j < 2 * kTM; ++j) {  // 16 rows: the lanes whose m is among them
-            if ((lane & 16) == (j & 1) * 16) {
+        for (int j = 0; j < kTM; ++j) {
 #pragma unroll
-                for (int i = 0; i < kTN; ++i)
+            for (int r0 = 0; r0 < 32; r0 += kR) {
+                if ((lane & (32 - kR)) == r0) {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const f32x16 &x = acc[i][j / 2];
-                        uint8_t *p = stage + (lane & 15) * kPitch + (i * 32 + 2 * e + 4 * g) * kEsz;
-                        if constexpr (F32) *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
-                        else *reinterpret_cast<u32x2 *>(p) = u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
-                    }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            constexpr int kPieces = kRowBytes / 16;
+                    for (int i = 0; i < kTN; ++i)
 #pragma unroll
-            for (int u0 = 0; u0 < 16 * kPieces; u0 += kWaveLanes) {
-                const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
-                const int64_t m = tile_m0 + (wm * kTM + j / 2) * 32 + (j & 1) * 16 + r;
-                const int64_t n = n_first + c * (16 / kEsz);
-                if (u < 16 * kPieces && m < a.rows && n < b.rows) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + c * 16);
-                    uint8_t *o = out + m * row_bytes + n * kEsz;
-                    if (VEC && n + 16 / kEsz <= b.rows) {
-                        *reinterpret_cast<u32x4 *>(o) = w;
-                    } else {
+                        for (int e = 0; e < 16; e += 4) {
+                            const f32x16 &x = acc[i][j];
+                            uint8_t *p = stage + (lane & (kR - 1)) * kPitch + (i * 32 + 2 * e + 4 * g) * kEsz;
+                            if constexpr (F32)
+                                *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                            else
+                                *reinterpret_cast<u32x2 *>(p) =
+                                    u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
+                        }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                        for (int x = 0; x < 16 / kEsz; ++x) {
-                            if (n + x >= b.rows) break;
-                            if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
-                            else reinterpret_cast<uint16_t *>(o)[x] = static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
+                for (int u0 = 0; u0 < kR * kPieces; u0 += kWaveLanes) {
+                    const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
+                    const int64_t m = m_first + j * 32 + r0 + r, n = n_first + c * (16 / kEsz);
+                    if (u < kR * kPieces && m < a.rows && n < b.rows) {
+                        const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + c * 16);
+                        uint8_t *o = out + m * row_bytes + n * kEsz;
+                        if (VEC && n + 16 / kEsz <= b.rows) {
+                            *reinterpret_cast<u32x4 *>(o) = w;
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 16 / kEsz; ++x) {
+                                if (n + x >= b.rows) break;
+                                if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
+                                else
+                                    reinterpret_cast<uint16_t *>(o)[x] =
+                                        static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
+                            }
                         }
                     }
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
         }
-        if (!more) return;
-        t += gridDim.x;
     }
+    __builtin_amdgcn_s_waitcnt(0);       // no copy outlives the workgroup's LDS
 }
 
 // out = 0, for a product over nothing.
@@ -824,7 +920,7 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
     if (total > UINT32_MAX / 2) return hipErrorInvalidValue;
     // as many workgroups as run at once (their LDS decides), each taking tiles
     // in turn; a multiple of the 8 XCDs
-    constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds);
+    constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds(F32));
     const unsigned grid = total < kAtOnce ? static_cast<unsigned>(total) : kAtOnce;
     hipLaunchKernelGGL((mx_tile_kernel<F32, VEC, BN, BM, WN, WM>), dim3(grid),
                        dim3(WN * WM * kWaveLanes), 0, st, a, b, kp, tn, tm, out, row_bytes);

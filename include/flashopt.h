@@ -522,7 +522,7 @@ flashopt_status flashopt_mx_dequantize(const void *codes, const void *scales, in
  *   y  = product(x, w)          groups along k
  *   dx = product(dy, w_t)       w_t: w's transposed codes, groups along n
  *   dw = product(dy_t, x_t)     groups along m
- * Errors: EINVAL (sizes, k above 2^25, out_fp32, row_stride < n, NULL), EALIGN,
+ * Errors: EINVAL (sizes, k above 2^25 - 128, out_fp32, row_stride < n, NULL), EALIGN,
  * EHIP. */
 flashopt_status flashopt_mx_product(const void *a_codes, const void *a_scales,
                                     const void *b_codes, const void *b_scales, int64_t m,

@@ -59,7 +59,7 @@ def test_product_refuses(L):
     def p(a=A, sa=A, b=A, sb=A, m=4, n=5, k=40, out=A, wide=0, stride=5):
         return L.flashopt_mx_product(a, sa, b, sb, m, n, k, out, wide, stride, None)
     assert p(m=0, out=None) == OK and p(n=0, out=None) == OK
-    for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(m=BIG), dict(n=BIG, stride=BIG), dict(k=BIG), dict(k=(1 << 25) + 1),
+    for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(m=BIG), dict(n=BIG, stride=BIG), dict(k=BIG), dict(k=(1 << 25) - 127),
                 dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(out=None), dict(wide=2),
                 dict(stride=4)):
         assert p(**bad) == EINVAL, bad
