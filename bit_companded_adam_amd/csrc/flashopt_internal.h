@@ -185,6 +185,11 @@ hipError_t launch_mx_quantize(const MxMatrix &x, uint8_t *codes, uint8_t *scales
                               uint8_t *scales_t, hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, const MxMatrix &out,
                                 hipStream_t stream);
+// x w^T in one launch, x quantized inside it: whether x allows it (a few
+// aligned rows of bf16), and the launch.
+bool mx_linear_direct(const MxMatrix &x);
+hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
+                                   const MxMatrix &out, hipStream_t stream);
 // out = A B^T with A of out.rows and B of out.cols rows.
 hipError_t launch_mx_product(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *b_codes,
                              const uint8_t *b_scales, int64_t inner, const MxMatrix &out,

@@ -420,8 +420,8 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa
 // Within a step a lane holds groups 2 g and 2 g + 1 of its row (g = lane / 16):
 // 32 consecutive bytes, and any assignment of groups to the instruction's
 // four K slots is the same sum as long as both operands and their scales
-// agree.
-constexpr int kSkinnyWaves = kThreads / kWaveLanes;
+// agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.
+constexpr int kSkinnyWaves = 8;
 
 struct Step {
     u32x4 lo, hi;
@@ -440,14 +440,68 @@ __device__ __forceinline__ Step load_step(const MxIn &in, int64_t row, int64_t k
     return s;
 }
 
-template <bool F32, bool VEC, int MT, int NT>
-__global__ void __launch_bounds__(kThreads)
-mx_skinny_kernel(MxIn a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row_bytes)
+// A's rows as they come, in bf16, 16-byte aligned and of whole 16-byte pieces:
+// a lane's two groups are 64 elements of its own, so they are quantized where
+// they are used (as mx_quantize_kernel does, bit for bit).  Every workgroup
+// does it again: worth it while A is a few rows.
+struct MxRaw {
+    const uint8_t *data;
+    int64_t rows, row_bytes, cols;
+};
+
+// The codes of the 32 elements at p, of which `count` exist, and their scale.
+__device__ __forceinline__ u32x4 quantize_group(const uint8_t *p, int64_t count, uint32_t &byte)
+{
+    u32x4 w[4], q;
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = u32x4{0u, 0u, 0u, 0u};
+        if (i * 8 < count) w[i] = *reinterpret_cast<const u32x4 *>(p + i * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = max_u16(top, w[i][x] & 0x7FFF7FFFu);
+    top = umax32(top, top << 16);
+    const uint32_t scale = scale_bits(top);
+    byte = scale >> 23;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t c = codes2<0>(0u, w[i].x, scale);
+        c = codes2<1>(c, w[i].y, scale);
+        c = codes2<2>(c, w[i].z, scale);
+        q[i] = codes2<3>(c, w[i].w, scale);
+    }
+    if (top >= kExponent) {
+        byte = 255u;
+        q = u32x4{0u, 0u, 0u, 0u};
+    }
+    return q;
+}
+
+__device__ __forceinline__ Step load_step(const MxRaw &in, int64_t row, int64_t, int64_t group)
+{
+    const int64_t first = group * 32;
+    const uint8_t *p = in.data + row * in.row_bytes + first * 2;
+    uint32_t lo, hi;
+    Step s;
+    s.lo = quantize_group(p, in.cols - first, lo);
+    s.hi = quantize_group(p + 64, in.cols - first - 32, hi);
+    s.scale = lo | (hi << 8);
+    return s;
+}
+
+template <bool F32, bool VEC, int MT, int NT, typename A>
+__global__ void __launch_bounds__(kSkinnyWaves *kWaveLanes)
+mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row_bytes)
 {
     __shared__ f32x4 s_acc[kSkinnyWaves][NT][MT][kWaveLanes];
-    const int lane = threadIdx.x & (kWaveLanes - 1), wave = threadIdx.x / kWaveLanes;
+    const int lane = threadIdx.x & (kWaveLanes - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int l16 = lane & 15, g = lane >> 4;
-    const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT), steps = (kp + 255) / 256;
+    const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT);
+    const int steps = static_cast<int>((kp + 255) / 256);
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t n0 = tile * (16 * NT);
         int64_t brow[NT], arow[MT];
@@ -466,12 +520,13 @@ mx_skinny_kernel(MxIn a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t 
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int64_t k = wave; k < steps; k += kSkinnyWaves) {
+        for (int k = wave; k < steps; k += kSkinnyWaves) {
+            const int64_t group = static_cast<int64_t>(k) * 8 + 2 * g;
             Step sb[NT], sa[MT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) sb[i] = load_step(b, brow[i], kp, k * 8 + 2 * g);
+            for (int i = 0; i < NT; ++i) sb[i] = load_step(b, brow[i], kp, group);
 #pragma unroll
-            for (int j = 0; j < MT; ++j) sa[j] = load_step(a, arow[j], kp, k * 8 + 2 * g);
+            for (int j = 0; j < MT; ++j) sa[j] = load_step(a, arow[j], kp, group);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -901,13 +956,13 @@ hipError_t quantize_type(const MxMatrix &x, uint8_t *codes, uint8_t *scales, uin
     return quantize_layout<F32, false, true>(x, codes, scales, codes_t, scales_t, st);
 }
 
-template <bool F32, bool VEC, int MT, int NT>
-hipError_t skinny(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes, hipStream_t st)
+template <bool F32, bool VEC, int MT, int NT, typename A>
+hipError_t skinny(const A &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes, hipStream_t st)
 {
     const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT);
     const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
-    hipLaunchKernelGGL((mx_skinny_kernel<F32, VEC, MT, NT>), dim3(grid), dim3(kThreads), 0, st, a, b, kp, out,
-                       row_bytes);
+    hipLaunchKernelGGL((mx_skinny_kernel<F32, VEC, MT, NT, A>), dim3(grid),
+                       dim3(kSkinnyWaves * kWaveLanes), 0, st, a, b, kp, out, row_bytes);
     return hipGetLastError();
 }
 
@@ -927,12 +982,22 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
     return hipGetLastError();
 }
 
+// Rows of B up to which a skinny product gives a workgroup 16 of them: fewer
+// workgroups than that would leave CUs idle.  Above it they read A often
+// enough to share it among 32 or, with more than four rows of A, 64.  (M x N
+// x K in us, 16 / 32 / 64 rows of B: 1 x 4096 x 4096 4.4 / 6.2 / 8.9; 1 x
+// 14336 x 4096 10.0 / 9.5 / 9.3; 16 x 14336 x 4096 14.0 / 11.5 / 10.4.)
+constexpr int64_t kNarrow = 8192;
+
 template <bool F32, bool VEC>
 hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
                         hipStream_t st)
 {
-    if (a.rows <= 16) return skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
-    if (a.rows <= 32) return skinny<F32, VEC, 2, 2>(a, b, kp, out, row_bytes, st);
+    if (a.rows <= 32 && b.rows <= kNarrow)
+        return a.rows <= 16 ? skinny<F32, VEC, 1, 1>(a, b, kp, out, row_bytes, st)
+                            : skinny<F32, VEC, 2, 1>(a, b, kp, out, row_bytes, st);
+    if (a.rows <= 4) return skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
+    if (a.rows <= 16) return skinny<F32, VEC, 1, 4>(a, b, kp, out, row_bytes, st);
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
     if (big >= 200) return tiles<F32, VEC, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
@@ -940,7 +1005,38 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     return tiles<F32, VEC, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
+// Rows of A up to which the linear layer's product quantizes A itself.
+constexpr int64_t kRawRows = 4;
+
+template <bool F32, bool VEC>
+hipError_t linear_type(const MxRaw &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
+                       hipStream_t st)
+{
+    return b.rows <= kNarrow ? skinny<F32, VEC, 1, 1>(a, b, kp, out, row_bytes, st)
+                             : skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
+}
+
 }  // namespace
+
+bool mx_linear_direct(const MxMatrix &x)
+{
+    return !x.fp32 && x.rows <= kRawRows && x.cols > 0 && aligned_to(x.data, 16) && x.row_stride % 8 == 0 &&
+           x.cols % 8 == 0;
+}
+
+hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
+                                   const MxMatrix &out, hipStream_t st)
+{
+    const MxRaw a{static_cast<const uint8_t *>(x.data), x.rows, x.row_stride * 2, x.cols};
+    const MxIn b{w_codes, w_scales, out.cols};
+    const int64_t kp = mx_padded(x.cols), row_bytes = out.row_stride * (out.fp32 ? 4 : 2);
+    uint8_t *p = static_cast<uint8_t *>(out.data);
+    const bool vec = aligned_to(p, 16) && row_bytes % 16 == 0;
+    if (out.fp32) return vec ? linear_type<true, true>(a, b, kp, p, row_bytes, st)
+                             : linear_type<true, false>(a, b, kp, p, row_bytes, st);
+    return vec ? linear_type<false, true>(a, b, kp, p, row_bytes, st)
+               : linear_type<false, false>(a, b, kp, p, row_bytes, st);
+}
 
 hipError_t launch_mx_quantize(const MxMatrix &x, uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
                               uint8_t *scales_t, hipStream_t st)

@@ -262,15 +262,24 @@ def test_product_into_views():
 
 def test_linear_equals_quantize_and_product():
     require_gpu()
-    for m, n, k in ((1, 300, 500), (16, 64, 4096), (17, 40, 130), (200, 100, 64), (2100, 2048, 256)):
+    # up to four aligned rows of bf16 are quantized inside the product
+    for m, n, k in ((1, 300, 500), (1, 300, 504), (3, 9000, 4096), (4, 8200, 24), (4, 17, 264), (1, 5, 8),
+                    (16, 64, 4096), (17, 40, 130), (200, 100, 64), (2100, 2048, 256)):
         for dtype in (BF16, F32):
             x, w = _random(m, k, 1, dtype, 2), F.flashopt_mx_quantize(_random(n, k, 2, BF16, 2))
             for out in (BF16, F32):
                 y = F.flashopt_mx_linear(x, w, out)
                 assert torch.equal(y, F.flashopt_mx_product(F.flashopt_mx_quantize(x), w, out))
+    x, w = _random(2, 4096, 5, BF16), F.flashopt_mx_quantize(_random(50, 4096, 6, BF16, 2))
+    x[1, 70], x[1, 4000] = float("nan"), float("inf")
+    y = F.flashopt_mx_linear(x, w, F32)
+    assert torch.equal(y[0], F.flashopt_mx_linear(x[:1], w, F32)[0]) and torch.isnan(y[1]).all()
+    assert torch.isfinite(y[0]).all()
     wide = _random(40, 300, 3, BF16)
-    view = wide[:, 7:207]
     w = F.flashopt_mx_quantize(_random(33, 200, 4, BF16))
+    for view in (wide[:3, 8:208], wide[:3, 7:207], wide[4:5, 96:296], wide[2:3, :200].expand(4, 200)):
+        assert torch.equal(F.flashopt_mx_linear(view, w), F.flashopt_mx_linear(view.contiguous(), w))
+    view = wide[:, 7:207]
     assert torch.equal(F.flashopt_mx_linear(view, w), F.flashopt_mx_linear(view.contiguous(), w))
     with pytest.raises(ValueError, match="columns"):
         F.flashopt_mx_linear(wide, w)
