@@ -196,8 +196,8 @@ def _check(status: int, where: str):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:      # torch.cuda.current_stream().cuda_stream, without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -543,35 +543,46 @@ def flashopt_sgd_plan_launch(info: flashopt_sgd_plan_info, plan: torch.Tensor, s
 
 # --------------------------------------------- gradient norm and clipping
 
-def _stream_context(stream, device):
-    """Allocations and torch operations inside go to `stream` (None: the
-    current stream, nothing to do)."""
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Allocations, torch operations and launches inside go to `device` and
+    `stream` (None: the device's current stream)."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the input on {device}")
+    return torch.cuda.stream(stream)       # sets the stream's device as well
 
 
 def grad_array(grads):
     """(ctypes array of flashopt_grad, device) of a list of contiguous bf16
     and fp32 device tensors (device None for an empty list)."""
-    words, device = array("q"), None
-    for g in grads:
-        wide = g.dtype == torch.float32
-        if not wide and g.dtype != torch.bfloat16:
-            raise ValueError(f"gradients must be bf16 or fp32, got {g.dtype}")
-        if not g.is_cuda:
-            raise ValueError("gradients must be device tensors")
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-        if device is None:
-            device = g.device
-        elif g.device != device:
-            raise ValueError(f"all gradients must be on one device, got {device} and {g.device}")
-        words.extend((g.data_ptr(), g.numel(), int(wide)))
-    n = len(words) // 3
-    return (flashopt_grad * n).from_buffer(words) if n else (flashopt_grad * 0)(), device
+    if not grads:
+        return (flashopt_grad * 0)(), None
+    try:
+        wide = [_GRAD_FP32[g.dtype] for g in grads]
+    except KeyError as e:
+        raise ValueError(f"gradients must be bf16 or fp32, got {e.args[0]}") from None
+    devices = {g.device for g in grads}
+    device = next(iter(devices))
+    if any(d.type != "cuda" for d in devices):
+        raise ValueError("gradients must be device tensors")
+    if len(devices) > 1:
+        raise ValueError(f"all gradients must be on one device, got {sorted(map(str, devices))}")
+    if not all([g.is_contiguous() for g in grads]):
+        raise ValueError("gradients must be contiguous")
+    words = array("q", bytes(24 * len(grads)))
+    words[0::3] = array("q", [g.data_ptr() for g in grads])
+    words[1::3] = array("q", [g.numel() for g in grads])
+    words[2::3] = array("q", wide)
+    return (flashopt_grad * len(grads)).from_buffer(words), device
+
+
+_GRAD_FP32 = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def flashopt_grad_workspace_bytes(n_tensors: int) -> int:
@@ -584,40 +595,40 @@ def flashopt_grad_workspace_bytes(n_tensors: int) -> int:
 _grad_workspaces = {}
 
 
-def _grad_workspace(n: int, device, stream) -> torch.Tensor:
-    need = max(16, flashopt_grad_workspace_bytes(n))
-    with _stream_context(stream, device):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(need, dtype=torch.uint8, device=device)
-        key = (device, torch.cuda.current_stream().cuda_stream)
-        ws = _grad_workspaces.get(key)
-        if ws is None or ws.numel() < need:
-            ws = _grad_workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=device)
-        return ws
+def _grad_workspace(n: int, device) -> torch.Tensor:
+    """For the current stream."""
+    need = _GRAD_SHORT_BYTES if 0 < n <= 64 else max(16, flashopt_grad_workspace_bytes(n))
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(need, dtype=torch.uint8, device=device)
+    key = (device.index, _stream(None))
+    ws = _grad_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _grad_workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+    return ws
 
 
-def _grad_out(out, device, stream) -> torch.Tensor:
+_GRAD_SHORT_BYTES = 128 + 512 * 8       # flashopt_grad_workspace_bytes of up to 64 tensors
+
+
+def _grad_out(out, device) -> torch.Tensor:
     if out is None:
-        with _stream_context(stream, device):
-            return torch.empty(2, dtype=torch.float32, device=device)
+        return torch.empty(2, dtype=torch.float32, device=device)
     _buf(out, "out", device, (4,), 2, float32=True)
     return out
 
 
 def _grad_call(name, grads, max_norm, out, workspace, stream):
-    arr, device = grads if isinstance(grads, tuple) else grad_array(grads)
+    arr, device = grad_array(list(grads))
     if device is None:
         device = out.device if out is not None else torch.device("cuda", torch.cuda.current_device())
-    dev = getattr(stream, "device", None)
-    if dev is not None and dev != device:
-        raise ValueError(f"stream is on {dev}, the gradients on {device}")
-    with torch.cuda.device(device):
-        out = _grad_out(out, device, stream)
-        ws = _grad_workspace(len(arr), device, stream) if workspace is None else workspace
+    with _on(device, stream):
+        out = _grad_out(out, device)
+        ws = _grad_workspace(len(arr), device) if workspace is None else workspace
         if ws.device != device:
             raise ValueError(f"workspace is on {ws.device}, the gradients on {device}")
-        _check(getattr(lib(), name)(arr, len(arr), max_norm, out.data_ptr(), _dev(ws, "workspace"),
-                                    ws.numel() * ws.element_size(), _stream(stream)), name)
+        status = getattr(lib(), name)(arr, len(arr), max_norm, out.data_ptr(), _dev(ws, "workspace"),
+                                      ws.numel() * ws.element_size(), _stream(None))
+    _check(status, name)
     return out
 
 
@@ -671,21 +682,21 @@ class GradPlan:
         self.grads = list(grads)
         arr, device = grad_array(self.grads)
         self.device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-        with torch.cuda.device(self.device), _stream_context(stream, self.device):
+        with _on(self.device, stream):
             self.buffer = torch.empty(max(16, flashopt_grad_plan_bytes(len(arr))), dtype=torch.uint8,
                                       device=self.device)
-            self.info = flashopt_grad_plan(arr, self.buffer, stream)
+            self.info = flashopt_grad_plan(arr, self.buffer)
 
     def norm(self, max_norm: float = float("inf"), out=None, stream=None) -> torch.Tensor:
-        with torch.cuda.device(self.device):
-            out = _grad_out(out, self.device, stream)
-            flashopt_grad_plan_norm(self.info, self.buffer, max_norm, out, stream)
+        with _on(self.device, stream):
+            out = _grad_out(out, self.device)
+            flashopt_grad_plan_norm(self.info, self.buffer, max_norm, out)
         return out
 
     def clip(self, max_norm: float, out=None, stream=None) -> torch.Tensor:
-        with torch.cuda.device(self.device):
-            out = _grad_out(out, self.device, stream)
-            flashopt_grad_plan_clip(self.info, self.buffer, max_norm, out, stream)
+        with _on(self.device, stream):
+            out = _grad_out(out, self.device)
+            flashopt_grad_plan_clip(self.info, self.buffer, max_norm, out)
         return out
 
 
@@ -1012,7 +1023,7 @@ class MXTensor:
     """A rows x cols matrix in MXFP4: uint8 tensors of packed codes (two to a
     byte, rows padded to 128 elements) and of E8M0 scales (one for 32)."""
 
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("rows", "cols", "device", "code_ptr", "scale_ptr", "_codes", "_scales", "_buffer")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         blocks = rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
@@ -1023,17 +1034,37 @@ class MXTensor:
                 raise ValueError(f"{name} holds {t.numel()} bytes, {blocks * each} needed")
         if codes.device != scales.device:
             raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        self.code_ptr, self.scale_ptr = codes.data_ptr(), scales.data_ptr()
+        self._codes, self._scales, self._buffer = codes, scales, None
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "MXTensor":
-        blocks = (cols + MX_BLOCK - 1) // MX_BLOCK
-        return MXTensor(torch.empty((rows, 64 * blocks), dtype=torch.uint8, device=device),
-                        torch.empty((rows, 4 * blocks), dtype=torch.uint8, device=device), rows, cols)
+        """Uninitialized, codes and then scales in one buffer."""
+        blocks = rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
+        return MXTensor._over(torch.empty(68 * blocks, dtype=torch.uint8, device=device), rows, cols)
+
+    @staticmethod
+    def _over(buffer: torch.Tensor, rows: int, cols: int) -> "MXTensor":
+        q = object.__new__(MXTensor)
+        q.rows, q.cols, q.device, q._buffer, q._codes, q._scales = rows, cols, buffer.device, buffer, None, None
+        q.code_ptr = buffer.data_ptr()
+        q.scale_ptr = q.code_ptr + 64 * rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
+        return q
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            width = 64 * ((self.cols + MX_BLOCK - 1) // MX_BLOCK)
+            self._codes = self._buffer[:self.rows * width].view(self.rows, width)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            width = 4 * ((self.cols + MX_BLOCK - 1) // MX_BLOCK)
+            self._scales = self._buffer[16 * self.rows * width:].view(self.rows, width)
+        return self._scales
 
     def __repr__(self):
         return f"MXTensor({self.rows} x {self.cols}, {self.device})"
@@ -1055,10 +1086,9 @@ def _matrix(x: torch.Tensor, name: str):
     return x.data_ptr(), int(x.dtype == torch.float32), rows, cols, stride if rows > 1 else cols
 
 
-def _same_device(device, *named):
-    for t, name in named:
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the input on {device}")
+def _same_device(device, t, name):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the input on {device}")
 
 
 def _out_matrix(out, rows, cols, dtype, device):
@@ -1068,7 +1098,7 @@ def _out_matrix(out, rows, cols, dtype, device):
         raise ValueError(f"out must be {rows} x {cols}, got {tuple(out.shape)}")
     if rows > 1 and out.stride(0) < cols:
         raise ValueError("out's rows overlap")
-    _same_device(device, (out, "out"))
+    _same_device(device, out, "out")
     return out
 
 
@@ -1077,7 +1107,7 @@ def _mx_target(q, rows, cols, device):
         return MXTensor.empty(rows, cols, device)
     if (q.rows, q.cols) != (rows, cols):
         raise ValueError(f"out is {q.rows} x {q.cols}, {rows} x {cols} needed")
-    _same_device(device, (q.codes, "out"))
+    _same_device(device, q, "out")
     return q
 
 
@@ -1090,23 +1120,27 @@ def flashopt_mx_quantize(x: torch.Tensor, layout: str = "rows", out=None, stream
         raise ValueError("layout must be 'rows', 'cols' or 'both'")
     dev = x.device
     first, second = out if layout == "both" and out is not None else (out, out)
-    with torch.cuda.device(dev), _stream_context(stream, dev):
-        q = _mx_target(first, rows, cols, dev) if layout != "cols" else None
-        t = _mx_target(second, cols, rows, dev) if layout != "rows" else None
-        _check(lib().flashopt_mx_quantize(
-            ptr, wide, rows, cols, stride, *((q.codes.data_ptr(), q.scales.data_ptr()) if q else (None, None)),
-            *((t.codes.data_ptr(), t.scales.data_ptr()) if t else (None, None)), _stream(stream)),
-            "flashopt_mx_quantize")
+    q = t = c = sc = ct = sct = None
+    with _on(dev, stream):
+        if layout != "cols":
+            q = _mx_target(first, rows, cols, dev)
+            c, sc = q.code_ptr, q.scale_ptr
+        if layout != "rows":
+            t = _mx_target(second, cols, rows, dev)
+            ct, sct = t.code_ptr, t.scale_ptr
+        status = lib().flashopt_mx_quantize(ptr, wide, rows, cols, stride, c, sc, ct, sct, _stream(None))
+    _check(status, "flashopt_mx_quantize")
     return (q, t) if layout == "both" else (q or t)
 
 
 def flashopt_mx_dequantize(q: MXTensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an MXTensor."""
-    with torch.cuda.device(q.device), _stream_context(stream, q.device):
+    with _on(q.device, stream):
         out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
         ptr, wide, rows, cols, stride = _matrix(out, "out")
-        _check(lib().flashopt_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, ptr, wide,
-                                            stride, _stream(stream)), "flashopt_mx_dequantize")
+        status = lib().flashopt_mx_dequantize(q.code_ptr, q.scale_ptr, rows, cols, ptr, wide, stride,
+                                              _stream(None))
+    _check(status, "flashopt_mx_dequantize")
     return out
 
 
@@ -1115,13 +1149,13 @@ def flashopt_mx_product(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     dev = a.device
-    _same_device(dev, (b, "b"))
-    with torch.cuda.device(dev), _stream_context(stream, dev):
+    _same_device(dev, b, "b")
+    with _on(dev, stream):
         out = _out_matrix(out, a.rows, b.rows, dtype, dev)
         ptr, wide, m, n, stride = _matrix(out, "out")
-        _check(lib().flashopt_mx_product(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
-                                         b.scales.data_ptr(), m, n, a.cols, ptr, wide, stride,
-                                         _stream(stream)), "flashopt_mx_product")
+        status = lib().flashopt_mx_product(a.code_ptr, a.scale_ptr, b.code_ptr, b.scale_ptr, m, n, a.cols, ptr,
+                                           wide, stride, _stream(None))
+    _check(status, "flashopt_mx_product")
     return out
 
 
@@ -1136,18 +1170,19 @@ def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, works
     if k != w.cols:
         raise ValueError(f"x has {k} columns, w {w.cols}")
     dev = x.device
-    _same_device(dev, (w, "w"))
-    with torch.cuda.device(dev), _stream_context(stream, dev):
+    _same_device(dev, w, "w")
+    with _on(dev, stream):
         out = _out_matrix(out, m, w.rows, dtype or x.dtype, dev)
         optr, owide, _, n, ostride = _matrix(out, "out")
         if workspace is None:
             workspace = torch.empty(68 * m * ((k + MX_BLOCK - 1) // MX_BLOCK) + 16, dtype=torch.uint8,
                                     device=dev)
-        _same_device(dev, (workspace, "workspace"))
-        _check(lib().flashopt_mx_linear(ptr, wide, m, k, stride, w.codes.data_ptr(), w.scales.data_ptr(), n,
-                                        optr, owide, ostride, _dev(workspace, "workspace"),
-                                        workspace.numel() * workspace.element_size(), _stream(stream)),
-               "flashopt_mx_linear")
+        else:
+            _same_device(dev, workspace, "workspace")
+        status = lib().flashopt_mx_linear(ptr, wide, m, k, stride, w.code_ptr, w.scale_ptr, n, optr, owide,
+                                          ostride, _dev(workspace, "workspace"),
+                                          workspace.numel() * workspace.element_size(), _stream(None))
+    _check(status, "flashopt_mx_linear")
     return out
 
 
@@ -1191,9 +1226,9 @@ class _MXLinear(torch.autograd.Function):
         x_rows, x_cols = q if need_w else (q, None)
         ctx.weight, ctx.version = weight, None if weight is None else weight.version
         ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
+        # the transposed copies are this call's own buffers, or the MXWeight's
         ctx.kept = [None if t is None else (t.rows, t.cols) for t in (x_cols, w_cols if need_x else None)]
-        ctx.save_for_backward(*[part for t, k in zip((x_cols, w_cols), ctx.kept) if k
-                                for part in (t.codes, t.scales)])
+        ctx.save_for_backward(*[t._buffer for t, k in zip((x_cols, w_cols), ctx.kept) if k])
         y = flashopt_mx_product(x_rows, w_rows, x.dtype)
         return y.view(*x.shape[:-1], w.shape[0])
 
@@ -1203,7 +1238,7 @@ class _MXLinear(torch.autograd.Function):
         if ctx.weight is not None and ctx.weight.version != ctx.version:
             raise RuntimeError("the MXWeight was refreshed between the forward and the backward pass")
         saved = list(ctx.saved_tensors)
-        x_cols, w_cols = [None if k is None else MXTensor(saved.pop(0), saved.pop(0), *k) for k in ctx.kept]
+        x_cols, w_cols = [None if k is None else MXTensor._over(saved.pop(0), *k) for k in ctx.kept]
         need_x, need_w = ctx.needs_input_grad[:2]
         flat = _flat(dy)
         layout = "both" if need_x and need_w else "rows" if need_x else "cols"
