@@ -644,11 +644,11 @@ flashopt_status check_codes(const void *codes, const void *scales, int64_t rows,
 // by a row's bytes of codes in 24 bits.
 constexpr int64_t kMaxInner = (int64_t{1} << 25) - 128;
 
-// Workgroups of a quantization: tiles of 128 rows by 256 columns, whose
-// work-items a dispatch counts in 32 bits.
+// Workgroups of a quantization: tiles of 32 rows (128 with groups along the
+// columns) by 256 columns, whose work-items a dispatch counts in 32 bits.
 bool quantizable(int64_t rows, int64_t cols)
 {
-    return ((rows + 127) / 128) * ((cols + 255) / 256) < (int64_t{1} << 24);
+    return ((rows + 31) / 32) * ((cols + 255) / 256) < (int64_t{1} << 24);
 }
 
 // The part of a buffer of codes that scales follow in: 16-byte rounded.

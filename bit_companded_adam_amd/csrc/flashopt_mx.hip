@@ -81,18 +81,25 @@ __device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b)
                                                                   __builtin_bit_cast(u16x2, b)));
 }
 
-// Maximum over aligned groups of eight lanes.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t x)
+// Maxima over aligned groups of eight lanes, of four rows at once: lane ^ 1,
+// lane ^ 2, then the other four of the eight.  A DPP read needs two wait
+// states after the write of its source, which the other three rows fill.
+__device__ __forceinline__ void max8(uint32_t (&x)[4])
 {
-    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), CTRL,
-                                                             0xF, 0xF, false));
-}
-__device__ __forceinline__ uint32_t max8(uint32_t x)
-{
-    x = umax32(x, dpp<0xB1>(x));       // lane ^ 1
-    x = umax32(x, dpp<0x4E>(x));       // lane ^ 2
-    return umax32(x, dpp<0x141>(x));   // the other four of the eight
+    asm("s_nop 1\n\t"
+        "v_max_u32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %1, %1, %1 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %2, %2, %2 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %3, %3, %3 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %0, %0, %0 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %1, %1, %1 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %2, %2, %2 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %3, %3, %3 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %0, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %1, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %2, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_max_u32_dpp %3, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xf"
+        : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]));
 }
 
 // Two E2M1 codes in byte SEL of acc (half to even, saturating at 6), from
@@ -110,14 +117,14 @@ __device__ __forceinline__ uint32_t codes2(uint32_t acc, uint32_t ab, uint32_t s
                                                      __uint_as_float(scale), SEL);
 }
 
-// A wavefront takes 32 rows by 256 columns, four columns to a lane: every
-// load covers 512 (bf16) or 1024 bytes of a row, a group along a row is
-// eight lanes, and a group along a column is one lane's 32 values.
+// A wavefront takes 256 columns, four to a lane, of 32 rows, or of 8 where no
+// groups along columns are wanted: every load covers 512 (bf16) or 1024 bytes
+// of a row, a group along a row is eight lanes, and a group along a column is
+// one lane's 32 values.
 constexpr int kLaneCols = 4;
 constexpr int kTileCols = 64 * kLaneCols;
-constexpr int kWaveRows = 32;
 constexpr int kQuantWaves = kThreads / kWaveLanes;
-constexpr int kTileRows = kWaveRows * kQuantWaves;
+constexpr int quant_rows(bool columns) { return (columns ? 32 : 8) * kQuantWaves; }
 
 // A lane's four values of one row, in the words they came in.
 template <bool F32>
@@ -125,22 +132,24 @@ struct Four {
     uint32_t w[F32 ? 4 : 2];
 };
 
-template <bool F32, bool VEC>
+template <bool F32>
+__device__ __forceinline__ Four<F32> load4(const uint8_t *p)
+{
+    Four<F32> f;
+    if constexpr (F32) {
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        f.w[0] = v.x; f.w[1] = v.y; f.w[2] = v.z; f.w[3] = v.w;
+    } else {
+        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+        f.w[0] = v.x; f.w[1] = v.y;
+    }
+    return f;
+}
+// The same where the row may be unaligned, or end within the four.
+template <bool F32>
 __device__ __forceinline__ Four<F32> load4(const uint8_t *row, int64_t c, int64_t cols)
 {
     Four<F32> f{};
-    if constexpr (VEC) {
-        if (c + 4 <= cols) {
-            if constexpr (F32) {
-                const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + c * 4));
-                f.w[0] = v.x; f.w[1] = v.y; f.w[2] = v.z; f.w[3] = v.w;
-            } else {
-                const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + c * 2));
-                f.w[0] = v.x; f.w[1] = v.y;
-            }
-            return f;
-        }
-    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (c + j >= cols) continue;
@@ -194,15 +203,16 @@ __device__ __forceinline__ uint32_t column_codes(const Four<F32> *f, int j, uint
 }
 
 // Codes of x along its rows (ROWS) and of its transpose (COLS), from one
-// read.  A workgroup's four wavefronts take 128 rows, so that it writes 64
-// bytes of each column's codes and one word of its scales; those, and the
-// rows' scales, go through LDS to be stored in such pieces.
+// read.  With COLS a workgroup's four wavefronts take 128 rows, so that it
+// writes 64 bytes of each column's codes and one word of its scales; those,
+// and the rows', go through LDS to be stored in such pieces.
 template <bool F32, bool ROWS, bool COLS, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, int64_t row_bytes,
                    uint32_t row_tiles, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                    uint8_t *__restrict__ codes_t, uint8_t *__restrict__ scales_t)
 {
+    constexpr int kTileRows = quant_rows(COLS), kWaveRows = kTileRows / kQuantWaves;
     __shared__ __align__(16) u32x4 s_codes[COLS ? kTileCols * kQuantWaves : 1];
     __shared__ __align__(16) uint8_t s_scales_t[COLS ? kTileCols * kQuantWaves : 1];
     __shared__ __align__(16) uint16_t s_rows[ROWS ? kTileRows * 64 : 1];
@@ -218,10 +228,20 @@ mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, in
     const int64_t colsp = mx_padded(cols), rowsp = mx_padded(rows);
 
     Four<F32> f[kWaveRows];
+    if (VEC && tile_col + kTileCols <= cols && row0 + kWaveRows <= rows) {
+        const uint8_t *p = x + row0 * row_bytes + tile_col * (F32 ? 4 : 2);
+        const uint32_t at = lane * (kLaneCols * (F32 ? 4 : 2));
 #pragma unroll
-    for (int r = 0; r < kWaveRows; ++r) {
-        f[r] = Four<F32>{};
-        if (row0 + r < rows) f[r] = load4<F32, VEC>(x + (row0 + r) * row_bytes, c, cols);
+        for (int r = 0; r < kWaveRows; ++r, p += row_bytes) f[r] = load4<F32>(p + at);
+    } else {
+#pragma unroll
+        for (int r = 0; r < kWaveRows; ++r) {
+            f[r] = Four<F32>{};
+            if (row0 + r < rows) {
+                const uint8_t *row = x + (row0 + r) * row_bytes;
+                f[r] = VEC && c + 4 <= cols ? load4<F32>(row + c * (F32 ? 4 : 2)) : load4<F32>(row, c, cols);
+            }
+        }
     }
     Four<F32> col_top{};
 #pragma unroll
@@ -231,30 +251,50 @@ mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, in
     const bool bad = __any(largest(col_top) >= kExponent);
 
     if constexpr (ROWS) {
+        // opaque, or the magnitudes above would be kept for the rows' maxima
+        // and double the registers
 #pragma unroll
-        for (int r = 0; r < kWaveRows; ++r) {
-            // opaque, or the magnitudes above would be kept for this use and
-            // double the registers
+        for (int r = 0; r < kWaveRows; ++r)
 #pragma unroll
-            for (int i = 0; i < (F32 ? 4 : 2); ++i) asm volatile("" : "+v"(f[r].w[i]));
-            const uint32_t top = max8(largest(magnitudes(f[r])));
-            const uint32_t scale = scale_bits(top);
-            uint32_t q, b = scale >> 23;
-            if constexpr (F32) {
-                q = codes2<0>(0u, f[r].w[0], f[r].w[1], scale);
-                q = codes2<1>(q, f[r].w[2], f[r].w[3], scale);
-            } else {
-                q = codes2<0>(0u, f[r].w[0], scale);
-                q = codes2<1>(q, f[r].w[1], scale);
+            for (int w = 0; w < (F32 ? 4 : 2); ++w) asm volatile("" : "+v"(f[r].w[w]));
+        uint32_t keep[kWaveRows / 8] = {};       // lane l: the scale of its group in rows l % 8 + 8 i
+        auto four_rows = [&](int r0, auto check) {
+            uint32_t top[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = largest(magnitudes(f[r0 + i]));
+            max8(top);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + i;
+                const uint32_t scale = scale_bits(top[i]);
+                uint32_t q, b = scale >> 23;
+                if constexpr (F32) {
+                    q = codes2<0>(0u, f[r].w[0], f[r].w[1], scale);
+                    q = codes2<1>(q, f[r].w[2], f[r].w[3], scale);
+                } else {
+                    q = codes2<0>(0u, f[r].w[0], scale);
+                    q = codes2<1>(q, f[r].w[1], scale);
+                }
+                if (decltype(check)::value && top[i] >= kExponent) {
+                    q = 0u;
+                    b = 255u;
+                }
+                keep[r / 8] = (lane & 7) == (r & 7) ? b : keep[r / 8];
+                s_rows[(wave * kWaveRows + r) * 64 + lane] = static_cast<uint16_t>(q);
             }
-            if (bad && top >= kExponent) {
-                q = 0u;
-                b = 255u;
-            }
-            if ((lane & 7) == 0) s_scales[(wave * kWaveRows + r) * (kTileCols / 32) + lane / 8] = static_cast<uint8_t>(b);
-            s_rows[(wave * kWaveRows + r) * 64 + lane] = static_cast<uint16_t>(q);
-            __builtin_amdgcn_sched_barrier(0);        // row by row: fewer registers, more wavefronts
+            __builtin_amdgcn_sched_barrier(0);   // a few rows at a time: fewer registers, more wavefronts
+        };
+        if (!bad) {
+#pragma unroll
+            for (int r = 0; r < kWaveRows; r += 4) four_rows(r, std::false_type{});
+        } else {
+#pragma unroll
+            for (int r = 0; r < kWaveRows; r += 4) four_rows(r, std::true_type{});
         }
+#pragma unroll
+        for (int i = 0; i < kWaveRows / 8; ++i)
+            s_scales[(wave * kWaveRows + 8 * i + (lane & 7)) * (kTileCols / 32) + lane / 8] =
+                static_cast<uint8_t>(keep[i]);
     }
     if constexpr (COLS) {
 #pragma unroll
@@ -934,7 +974,7 @@ hipError_t quantize_layout(const MxMatrix &x, uint8_t *codes, uint8_t *scales, u
 {
     const int64_t row_bytes = x.row_stride * (F32 ? 4 : 2);
     const uint32_t col_tiles = static_cast<uint32_t>((mx_padded(x.cols) + kTileCols - 1) / kTileCols);
-    const uint32_t row_tiles = static_cast<uint32_t>((x.rows + kTileRows - 1) / kTileRows);
+    const uint32_t row_tiles = static_cast<uint32_t>((x.rows + quant_rows(COLS) - 1) / quant_rows(COLS));
     const dim3 grid(col_tiles * row_tiles);
     const uint8_t *p = static_cast<const uint8_t *>(x.data);
     constexpr int vec = F32 ? 16 : 8;

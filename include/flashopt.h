@@ -501,7 +501,7 @@ size_t flashopt_mx_scale_bytes(int64_t rows, int64_t cols);
  *                      columns; or both NULL.  Both pairs come from one read
  *   x                  aligned to its element; row_stride >= 0
  * Errors: EINVAL (negative or too large sizes, x_fp32 not 0 or 1, NULL x, no
- * or half an output pair, 2^24 tiles of 128 x 256 or more), EALIGN, EHIP.  An
+ * or half an output pair, 2^24 tiles of 32 x 256 or more), EALIGN, EHIP.  An
  * empty matrix is a no-op. */
 flashopt_status flashopt_mx_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols,
                                      int64_t row_stride, void *codes, void *scales,
