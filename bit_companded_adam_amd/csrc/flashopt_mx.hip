@@ -1040,8 +1040,8 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     if (a.rows <= 16) return skinny<F32, VEC, 1, 4>(a, b, kp, out, row_bytes, st);
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
-    if (big >= 200) return tiles<F32, VEC, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
-    if (mid >= 200) return tiles<F32, VEC, 128, 128, 2, 2>(a, b, kp, out, row_bytes, st);
+    if (big >= 160) return tiles<F32, VEC, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
+    if (mid >= 160) return tiles<F32, VEC, 128, 128, 2, 2>(a, b, kp, out, row_bytes, st);
     return tiles<F32, VEC, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
