@@ -1,5 +1,7 @@
 """Thin ctypes binding of libflashopt.so with the C entry points' names
-(FlashAdamW and FlashSGD steps, the codec and the weight split).
+(FlashAdamW and FlashSGD steps, the codec and the weight split; the gradient
+norm and clipping; MXFP4 quantization and products, and mx_linear on top of
+them for autograd).
 
 Argument marshalling only: every computation runs in the HIP kernels of the
 library.  Tensors are torch CUDA (HIP) tensors; outputs are allocated with
@@ -599,6 +601,8 @@ def _grad_workspace(n: int, device) -> torch.Tensor:
     """For the current stream."""
     need = _GRAD_SHORT_BYTES if 0 < n <= 64 else max(16, flashopt_grad_workspace_bytes(n))
     if torch.cuda.is_current_stream_capturing():
+        if n > 64:
+            raise ValueError("a list of more than 64 gradients is not captured as it is: use a GradPlan")
         return torch.zeros(need, dtype=torch.uint8, device=device)
     key = (device.index, _stream(None))
     ws = _grad_workspaces.get(key)
@@ -1165,7 +1169,8 @@ def flashopt_mx_linear_workspace_bytes(m: int, k: int) -> int:
 
 def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, workspace=None, stream=None):
     """x w^T of a bf16 or fp32 matrix, quantized on the way, and MXFP4 weights
-    (no gradients: mx_linear has them); in x's dtype unless given."""
+    (no gradients: mx_linear has them); in x's dtype unless given.  out must
+    not share elements with x."""
     ptr, wide, m, k, stride = _matrix(x, "x")
     if k != w.cols:
         raise ValueError(f"x has {k} columns, w {w.cols}")

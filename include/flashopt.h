@@ -1,8 +1,9 @@
 /*
  * flashopt.h -- C ABI of libflashopt.so, the MI355X (gfx950) FlashAdamW and
- * FlashSGD steps.
+ * FlashSGD steps, and what a training step around them needs: the gradient
+ * norm and clipping, and matrix products in 4 bits (MXFP4).
  *
- * The method is described on the pages
+ * The steps' method is described on the pages
  *   "code/flashsim/quantization.py"    (group-32 companded int8/uint8 state codec,
  *                                      Alg. 2 momentum / Alg. 3 variance),
  *   "code/flashsim/flash_adamw_sim.py" (FlashAdamWSim.step: Alg. 4, the step),
@@ -34,6 +35,9 @@
  *   - Alignment: every element stream (fp32, bf16, codes, rho) must start on a
  *     16-byte boundary, scale arrays on a 2-byte boundary; otherwise
  *     FLASHOPT_EALIGN.  Allocations from hipMalloc / torch satisfy this.
+ *     Gradients of a norm and matrices of the MXFP4 calls may start at any
+ *     element; those calls state their own rules, and what they do with
+ *     non-finite values.
  *   - A step call launches its step kernel once.  A list (or tensor) of more
  *     than 2^25 - 2 chunks of 1024 elements (2^24 - 1 with fp32 states or
  *     fp32 parameters) does not fit one dispatch's 32-bit count of
@@ -371,8 +375,9 @@ flashopt_status flashopt_sgd_step(const flashopt_tensor *tensors, int n_tensors,
  * args and the tables into `plan` (flashopt_sgd_plan_bytes(n) bytes) and
  * fills *info; flashopt_sgd_plan_set_step rewrites the scalars (any step and
  * hyper-parameters; master_bits, companded, fp32_states, state_layout and
- * whether there is a grad_scale must equal the plan's); flashopt_sgd_plan_launch enqueues the kernel only
- * and can be captured into a graph.
+ * whether there is a grad_scale must equal the plan's);
+ * flashopt_sgd_plan_launch enqueues the kernel only and can be captured into a
+ * graph.
  * Errors: as flashopt_sgd_step (EWORKSPACE for a NULL or short plan; EINVAL
  * also for a NULL info or a variant mismatch). */
 size_t flashopt_sgd_plan_bytes(int n_tensors);
@@ -533,6 +538,8 @@ flashopt_status flashopt_mx_product(const void *a_codes, const void *a_scales,
  * out once.  The result is that of flashopt_mx_quantize and
  * flashopt_mx_product.
  *   workspace  DEVICE, 16-byte aligned, holds x's codes until the call has run
+ *   out        may lie between x's columns (the same bytes from row to row),
+ *              but shares no element with x
  * Errors: as those calls; EWORKSPACE. */
 size_t flashopt_mx_linear_workspace_bytes(int64_t m, int64_t k);
 flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t k,

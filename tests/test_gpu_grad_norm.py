@@ -4,6 +4,7 @@ The norm is checked against a 64-bit sum: its squares and sums are fp64, so
 only the last rounding to fp32 counts (half a unit, 2^-24).  Clipped gradients
 and clipped steps are compared bit for bit, with the scale the GPU returned."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -180,6 +181,53 @@ def test_captured_norm_and_clipped_step(n):
         for x, y in zip(a.states, b.states):
             assert (u16(x.param) == u16(y.param)).all()
             assert torch.equal(x.block, y.block)
+
+
+def test_capture_of_a_long_list_is_refused():
+    """Its table is staged from the host, which a graph cannot hold."""
+    require_gpu()
+    grads = [torch.ones(8, device="cuda") for _ in range(65)]
+    out = torch.zeros(2, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in (F.flashopt_grad_norm, F.flashopt_grad_clip):
+            with pytest.raises(ValueError, match="GradPlan"):
+                call(grads, 1.0, out=out)
+        F.flashopt_grad_norm(grads[:64], 1.0, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        # 512 ones: the norm is one rounding of an fp64 square root
+        assert out[0].item() == float(torch.tensor(512.0).sqrt())
+
+
+def test_threads_on_streams_of_their_own():
+    """Norms from several host threads at once, each on its own stream."""
+    require_gpu()
+    lists = [[W.make_grad(50_000 + 1000 * i, k, device="cuda", stream_id=i) for i in range(n)]
+             for k, n in enumerate((3, 40, 90, 130))]
+    want = [F.flashopt_grad_norm(l, 0.5) for l in lists]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in lists], []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                got[k].append(F.flashopt_grad_norm(lists[k], 0.5, stream=stream))
+            stream.synchronize()
+        except Exception as e:                     # raised again below
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(lists))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for k, outs in enumerate(got):
+        assert len(outs) == 20 and all(torch.equal(o, want[k]) for o in outs)
 
 
 # ------------------------------------------------------------ clipped steps

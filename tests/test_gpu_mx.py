@@ -258,6 +258,42 @@ def test_product_into_views():
                 assert (wide[:, :first] == 3).all() and (wide[:, first + n:] == 3).all()
 
 
+def test_offsets_past_32_bits():
+    """Matrices, codes and outputs of more than 2^32 bytes and elements: the
+    far end equals the same rows on their own, and a product there is exact
+    (small integers: every sum is)."""
+    require_gpu()
+    rows, cols, tail = 70_000, 131_072, 300
+    x = torch.zeros(rows, cols, dtype=BF16, device="cuda")           # 18 GB, codes of 4.6 GB
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[-tail:] = torch.randint(-3, 4, (tail, cols), generator=g, device="cuda", dtype=torch.int32).to(BF16)
+    q, t = F.flashopt_mx_quantize(x, "both")
+    end = F.flashopt_mx_quantize(x[-tail:])
+    assert torch.equal(q.codes[-tail:], end.codes) and torch.equal(q.scales[-tail:], end.scales)
+    right = F.flashopt_mx_quantize(x[:, -256:], "cols")
+    assert torch.equal(t.codes[-256:], right.codes) and torch.equal(t.scales[-256:], right.scales)
+    wide = F.flashopt_mx_dequantize(q, BF16)
+    assert torch.equal(wide[-tail:], F.flashopt_mx_dequantize(end, BF16))
+    assert not wide[:4].any() and not wide[-tail - 4:-tail].any()
+    del wide, t, right, x
+    for m in (3, 40):                                                # few rows, tiles
+        a = F.flashopt_mx_quantize(_random(m, cols, 4, BF16, 0).round().clamp(-2, 2))
+        out = F.flashopt_mx_product(a, q, F32)
+        want = _values(a) @ _values(end).t()
+        assert torch.equal(out[:, -tail:], want.to(F32)), m
+        assert not out[:, :rows - tail].any()
+    del q, end, out, want
+    # an output of 4.6 G elements
+    n = 68_000
+    x = torch.randint(-3, 4, (n, 128), generator=g, device="cuda", dtype=torch.int32).to(BF16)
+    q = F.flashopt_mx_quantize(x)
+    out = F.flashopt_mx_product(q, q)
+    v = _values(q)
+    for at in (0, 31_000, n - 500):
+        want = v[at:at + 500] @ v.t()
+        assert torch.equal(out[at:at + 500], want.to(BF16)), at
+
+
 # ------------------------------------------------------------------ linear
 
 def test_linear_equals_quantize_and_product():
