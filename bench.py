@@ -18,7 +18,8 @@ flat-2^20 (one tensor of 2^20 params: cache-resident, a latency figure),
 codec ablation), --fp32-states (quantize_states=False), --optimizer sgd (the
 FlashSGD step: lr 1e-2, momentum 0.9, weight decay 0.01), --grad-release (one
 single-tensor launch per tensor, the gradient-release launch pattern).
---codec times the codec and split entry points instead (one JSON line each).
+--codec times the codec and split entry points instead, --ops the gradient
+norm, clipping and MXFP4 entry points (one JSON line each).
 
 Prints one JSON line: Gparam/s over the K timed steps, the roofline of the
 step kernel (algorithmic bytes per param of the configuration against
@@ -538,6 +539,72 @@ def bench_codec(n: int, reps: int, warmup: int):
         }), flush=True)
 
 
+def bench_ops(workload: str, reps: int, warmup: int):
+    """Times the gradient norm, clipping and the scaled step over a workload's
+    list, and the MXFP4 entry points at the 8.0B list's layer sizes (one JSON
+    line each).  Rates count each input read once and each output written
+    once; clipping reads and writes every gradient."""
+    shapes = WORKLOADS[workload]()
+    sizes = [W.numel(s) for _, s in shapes]
+    n = sum(sizes)
+    factors = W.grad_factors(len(sizes)).tolist()
+    grads = [W.make_grad(k, 1, device="cuda", factor=f, stream_id=i)
+             for i, (k, f) in enumerate(zip(sizes, factors))]
+    plan = F.GradPlan(grads)
+    out = torch.empty(2, device="cuda")
+    opt = F.FlashAdamW([W.init_param(k, device="cuda", seed=i) for i, k in enumerate(sizes)],
+                       **W.HP_DEFAULT)
+    bound = [float(plan.norm()[0])]
+
+    def clip():                      # a little more each time: the gradients stay clipped
+        bound[0] *= 0.999
+        plan.clip(bound[0], out=out)
+    m, k, f = 8192, 4096, 14336
+    g = torch.Generator(device="cuda").manual_seed(W.PARAM_SEED)
+    x = torch.randn((m, k), generator=g, device="cuda").bfloat16()
+    w = F.flashopt_mx_quantize(torch.randn((f, k), generator=g, device="cuda").bfloat16() * 0.02)
+    y = torch.empty((m, f), dtype=torch.bfloat16, device="cuda")
+    rows, both = F.flashopt_mx_quantize(x), F.flashopt_mx_quantize(x, "both")
+    mx = 17 / 32                     # bytes of an MXFP4 element
+    cases = [
+        ("flashopt_grad_norm", workload, 2 * n, 0, lambda: plan.norm(1.0, out=out)),
+        ("flashopt_grad_clip", workload, 4 * n, 0, clip),
+        ("flashopt_adamw_step, scaled", workload, bytes_per_param(24) * n, 0,
+         lambda: opt.step(grads, grad_scale=out[1:])),
+        ("flashopt_mx_quantize, rows", f"{m} x {k} bf16", (2 + mx) * m * k, 0,
+         lambda: F.flashopt_mx_quantize(x, out=rows)),
+        ("flashopt_mx_quantize, both", f"{m} x {k} bf16", (2 + 2 * mx) * m * k, 0,
+         lambda: F.flashopt_mx_quantize(x, "both", both)),
+        ("flashopt_mx_dequantize", f"{m} x {k} bf16", (2 + mx) * m * k, 0,
+         lambda: F.flashopt_mx_dequantize(rows, out=x)),
+        ("flashopt_mx_product", f"{m} x {f} x {k}", mx * (m + f) * k + 2 * m * f, 2 * m * f * k,
+         lambda: F.flashopt_mx_product(rows, w, out=y)),
+        ("flashopt_mx_linear", f"1 x {f} x {k}", 2 * k + mx * f * k + 2 * f, 2 * f * k,
+         lambda: F.flashopt_mx_linear(x[:1], w, out=y[:1])),
+    ]
+    for op, size, nbytes, flops, fn in cases:
+        for _ in range(warmup):
+            fn()
+        torch.cuda.synchronize()
+        ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+              for _ in range(reps)]
+        for a, b in ev:
+            a.record()
+            fn()
+            b.record()
+        torch.cuda.synchronize()
+        ms = float(np.median([a.elapsed_time(b) for a, b in ev]))
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        line = {"metric": f"{op} ({size}) GB/s, 1 GPU", "value": gbs, "unit": "GB/s", "n_gpus": 1,
+                "steps": reps, "warmup": warmup, "ms_per_step": ms, "higher_is_better": True,
+                "vs_baseline": None, "data": "synthetic", "config": {"op": op, "size": size},
+                "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
+                             "frac": gbs / PEAK_HBM_GBS, "traffic": None}}
+        if flops:
+            line["tflops"] = flops / (ms * 1e-3) / 1e12
+        print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -583,6 +650,9 @@ def main():
                     help="instead of the step, time the codec and split entry points on one "
                          "flat tensor (one JSON line each)")
     ap.add_argument("--codec-elems", type=int, default=1 << 29)
+    ap.add_argument("--ops", action="store_true",
+                    help="instead of the step, time the gradient norm, clipping, the scaled step and "
+                         "the MXFP4 entry points (one JSON line each)")
     args = ap.parse_args()
 
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) != 1:
@@ -598,6 +668,9 @@ def main():
         return
     if args.codec:
         bench_codec(args.codec_elems, args.steps, args.warmup)
+        return
+    if args.ops:
+        bench_ops(args.workload, args.steps, args.warmup)
         return
 
     mb, comp, qs = args.master_bits, not args.linear, not args.fp32_states
