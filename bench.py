@@ -52,6 +52,7 @@ from bit_companded_adam_amd import flashopt as F  # noqa: E402
 from bit_companded_adam_amd import workloads as W  # noqa: E402
 
 METRIC = "FlashAdamW step Gparam/s and % of HBM roofline (12.25 B/param), 1 GPU"
+PEAK_FP4_TFLOPS = 10066.0   # MI355X, dense
 PEAK_HBM_GBS = 8000.0
 KERNEL_SRC = os.path.join(ROOT, "bit_companded_adam_amd", "csrc", "flashopt_kernels.hip")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "adamw_step_8b_traffic.json")
@@ -594,14 +595,15 @@ def bench_ops(workload: str, reps: int, warmup: int):
             b.record()
         torch.cuda.synchronize()
         ms = float(np.median([a.elapsed_time(b) for a, b in ev]))
-        gbs = nbytes / (ms * 1e-3) / 1e9
-        line = {"metric": f"{op} ({size}) GB/s, 1 GPU", "value": gbs, "unit": "GB/s", "n_gpus": 1,
+        gbs, tflops = nbytes / (ms * 1e-3) / 1e9, flops / (ms * 1e-3) / 1e12
+        # the bound whose peak rate takes longer
+        matrix = flops / PEAK_FP4_TFLOPS / 1e12 > nbytes / PEAK_HBM_GBS / 1e9
+        value, unit, peak = (tflops, "TFLOP/s", PEAK_FP4_TFLOPS) if matrix else (gbs, "GB/s", PEAK_HBM_GBS)
+        line = {"metric": f"{op} ({size}) {unit}, 1 GPU", "value": value, "unit": unit, "n_gpus": 1,
                 "steps": reps, "warmup": warmup, "ms_per_step": ms, "higher_is_better": True,
                 "vs_baseline": None, "data": "synthetic", "config": {"op": op, "size": size},
-                "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
-                             "frac": gbs / PEAK_HBM_GBS, "traffic": None}}
-        if flops:
-            line["tflops"] = flops / (ms * 1e-3) / 1e12
+                "roofline": {"bound": "mfma" if matrix else "hbm", "achieved": value, "peak": peak,
+                             "unit": unit, "frac": value / peak, "traffic": None}}
         print(json.dumps(line), flush=True)
 
 

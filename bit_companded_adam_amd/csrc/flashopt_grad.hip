@@ -188,6 +188,8 @@ __device__ __forceinline__ int32_t share(int32_t total, uint32_t b, uint32_t nb)
     return static_cast<int32_t>(static_cast<int64_t>(total) * b / nb);
 }
 
+// A list of 1.2e9 bf16 elements takes 372 us (6.4 TB/s), one of 2.2e8 76 us
+// (5.8); memory bounds it, a large copy reaching 6.2.
 template <typename List>
 __global__ void __launch_bounds__(kNormThreads)
 grad_norm_kernel(List list, int n_tensors, int32_t total_chunks, double max_norm,

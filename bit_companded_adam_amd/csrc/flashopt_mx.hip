@@ -203,7 +203,9 @@ __device__ __forceinline__ uint32_t column_codes(const Four<F32> *f, int j, uint
 }
 
 // Codes of x along its rows (ROWS) and of its transpose (COLS), from one
-// read.  With COLS a workgroup's four wavefronts take 128 rows, so that it
+// read.  Bound by memory: 8192 x 4096 takes 16.5 us along rows (85 MB, 5.2
+// TB/s), 24 both ways (103 MB, 4.3 TB/s).  (Nontemporal stores save 2% and
+// cost 5% where the codes are read next.)  With COLS a workgroup's four wavefronts take 128 rows, so that it
 // writes 64 bytes of each column's codes and one word of its scales; those,
 // and the rows', go through LDS to be stored in such pieces.
 template <bool F32, bool ROWS, bool COLS, bool VEC>
@@ -359,7 +361,9 @@ __device__ __forceinline__ float scale_value(uint32_t b)
     return __uint_as_float(b == 255u ? 0x7FC00000u : b << 23);
 }
 
-// One thread per eight columns.
+// One thread per eight columns.  8192 x 4096 takes 15.3 us to bf16 and 25.5 to
+// fp32 (85 and 152 MB: 5.6 and 6.0 TB/s).  (Nontemporal stores save 4 us, and
+// cost 5 where out is read next.)
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
@@ -460,7 +464,9 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa
 // Within a step a lane holds groups 2 g and 2 g + 1 of its row (g = lane / 16):
 // 32 consecutive bytes, and any assignment of groups to the instruction's
 // four K slots is the same sum as long as both operands and their scales
-// agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.
+// agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.  1 x
+// 14336 x 4096 takes 9.0 us (31 MB, 3.5 TB/s), 1 x 4096 x 4096 4.4 (8.9 MB):
+// latency, of the launch, one pass over K and the sum across wavefronts.
 constexpr int kSkinnyWaves = 8;
 
 struct Step {
@@ -599,17 +605,26 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
 //
 // Each K step of 256 elements is 128 bytes of every row, one cache line,
 // copied from global memory to LDS by the DMA (16 bytes to a lane, eight rows
-// an instruction).  LDS holds row r's 16-byte chunk c at slot c ^ (r & 7) of
-// the row's 128 bytes: the DMA writes lanes in order, so each lane fetches
+// an instruction).  LDS holds row r's 16-byte chunk c at slot c ^ (r / 2 & 7)
+// of the row's 128 bytes: the DMA writes lanes in order, so each lane fetches
 // the chunk that belongs to its slot, and the 32 rows that an operand read
-// takes at one c then fall on all banks.  Two buffers: the copy of the next
-// step runs while this one is multiplied, one barrier a step.
+// takes at one c then fall on all banks.  Two buffers, and one barrier near
+// the end of a step: by then its buffer has been read, so the copy of the step
+// after next goes there and has a whole step's products to land in.
 //
 // Scales: each thread carries 16 bytes of one row, two steps' worth, through
 // a register to LDS.  (Loaded by the lanes that use them they cost 32 cache
 // lines an instruction, and set the time: 8192^3 took 485 us.)  The four that
 // a lane needs of a step's eight (groups 2 k + lane / 32) are gathered into
 // one word with a byte permutation, and the instruction selects its byte.
+//
+// What bounds it: 8192^3 takes 258-266 us (4.1-4.3 PFLOP/s) on random codes
+// and 192 us (5.7) on zeros, where the bare instructions on registers reach 6.4
+// and 9.1 PFLOP/s: random operands cost clock, the rest is waiting for copies
+// (155 us without them) and 6 us a tile for storing out, while every CU
+// stores.  Four wavefronts of 128 x 128 instead of eight of 64 x 128 (a third
+// fewer LDS reads, accumulators in AGPRs) take 275 us: nothing runs beside a
+// wavefront's own waits then.
 typedef __attribute__((address_space(3))) uint8_t l_u8;
 
 // 16 bytes a lane from base + offset to LDS, the lanes' in order from byte
@@ -656,7 +671,7 @@ struct Tile {
 
 // Tile number t of a launch: neighbours on one XCD take neighbouring tiles,
 // in columns of kGroupM tiles, so that the 32 or so that run together share
-// their rows in the XCD's L2.
+// their rows in the XCD's L2 (columns of 8 are level).
 constexpr uint32_t kGroupM = 4;
 
 __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_n, uint32_t tiles_m, uint32_t &tn, uint32_t &tm)
@@ -738,46 +753,54 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
     struct Operands {
         u32x4 n[kTN], m[kTM];
     };
-    auto fetch = [&](int buf, int q, Operands &v) {
+    // Operand i of a quarter, in the order the products need them.
+    constexpr int kReads = kTN + kTM;
+    auto fetch = [&](int buf, int q, Operands &v, int i) {
         const uint32_t at = off ^ (32 * q);
-#pragma unroll
-        for (int i = 0; i < kTN; ++i)
-            v.n[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * kTN + i) * 4096 + at]);
-#pragma unroll
-        for (int i = 0; i < kTM; ++i)
-            v.m[i] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * kTM + i) * 4096 + at]);
+        if (i == 0 || i > kTM) {
+            const int r = i == 0 ? 0 : i - kTM;
+            v.n[r] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][(wn * kTN + r) * 4096 + at]);
+        } else {
+            v.m[i - 1] = *reinterpret_cast<const u32x4 *>(&s_buf[buf][BN * 128 + (wm * kTM + i - 1) * 4096 + at]);
+        }
     };
 
     f32x16 acc[kTN][kTM];
     uint32_t sn[kTN], sm[kTM];
-    // One quarter's products; with COPY, the copies of step pk are issued
-    // between them, where they cost nothing.  Each block is pinned in its
-    // place: the compiler would sink products past the barrier and the
-    // branches after it, and hold all four quarters' operands.
-    auto multiply = [&](const Operands &v, auto quarter, auto with_copy, int to) {
-        constexpr int q = decltype(quarter)::value, kBlocks = kTN * kTM;
+    // Products [FROM, TO) of a quarter, each after before(x).  Reads of LDS and
+    // copies go there, one or two at a time: a wavefront issues in order, and
+    // six reads in a row, from all wavefronts at once, would keep its products
+    // waiting for LDS.  Each product is pinned in its place: the compiler would
+    // sink products past the barrier and the branches after it, and hold all
+    // four quarters' operands.
+    constexpr int kBlocks = kTN * kTM, kSplit = kBlocks / 4, kRest = kBlocks - kSplit;
+    auto multiply = [&](Operands &v, auto quarter, int from, int to, uint32_t mask, auto &&before) {
+        constexpr int q = decltype(quarter)::value;
 #pragma unroll
-        for (int x = 0; x < kBlocks; ++x) {
+        for (int x = from; x < to; ++x) {
             const int i = x / kTM, j = x % kTM;
+            before(x);
+            if (q >= 2 && j == 0) v.n[i] &= mask;
             acc[i][j] = mfma32<q>(v.n[i], v.m[j], acc[i][j], sn[i], sm[j]);
             asm volatile("" : "+v"(acc[i][j]));
-            if constexpr (decltype(with_copy)::value) {
-#pragma unroll
-                for (int c = x * T::kCopies / kBlocks; c < (x + 1) * T::kCopies / kBlocks; ++c) copy(c, to);
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // Item c of `items` shared out over `blocks`, as early as they go evenly.
+    auto share = [](int items, int blocks, int x, auto &&item) {
+        const int per = (items + blocks - 1) / blocks;
+#pragma unroll
+        for (int c = x * per; c < (x + 1) * per && c < items; ++c) item(c);
     };
     constexpr std::integral_constant<int, 0> q0{};
     constexpr std::integral_constant<int, 1> q1{};
     constexpr std::integral_constant<int, 2> q2{};
     constexpr std::integral_constant<int, 3> q3{};
-    constexpr std::true_type with_copies{};
-    constexpr std::false_type alone{};
 
     // After the copies of step pk: with the first of two steps, the scales of
     // both go to a register (16 bytes, from a window that ends with the row, so
-    // nothing past it is read), and half a step on settle() moves them to LDS
-    // and back to their place.  Rows of less than 16 bytes, products over less
+    // nothing past it is read), and before the next barrier settle() moves them
+    // to LDS, each to its place.  Rows of less than 16 bytes, products over less
     // than 512 elements, go there at once.  Past the last tile its last copies
     // are repeated, unused.
     u32x4 next_scales{0u, 0u, 0u, 0u};
@@ -835,7 +858,8 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
     for (int i = 0; i < T::kCopies; ++i) copy(i, 1);
     advance();
     Operands v[2];
-    fetch(0, 0, v[0]);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) fetch(0, 0, v[0], i);
     u32x2 next_n[kTN], next_m[kTM];      // scales of the step to come
     auto fetch_scales = [&](int k) {
 #pragma unroll
@@ -853,10 +877,10 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
         // Each step starts with its first quarter and scales in registers.
-        // Half way through, its buffer has been read by everyone and the next
-        // one has landed: the only barrier, after which the copy two steps on
-        // starts and the next step's first quarter is fetched under the
-        // remaining products.
+        // Early in its last quarter its buffer has been read by everyone and
+        // the next one has landed: the only barrier, after which the copy two
+        // steps on starts and the next step's first quarter is fetched, under
+        // the remaining products.
         for (int k = 0; k < steps; ++k, buf ^= 1) {
 #pragma unroll
             for (int i = 0; i < kTN; ++i) sn[i] = __builtin_amdgcn_perm(next_n[i].y, next_n[i].x, gather);
@@ -866,27 +890,26 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
             // a half step's second half counts as zeros (a branch around its
             // products would double the accumulators)
             const uint32_t second = half_end && last ? 0u : 0xFFFFFFFFu;
-            fetch(buf, 1, v[1]);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(v[0], q0, alone, 0);
-            fetch(buf, 2, v[0]);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(v[1], q1, alone, 0);
-            fetch(buf, 3, v[1]);
+            multiply(v[0], q0, 0, kBlocks, second, [&](int x) {
+                share(kReads, kBlocks, x, [&](int c) { fetch(buf, 1, v[1], c); });
+            });
+            multiply(v[1], q1, 0, kBlocks, second, [&](int x) {
+                share(kReads, kBlocks, x, [&](int c) { fetch(buf, 2, v[0], c); });
+            });
+            multiply(v[0], q2, 0, kBlocks, second, [&](int x) {
+                share(kReads, kBlocks, x, [&](int c) { fetch(buf, 3, v[1], c); });
+            });
+            multiply(v[1], q3, 0, kSplit, second, [](int) {});
             __builtin_amdgcn_s_waitcnt(0);
             settle();
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kTN; ++i) v[0].n[i] &= second;
-            multiply(v[0], q2, with_copies, buf);
-            advance();
             if ((k & 1) || last) set ^= 1;
-            fetch(buf ^ 1, 0, v[0]);
             fetch_scales(last ? 0 : k + 1);
-#pragma unroll
-            for (int i = 0; i < kTN; ++i) v[1].n[i] &= second;
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(v[1], q3, alone, 0);
+            multiply(v[1], q3, kSplit, kBlocks, second, [&](int x) {
+                share(kReads, kRest, x - kSplit, [&](int c) { fetch(buf ^ 1, 0, v[0], c); });
+                share(T::kCopies, kRest, x - kSplit, [&](int c) { copy(c, buf); });
+            });
+            advance();
         }
 
         // Block element e of a lane is m = lane % 32, n = 8 (e / 4) +
@@ -929,6 +952,8 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
                     if (u < kR * kPieces && m < a.rows && n < b.rows) {
                         const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + c * 16);
                         uint8_t *o = out + m * row_bytes + n * kEsz;
+                        // (nontemporal stores save 1-4% here and cost as
+                        // much where out is read next)
                         if (VEC && n + 16 / kEsz <= b.rows) {
                             *reinterpret_cast<u32x4 *>(o) = w;
                         } else {
@@ -1038,6 +1063,12 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
                             : skinny<F32, VEC, 2, 1>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 4) return skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 16) return skinny<F32, VEC, 1, 4>(a, b, kp, out, row_bytes, st);
+    // The largest tile of which there are enough for the 256 CUs: a larger one
+    // reads A and B less often, a smaller one leaves fewer CUs idle.  M x N x
+    // K in us, tiles of 256 / 128: 5632 x 2048 x 8192 (176 tiles) 60.6 / 69.2;
+    // 3000^3 (144) 28.9 / 29.5; 2048 x 4096 x 4096 (128) 32.2 / 27.7.  Of 128 /
+    // 64: 1024 x 4096 x 4096 (256 tiles) 17.7 / 22.1; 1500 x 1500 x 4096 (144)
+    // 18.1 / 19.4; 1024 x 1024 x 4096 (64) 13.5 / 9.5.
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
     if (big >= 160) return tiles<F32, VEC, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
@@ -1045,7 +1076,12 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     return tiles<F32, VEC, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
-// Rows of A up to which the linear layer's product quantizes A itself.
+// Rows of A up to which the linear layer's product quantizes A itself, every
+// workgroup all of it, instead of in a launch before.  N x K of W, in us, in
+// the product / before: 4096 x 4096 5.6 / 7.0 with one row, 6.2 / 7.4 with
+// four, 6.8 / 7.6 with eight; 14336 x 4096 10.6 / 11.8, 11.9 / 12.7 and 13.6 /
+// 12.5; 4096 x 14336 11.9 / 11.5, 13.4 / 12.8 and 16.2 / 13.4 (and a launch
+// less for the host).
 constexpr int64_t kRawRows = 4;
 
 template <bool F32, bool VEC>
