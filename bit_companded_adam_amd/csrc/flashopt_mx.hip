@@ -618,10 +618,10 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
 // a lane needs of a step's eight (groups 2 k + lane / 32) are gathered into
 // one word with a byte permutation, and the instruction selects its byte.
 //
-// What bounds it: 8192^3 takes 258-266 us (4.1-4.3 PFLOP/s) on random codes
-// and 192 us (5.7) on zeros, where the bare instructions on registers reach 6.4
+// What bounds it: 8192^3 takes 256-261 us (4.2-4.3 PFLOP/s) on random codes
+// and 190 us (5.8) on zeros, where the bare instructions on registers reach 6.4
 // and 9.1 PFLOP/s: random operands cost clock, the rest is waiting for copies
-// (155 us without them) and 6 us a tile for storing out, while every CU
+// (150 us without them) and about 5 us a tile for storing out, while every CU
 // stores.  Four wavefronts of 128 x 128 instead of eight of 64 x 128 (a third
 // fewer LDS reads, accumulators in AGPRs) take 275 us: nothing runs beside a
 // wavefront's own waits then.
@@ -657,10 +657,9 @@ struct Tile {
     // as LDS allows; the compiler keeps accumulators out of the AGPRs (moves
     // around each pinned product) where it is held to this
     static constexpr int kWavesPerSimd = BN * BM >= 128 * 128 ? 2 : 4;
-    // a wavefront's turned-over rows of out: so many at a time, 16 bytes of
-    // padding to a row
-    static constexpr int kStageRows(bool f32) { return f32 ? 4 : 8; }
-    static constexpr int kPitch(bool f32) { return kTN * 32 * (f32 ? 4 : 2) + 16; }
+    // a wavefront's turned-over rows of out: so many at a time
+    static constexpr int kStageRows(bool f32) { return f32 ? 8 : 16; }
+    static constexpr int kPitch(bool f32) { return kTN * 32 * (f32 ? 4 : 2); }
     static constexpr int kLds(bool f32)
     {
         return 2 * kBytes + 2 * kRows * 16 + kWaves * kStageRows(f32) * kPitch(f32);
@@ -925,6 +924,9 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
         const int64_t m_first = static_cast<int64_t>(tile_m) * BM + wm * (kTM * 32);
         const int64_t n_first = static_cast<int64_t>(tile_n) * BN + wn * (kTN * 32);
         uint8_t *stage = s_stage[wave];
+        // where piece c of row r lies in the row, so that 16 rows' pieces c
+        // fall on all banks
+        auto turned = [](int r, int c) { return (c ^ ((r * kPieces / 16) & (kPieces - 1))) * 16; };
 #pragma unroll
         for (int j = 0; j < kTM; ++j) {
 #pragma unroll
@@ -935,7 +937,8 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             const f32x16 &x = acc[i][j];
-                            uint8_t *p = stage + (lane & (kR - 1)) * kPitch + (i * 32 + 2 * e + 4 * g) * kEsz;
+                            const int r = lane & (kR - 1), n = i * 32 + 2 * e + 4 * g;
+                            uint8_t *p = stage + r * kPitch + turned(r, n * kEsz / 16) + n * kEsz % 16;
                             if constexpr (F32)
                                 *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
                             else
@@ -950,7 +953,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
                     const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
                     const int64_t m = m_first + j * 32 + r0 + r, n = n_first + c * (16 / kEsz);
                     if (u < kR * kPieces && m < a.rows && n < b.rows) {
-                        const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + c * 16);
+                        const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + turned(r, c));
                         uint8_t *o = out + m * row_bytes + n * kEsz;
                         // (nontemporal stores save 1-4% here and cost as
                         // much where out is read next)
