@@ -28,7 +28,11 @@ namespace {
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_packed __attribute__((aligned(4)));
+// Vectors at any address that their elements may have: global loads and stores
+// of these widths need no alignment.  (8191 x 5631 x 2048 takes 68 us with
+// such stores of out, 125 with one an element; 8192 x 5632 64.)
+typedef u32x4 u32x4_packed __attribute__((aligned(2)));
+typedef u32x2 u32x2_packed __attribute__((aligned(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -137,26 +141,20 @@ __device__ __forceinline__ Four<F32> load4(const uint8_t *p)
 {
     Four<F32> f;
     if constexpr (F32) {
-        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_packed *>(p));
         f.w[0] = v.x; f.w[1] = v.y; f.w[2] = v.z; f.w[3] = v.w;
     } else {
-        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+        const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_packed *>(p));
         f.w[0] = v.x; f.w[1] = v.y;
     }
     return f;
 }
-// The same where the row may be unaligned, or end within the four.
+// One of the four, where the row ends within them.
 template <bool F32>
-__device__ __forceinline__ Four<F32> load4(const uint8_t *row, int64_t c, int64_t cols)
+__device__ __forceinline__ void load1(Four<F32> &f, int j, const uint8_t *p)
 {
-    Four<F32> f{};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (c + j >= cols) continue;
-        if constexpr (F32) f.w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
-        else f.w[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c + j]) << (16 * (j & 1));
-    }
-    return f;
+    if constexpr (F32) f.w[j] = *reinterpret_cast<const uint32_t *>(p + j * 4);
+    else f.w[j / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p + j * 2)) << (16 * (j & 1));
 }
 
 // Magnitude patterns: word by word, and the largest of the four as fp32 bits
@@ -208,7 +206,7 @@ __device__ __forceinline__ uint32_t column_codes(const Four<F32> *f, int j, uint
 // cost 5% where the codes are read next.)  With COLS a workgroup's four wavefronts take 128 rows, so that it
 // writes 64 bytes of each column's codes and one word of its scales; those,
 // and the rows', go through LDS to be stored in such pieces.
-template <bool F32, bool ROWS, bool COLS, bool VEC>
+template <bool F32, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kThreads)
 mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, int64_t row_bytes,
                    uint32_t row_tiles, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
@@ -230,20 +228,34 @@ mx_quantize_kernel(const uint8_t *__restrict__ x, int64_t rows, int64_t cols, in
     const int64_t colsp = mx_padded(cols), rowsp = mx_padded(rows);
 
     Four<F32> f[kWaveRows];
-    if (VEC && tile_col + kTileCols <= cols && row0 + kWaveRows <= rows) {
+    if (tile_col + kTileCols <= cols && row0 + kWaveRows <= rows) {
         const uint8_t *p = x + row0 * row_bytes + tile_col * (F32 ? 4 : 2);
         const uint32_t at = lane * (kLaneCols * (F32 ? 4 : 2));
 #pragma unroll
         for (int r = 0; r < kWaveRows; ++r, p += row_bytes) f[r] = load4<F32>(p + at);
     } else {
+        // rows past the end repeat the last and then count as zeros: no
+        // branch, and so no wait, between the loads (1111 x 1000 bf16 both
+        // ways: 11.2 us with one a row, 7.3 without)
+        auto row = [&](int r) {
+            return x + (row0 + r < rows ? row0 + r : rows - 1) * row_bytes + c * (F32 ? 4 : 2);
+        };
 #pragma unroll
-        for (int r = 0; r < kWaveRows; ++r) {
-            f[r] = Four<F32>{};
-            if (row0 + r < rows) {
-                const uint8_t *row = x + (row0 + r) * row_bytes;
-                f[r] = VEC && c + 4 <= cols ? load4<F32>(row + c * (F32 ? 4 : 2)) : load4<F32>(row, c, cols);
-            }
+        for (int r = 0; r < kWaveRows; ++r) f[r] = Four<F32>{};
+        if (c + 4 <= cols) {
+#pragma unroll
+            for (int r = 0; r < kWaveRows; ++r) f[r] = load4<F32>(row(r));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < cols) {
+#pragma unroll
+                    for (int r = 0; r < kWaveRows; ++r) load1<F32>(f[r], j, row(r));
+                }
         }
+#pragma unroll
+        for (int r = 0; r < kWaveRows; ++r)
+            if (row0 + r >= rows) f[r] = Four<F32>{};
     }
     Four<F32> col_top{};
 #pragma unroll
@@ -364,7 +376,7 @@ __device__ __forceinline__ float scale_value(uint32_t b)
 // One thread per eight columns.  8192 x 4096 takes 15.3 us to bf16 and 25.5 to
 // fp32 (85 and 152 MB: 5.6 and 6.0 TB/s).  (Nontemporal stores save 4 us, and
 // cost 5 where out is read next.)
-template <bool F32, bool VEC>
+template <bool F32>
 __global__ void __launch_bounds__(kThreads)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
                      int64_t cols, uint8_t *__restrict__ out, int64_t row_bytes)
@@ -383,15 +395,17 @@ mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restric
         v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
         v[4] = d.x * s; v[5] = d.y * s; v[6] = e.x * s; v[7] = e.y * s;
         uint8_t *o = out + r * row_bytes;
-        if (VEC && c + 8 <= cols) {
+        if (c + 8 <= cols) {
+            u32x4 p;
             if constexpr (F32) {
-                *reinterpret_cast<f32x4 *>(o + c * 4) = f32x4{v[0], v[1], v[2], v[3]};
-                *reinterpret_cast<f32x4 *>(o + c * 4 + 16) = f32x4{v[4], v[5], v[6], v[7]};
+                for (int k = 0; k < 4; ++k) p[k] = __float_as_uint(v[k]);
+                *reinterpret_cast<u32x4_packed *>(o + c * 4) = p;
+                for (int k = 0; k < 4; ++k) p[k] = __float_as_uint(v[4 + k]);
+                *reinterpret_cast<u32x4_packed *>(o + c * 4 + 16) = p;
             } else {
-                u32x4 p;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) p[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
-                *reinterpret_cast<u32x4 *>(o + c * 2) = p;
+                *reinterpret_cast<u32x4_packed *>(o + c * 2) = p;
             }
         } else {
 #pragma unroll
@@ -416,16 +430,17 @@ struct MxIn {
 };
 
 // Four consecutive outputs of row m from column n on.
-template <bool F32, bool VEC>
+template <bool F32>
 __device__ __forceinline__ void store4(uint8_t *out, int64_t row_bytes, int64_t m, int64_t n, int64_t cols,
                                        float a, float b, float c, float d)
 {
     uint8_t *o = out + m * row_bytes;
-    if (VEC && n + 4 <= cols) {
+    if (n + 4 <= cols) {
         if constexpr (F32) {
-            *reinterpret_cast<f32x4 *>(o + n * 4) = f32x4{a, b, c, d};
+            *reinterpret_cast<u32x4_packed *>(o + n * 4) =
+                u32x4{__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
         } else {
-            *reinterpret_cast<u32x2 *>(o + n * 2) = u32x2{bf16_pair(a, b), bf16_pair(c, d)};
+            *reinterpret_cast<u32x2_packed *>(o + n * 2) = u32x2{bf16_pair(a, b), bf16_pair(c, d)};
         }
         return;
     }
@@ -538,7 +553,7 @@ __device__ __forceinline__ Step load_step(const MxRaw &in, int64_t row, int64_t,
     return s;
 }
 
-template <bool F32, bool VEC, int MT, int NT, typename A>
+template <bool F32, int MT, int NT, typename A>
 __global__ void __launch_bounds__(kSkinnyWaves *kWaveLanes)
 mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row_bytes)
 {
@@ -594,7 +609,7 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
                 v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
             }
             const int64_t m = 16 * (i % MT) + l16, n = n0 + 16 * (i / MT) + 4 * g;
-            if (m < a.rows) store4<F32, VEC>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
+            if (m < a.rows) store4<F32>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
         }
         __syncthreads();
     }
@@ -683,7 +698,7 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_n, uint32_t t
     tn = in / width;
 }
 
-template <bool F32, bool VEC, int BN, int BM, int WN, int WM>
+template <bool F32, int BN, int BM, int WN, int WM>
 __global__ void __launch_bounds__(WN *WM *kWaveLanes)
     __attribute__((amdgpu_waves_per_eu(Tile<BN, BM, WN, WM>::kWavesPerSimd)))
 mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, uint8_t *__restrict__ out,
@@ -957,8 +972,8 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
                         uint8_t *o = out + m * row_bytes + n * kEsz;
                         // (nontemporal stores save 1-4% here and cost as
                         // much where out is read next)
-                        if (VEC && n + 16 / kEsz <= b.rows) {
-                            *reinterpret_cast<u32x4 *>(o) = w;
+                        if (n + 16 / kEsz <= b.rows) {
+                            *reinterpret_cast<u32x4_packed *>(o) = w;
                         } else {
 #pragma unroll
                             for (int x = 0; x < 16 / kEsz; ++x) {
@@ -1005,13 +1020,8 @@ hipError_t quantize_layout(const MxMatrix &x, uint8_t *codes, uint8_t *scales, u
     const uint32_t row_tiles = static_cast<uint32_t>((x.rows + quant_rows(COLS) - 1) / quant_rows(COLS));
     const dim3 grid(col_tiles * row_tiles);
     const uint8_t *p = static_cast<const uint8_t *>(x.data);
-    constexpr int vec = F32 ? 16 : 8;
-    if (aligned_to(p, vec) && row_bytes % vec == 0)
-        hipLaunchKernelGGL((mx_quantize_kernel<F32, ROWS, COLS, true>), grid, dim3(kThreads), 0, st, p, x.rows,
-                           x.cols, row_bytes, row_tiles, codes, scales, codes_t, scales_t);
-    else
-        hipLaunchKernelGGL((mx_quantize_kernel<F32, ROWS, COLS, false>), grid, dim3(kThreads), 0, st, p, x.rows,
-                           x.cols, row_bytes, row_tiles, codes, scales, codes_t, scales_t);
+    hipLaunchKernelGGL((mx_quantize_kernel<F32, ROWS, COLS>), grid, dim3(kThreads), 0, st, p, x.rows, x.cols,
+                       row_bytes, row_tiles, codes, scales, codes_t, scales_t);
     return hipGetLastError();
 }
 
@@ -1024,17 +1034,17 @@ hipError_t quantize_type(const MxMatrix &x, uint8_t *codes, uint8_t *scales, uin
     return quantize_layout<F32, false, true>(x, codes, scales, codes_t, scales_t, st);
 }
 
-template <bool F32, bool VEC, int MT, int NT, typename A>
+template <bool F32, int MT, int NT, typename A>
 hipError_t skinny(const A &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes, hipStream_t st)
 {
     const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT);
     const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
-    hipLaunchKernelGGL((mx_skinny_kernel<F32, VEC, MT, NT, A>), dim3(grid),
+    hipLaunchKernelGGL((mx_skinny_kernel<F32, MT, NT, A>), dim3(grid),
                        dim3(kSkinnyWaves * kWaveLanes), 0, st, a, b, kp, out, row_bytes);
     return hipGetLastError();
 }
 
-template <bool F32, bool VEC, int BN, int BM, int WN, int WM>
+template <bool F32, int BN, int BM, int WN, int WM>
 hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes, hipStream_t st)
 {
     const uint32_t tn = static_cast<uint32_t>((b.rows + BN - 1) / BN);
@@ -1045,7 +1055,7 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
     // in turn; a multiple of the 8 XCDs
     constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds(F32));
     const unsigned grid = total < kAtOnce ? static_cast<unsigned>(total) : kAtOnce;
-    hipLaunchKernelGGL((mx_tile_kernel<F32, VEC, BN, BM, WN, WM>), dim3(grid),
+    hipLaunchKernelGGL((mx_tile_kernel<F32, BN, BM, WN, WM>), dim3(grid),
                        dim3(WN * WM * kWaveLanes), 0, st, a, b, kp, tn, tm, out, row_bytes);
     return hipGetLastError();
 }
@@ -1057,15 +1067,15 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
 // 14336 x 4096 10.0 / 9.5 / 9.3; 16 x 14336 x 4096 14.0 / 11.5 / 10.4.)
 constexpr int64_t kNarrow = 8192;
 
-template <bool F32, bool VEC>
+template <bool F32>
 hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
                         hipStream_t st)
 {
     if (a.rows <= 32 && b.rows <= kNarrow)
-        return a.rows <= 16 ? skinny<F32, VEC, 1, 1>(a, b, kp, out, row_bytes, st)
-                            : skinny<F32, VEC, 2, 1>(a, b, kp, out, row_bytes, st);
-    if (a.rows <= 4) return skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
-    if (a.rows <= 16) return skinny<F32, VEC, 1, 4>(a, b, kp, out, row_bytes, st);
+        return a.rows <= 16 ? skinny<F32, 1, 1>(a, b, kp, out, row_bytes, st)
+                            : skinny<F32, 2, 1>(a, b, kp, out, row_bytes, st);
+    if (a.rows <= 4) return skinny<F32, 1, 2>(a, b, kp, out, row_bytes, st);
+    if (a.rows <= 16) return skinny<F32, 1, 4>(a, b, kp, out, row_bytes, st);
     // The largest tile of which there are enough for the 256 CUs: a larger one
     // reads A and B less often, a smaller one leaves fewer CUs idle.  M x N x
     // K in us, tiles of 256 / 128: 5632 x 2048 x 8192 (176 tiles) 60.6 / 69.2;
@@ -1074,9 +1084,9 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     // 18.1 / 19.4; 1024 x 1024 x 4096 (64) 13.5 / 9.5.
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
-    if (big >= 160) return tiles<F32, VEC, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
-    if (mid >= 160) return tiles<F32, VEC, 128, 128, 2, 2>(a, b, kp, out, row_bytes, st);
-    return tiles<F32, VEC, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
+    if (big >= 160) return tiles<F32, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
+    if (mid >= 160) return tiles<F32, 128, 128, 2, 2>(a, b, kp, out, row_bytes, st);
+    return tiles<F32, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
 // Rows of A up to which the linear layer's product quantizes A itself, every
@@ -1087,12 +1097,12 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
 // less for the host).
 constexpr int64_t kRawRows = 4;
 
-template <bool F32, bool VEC>
+template <bool F32>
 hipError_t linear_type(const MxRaw &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
                        hipStream_t st)
 {
-    return b.rows <= kNarrow ? skinny<F32, VEC, 1, 1>(a, b, kp, out, row_bytes, st)
-                             : skinny<F32, VEC, 1, 2>(a, b, kp, out, row_bytes, st);
+    return b.rows <= kNarrow ? skinny<F32, 1, 1>(a, b, kp, out, row_bytes, st)
+                             : skinny<F32, 1, 2>(a, b, kp, out, row_bytes, st);
 }
 
 }  // namespace
@@ -1110,11 +1120,7 @@ hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, co
     const MxIn b{w_codes, w_scales, out.cols};
     const int64_t kp = mx_padded(x.cols), row_bytes = out.row_stride * (out.fp32 ? 4 : 2);
     uint8_t *p = static_cast<uint8_t *>(out.data);
-    const bool vec = aligned_to(p, 16) && row_bytes % 16 == 0;
-    if (out.fp32) return vec ? linear_type<true, true>(a, b, kp, p, row_bytes, st)
-                             : linear_type<true, false>(a, b, kp, p, row_bytes, st);
-    return vec ? linear_type<false, true>(a, b, kp, p, row_bytes, st)
-               : linear_type<false, false>(a, b, kp, p, row_bytes, st);
+    return out.fp32 ? linear_type<true>(a, b, kp, p, row_bytes, st) : linear_type<false>(a, b, kp, p, row_bytes, st);
 }
 
 hipError_t launch_mx_quantize(const MxMatrix &x, uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
@@ -1132,19 +1138,12 @@ hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, con
     const dim3 grid(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)));
     uint8_t *p = static_cast<uint8_t *>(out.data);
     const int64_t row_bytes = out.row_stride * (out.fp32 ? 4 : 2);
-    const bool vec = aligned_to(p, 16) && row_bytes % 16 == 0;
-    if (out.fp32 && vec)
-        hipLaunchKernelGGL((mx_dequantize_kernel<true, true>), grid, dim3(kThreads), 0, st, codes, scales,
-                           out.rows, out.cols, p, row_bytes);
-    else if (out.fp32)
-        hipLaunchKernelGGL((mx_dequantize_kernel<true, false>), grid, dim3(kThreads), 0, st, codes, scales,
-                           out.rows, out.cols, p, row_bytes);
-    else if (vec)
-        hipLaunchKernelGGL((mx_dequantize_kernel<false, true>), grid, dim3(kThreads), 0, st, codes, scales,
-                           out.rows, out.cols, p, row_bytes);
+    if (out.fp32)
+        hipLaunchKernelGGL(mx_dequantize_kernel<true>, grid, dim3(kThreads), 0, st, codes, scales, out.rows,
+                           out.cols, p, row_bytes);
     else
-        hipLaunchKernelGGL((mx_dequantize_kernel<false, false>), grid, dim3(kThreads), 0, st, codes, scales,
-                           out.rows, out.cols, p, row_bytes);
+        hipLaunchKernelGGL(mx_dequantize_kernel<false>, grid, dim3(kThreads), 0, st, codes, scales, out.rows,
+                           out.cols, p, row_bytes);
     return hipGetLastError();
 }
 
@@ -1161,11 +1160,8 @@ hipError_t launch_mx_product(const uint8_t *a_codes, const uint8_t *a_scales, co
         else hipLaunchKernelGGL(mx_zero_kernel<false>, grid, dim3(kThreads), 0, st, out.rows, out.cols, p, row_bytes);
         return hipGetLastError();
     }
-    const bool vec = aligned_to(p, 16) && row_bytes % 16 == 0;
-    if (out.fp32) return vec ? product_type<true, true>(a, b, kp, p, row_bytes, st)
-                             : product_type<true, false>(a, b, kp, p, row_bytes, st);
-    return vec ? product_type<false, true>(a, b, kp, p, row_bytes, st)
-               : product_type<false, false>(a, b, kp, p, row_bytes, st);
+    return out.fp32 ? product_type<true>(a, b, kp, p, row_bytes, st)
+                    : product_type<false>(a, b, kp, p, row_bytes, st);
 }
 
 }  // namespace flashopt
