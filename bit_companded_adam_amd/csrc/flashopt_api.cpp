@@ -1101,7 +1101,7 @@ flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t
     uint8_t *codes = static_cast<uint8_t *>(workspace);
     uint8_t *scales = codes + rounded(flashopt_mx_code_bytes(m, k));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (flashopt::mx_linear_direct(in))
+    if (flashopt::mx_linear_direct(in, n))
         return hip_status(flashopt::launch_mx_linear_direct(in, static_cast<const uint8_t *>(w_codes),
                                                             static_cast<const uint8_t *>(w_scales), o, st));
     if (k > 0) {

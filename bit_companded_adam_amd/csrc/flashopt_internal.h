@@ -185,9 +185,9 @@ hipError_t launch_mx_quantize(const MxMatrix &x, uint8_t *codes, uint8_t *scales
                               uint8_t *scales_t, hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, const MxMatrix &out,
                                 hipStream_t stream);
-// x w^T in one launch, x quantized inside it: whether x allows it (a few
-// aligned rows of bf16), and the launch.
-bool mx_linear_direct(const MxMatrix &x);
+// x w^T in one launch, x quantized inside it: whether x (a few aligned rows of
+// bf16) and the n rows of w allow it, and the launch.
+bool mx_linear_direct(const MxMatrix &x, int64_t n);
 hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
                                    const MxMatrix &out, hipStream_t stream);
 // out = A B^T with A of out.rows and B of out.cols rows.

@@ -1062,8 +1062,8 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
 
 // Rows of B up to which a skinny product gives a workgroup 16 of them: fewer
 // workgroups than that would leave CUs idle.  Above it they read A often
-// enough to share it among 32 or, with more than four rows of A, 64.  (M x N
-// x K in us, 16 / 32 / 64 rows of B: 1 x 4096 x 4096 4.4 / 6.2 / 8.9; 1 x
+// enough to share it among 32 or, with more than four rows of A or rows to
+// quantize on the way, 64.  (M x N x K in us, 16 / 32 / 64 rows of B: 1 x 4096 x 4096 4.4 / 6.2 / 8.9; 1 x
 // 14336 x 4096 10.0 / 9.5 / 9.3; 16 x 14336 x 4096 14.0 / 11.5 / 10.4.)
 constexpr int64_t kNarrow = 8192;
 
@@ -1089,28 +1089,29 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     return tiles<F32, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
-// Rows of A up to which the linear layer's product quantizes A itself, every
-// workgroup all of it, instead of in a launch before.  N x K of W, in us, in
-// the product / before: 4096 x 4096 5.6 / 7.0 with one row, 6.2 / 7.4 with
-// four, 6.8 / 7.6 with eight; 14336 x 4096 10.6 / 11.8, 11.9 / 12.7 and 13.6 /
-// 12.5; 4096 x 14336 11.9 / 11.5, 13.4 / 12.8 and 16.2 / 13.4 (and a launch
-// less for the host).
-constexpr int64_t kRawRows = 4;
+// Rows of A, and elements of W, up to which the linear layer's product
+// quantizes A itself, every workgroup all of it, instead of in a launch
+// before.  N x K of W, in us, in the product / before: 4096 x 4096 5.6 / 7.0
+// with one row, 6.2 / 7.4 with four, 6.8 / 7.6 with eight; 14336 x 4096 11.3 /
+// 12.9, 11.9 / 13.5 and 13.6 / 12.5; 32000 x 2048 10.9 / 13.1 and 11.3 / 13.6;
+// 4096 x 14336 11.9 / 11.5 and 13.4 / 12.8; 20480 x 5120 20.0 / 19.9 and 21.6 /
+// 19.6; 28672 x 8192 35.8 / 33.5 and 37.3 / 35.1.
+constexpr int64_t kRawRows = 4, kRawWeight = 1 << 26;
 
 template <bool F32>
 hipError_t linear_type(const MxRaw &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
                        hipStream_t st)
 {
     return b.rows <= kNarrow ? skinny<F32, 1, 1>(a, b, kp, out, row_bytes, st)
-                             : skinny<F32, 1, 2>(a, b, kp, out, row_bytes, st);
+                             : skinny<F32, 1, 4>(a, b, kp, out, row_bytes, st);
 }
 
 }  // namespace
 
-bool mx_linear_direct(const MxMatrix &x)
+bool mx_linear_direct(const MxMatrix &x, int64_t n)
 {
-    return !x.fp32 && x.rows <= kRawRows && x.cols > 0 && aligned_to(x.data, 16) && x.row_stride % 8 == 0 &&
-           x.cols % 8 == 0;
+    return !x.fp32 && x.rows <= kRawRows && x.cols > 0 && n * x.cols <= kRawWeight && aligned_to(x.data, 16) &&
+           x.row_stride % 8 == 0 && x.cols % 8 == 0;
 }
 
 hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,

@@ -323,6 +323,18 @@ def test_linear_equals_quantize_and_product():
         F.flashopt_mx_linear(view, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
+def test_linear_on_both_sides_of_its_rule():
+    """Few rows and a weight of 2^26 elements, and more: in one launch and in
+    two, the same values."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for n in ((1 << 26) // 4096, (1 << 26) // 4096 + 1):
+        w = F.flashopt_mx_quantize(torch.randn(n, 4096, generator=g, device="cuda"))
+        for m in (1, 4, 5):
+            x = _random(m, 4096, m, BF16, 2)
+            assert torch.equal(F.flashopt_mx_linear(x, w), F.flashopt_mx_product(F.flashopt_mx_quantize(x), w))
+
+
 @pytest.mark.parametrize("held", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("shape,n", [((5,), 40), ((1, 64), 33), ((3, 17, 100), 64), ((300, 257), 129), ((0, 8), 4)])
