@@ -138,7 +138,7 @@ hipError_t launch_sgd_tensor(const DevTensor &d, const SgdScalars &sc, int maste
 // ---- gradient norm and clipping (flashopt_grad.hip)
 
 // One gradient of a list; the chunk table counts kGradChunk elements (four or
-// eight 16-byte loads of each of a workgroup's 256 threads).
+// eight 16-byte loads of each of a scaling workgroup's 256 threads).
 struct GradDesc {
     void *data;
     int64_t numel;

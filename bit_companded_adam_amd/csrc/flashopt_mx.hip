@@ -203,7 +203,7 @@ __device__ __forceinline__ uint32_t column_codes(const Four<F32> *f, int j, uint
 // Codes of x along its rows (ROWS) and of its transpose (COLS), from one
 // read.  Bound by memory: 8192 x 4096 takes 16.5 us along rows (85 MB, 5.2
 // TB/s), 24 both ways (103 MB, 4.3 TB/s).  (Nontemporal stores save 2% and
-// cost 5% where the codes are read next.)  With COLS a workgroup's four wavefronts take 128 rows, so that it
+// cost 1-6% with the product that reads the codes.)  With COLS a workgroup's four wavefronts take 128 rows, so that it
 // writes 64 bytes of each column's codes and one word of its scales; those,
 // and the rows', go through LDS to be stored in such pieces.
 template <bool F32, bool ROWS, bool COLS>
@@ -374,8 +374,8 @@ __device__ __forceinline__ float scale_value(uint32_t b)
 }
 
 // One thread per eight columns.  8192 x 4096 takes 15.3 us to bf16 and 25.5 to
-// fp32 (85 and 152 MB: 5.6 and 6.0 TB/s).  (Nontemporal stores save 4 us, and
-// cost 5 where out is read next.)
+// fp32 (85 and 152 MB: 5.6 and 6.0 TB/s).  (Nontemporal stores save 4 us and
+// cost the next reader of out 5.)
 template <bool F32>
 __global__ void __launch_bounds__(kThreads)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
@@ -480,8 +480,10 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa
 // 32 consecutive bytes, and any assignment of groups to the instruction's
 // four K slots is the same sum as long as both operands and their scales
 // agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.  1 x
-// 14336 x 4096 takes 9.0 us (31 MB, 3.5 TB/s), 1 x 4096 x 4096 4.4 (8.9 MB):
-// latency, of the launch, one pass over K and the sum across wavefronts.
+// 14336 x 4096 takes 9.4 us (31 MB, 3.3 TB/s), 1 x 4096 x 4096 4.4 (8.9 MB),
+// 1 x 28672 x 8192 30 (125 MB, 4.2 TB/s): latency, of the launch, one pass
+// over K and the sum across wavefronts.  (Two steps' loads ahead are level;
+// nontemporal ones, or 64 contiguous bytes of a row in each, 10-20% slower.)
 constexpr int kSkinnyWaves = 8;
 
 struct Step {

@@ -1258,7 +1258,9 @@ def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
     """A linear layer in MXFP4 with gradients: x [..., in] and a weight
     parameter [out, in] (quantized in the call) or an MXWeight (quantized when
     it was last refreshed; the gradient goes to its param).  Work goes to the
-    current stream."""
+    current stream.  In a graph, capture forward and backward together, with no
+    eager graph of the same parameters alive (autograd would reach for that
+    one's stream)."""
     w, held = (weight.param, weight) if isinstance(weight, MXWeight) else (weight, None)
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")

@@ -448,6 +448,44 @@ def test_other_stream_and_graph():
 
 # ---------------------------------------------------- the operators together
 
+def test_captured_training_step():
+    """Forward, backward, norm, clipped step and requantization in one graph;
+    replays with new inputs, eager steps of a second copy between them, equal
+    bits.  The captured parameter is in no eager graph."""
+    require_gpu()
+    rows, cols = 130, 200
+    pa, pb = [W.init_param(rows * cols, device="cuda", seed=3).view(rows, cols).requires_grad_() for _ in range(2)]
+    a, b = [F.FlashAdamW([p.detach()], **W.HP_DEFAULT) for p in (pa, pb)]
+    wa, wb = F.MXWeight(pa), F.MXWeight(pb)
+    x, dy = torch.zeros(70, cols, dtype=BF16, device="cuda"), torch.zeros(70, rows, dtype=BF16, device="cuda")
+    grad, out = torch.zeros(rows, cols, dtype=BF16, device="cuda"), torch.zeros(2, device="cuda")
+    norm, plan = F.GradPlan([grad]), a.plan([grad], step=1, grad_scale=out[1:])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = F.mx_linear(x, wa)
+        grad.copy_(torch.autograd.grad(y, [pa], dy)[0])
+        y = y.detach()
+        norm.norm(0.01, out=out)
+        plan.launch()
+        wa.refresh()
+    for t in (1, 2, 3, 4):
+        x.copy_(_random(70, cols, t, BF16, 1))
+        dy.copy_(_random(70, rows, 40 + t, BF16, 1) * 1e-2)
+        plan.set_step(t)
+        graph.replay()
+        z = F.mx_linear(x, wb)
+        z.backward(dy)
+        eager = b.step([pb.grad], max_norm=0.01)
+        pb.grad = None
+        wb.refresh()
+        torch.cuda.synchronize()
+        assert torch.equal(y, z) and torch.equal(out, eager) and float(out[1]) < 1.0, t
+        assert torch.equal(pa, pb) and torch.equal(a.states[0].block, b.states[0].block), t
+        for q, r in ((wa.rows, wb.rows), (wa.cols, wb.cols)):
+            assert torch.equal(q.codes, r.codes) and torch.equal(q.scales, r.scales), t
+
+
 @pytest.mark.parametrize("release", [False, True])
 def test_training_steps(release):
     """MXFP4 layers, the clipped step on compressed states and new copies of
