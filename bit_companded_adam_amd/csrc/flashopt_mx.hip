@@ -473,9 +473,9 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa
         operand(a), operand(b), c, 4, 4, BYTE, static_cast<int>(sa), BYTE, static_cast<int>(sb));
 }
 
-// Few rows of A (at most 16 MT): the time is B's, read once, so nothing is
-// staged.  A workgroup takes 16 NT rows of B; its wavefronts take 256-element
-// steps of K in turn and add their sums at the end, in wavefront order.
+// Few rows of A: the time is B's, read once, so nothing is staged.  A workgroup
+// takes 16 NT rows of B and 16 MT of A; its wavefronts take 256-element steps
+// of K in turn and add their sums at the end, in wavefront order.
 // Within a step a lane holds groups 2 g and 2 g + 1 of its row (g = lane / 16):
 // 32 consecutive bytes, and any assignment of groups to the instruction's
 // four K slots is the same sum as long as both operands and their scales
@@ -564,6 +564,7 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int l16 = lane & 15, g = lane >> 4;
     const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT);
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT);
     const int steps = static_cast<int>((kp + 255) / 256);
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t n0 = tile * (16 * NT);
@@ -575,7 +576,7 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            arow[t] = 16 * t + l16;
+            arow[t] = m0 + 16 * t + l16;
             if (arow[t] >= a.rows) arow[t] = a.rows - 1;
         }
         f32x4 acc[NT][MT];
@@ -610,7 +611,7 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
                 const f32x4 u = s_acc[w][i / MT][i % MT][lane];
                 v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
             }
-            const int64_t m = 16 * (i % MT) + l16, n = n0 + 16 * (i / MT) + 4 * g;
+            const int64_t m = m0 + 16 * (i % MT) + l16, n = n0 + 16 * (i / MT) + 4 * g;
             if (m < a.rows) store4<F32>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
         }
         __syncthreads();
@@ -1041,7 +1042,7 @@ hipError_t skinny(const A &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t r
 {
     const int64_t tiles = (b.rows + 16 * NT - 1) / (16 * NT);
     const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
-    hipLaunchKernelGGL((mx_skinny_kernel<F32, MT, NT, A>), dim3(grid),
+    hipLaunchKernelGGL((mx_skinny_kernel<F32, MT, NT, A>), dim3(grid, static_cast<unsigned>((a.rows + 16 * MT - 1) / (16 * MT))),
                        dim3(kSkinnyWaves * kWaveLanes), 0, st, a, b, kp, out, row_bytes);
     return hipGetLastError();
 }
@@ -1078,6 +1079,14 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
                             : skinny<F32, 2, 1>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 4) return skinny<F32, 1, 2>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 16) return skinny<F32, 1, 4>(a, b, kp, out, row_bytes, st);
+    // More rows, but so few tiles that each workgroup may have a CU: these split
+    // K among wavefronts, which the tiles below run along (M x N x K in us, here
+    // / there: 33 x 1000 x 14000 12.7 / 21.9, 64 x 2048 x 5632 7.5 / 10.7, 64 x
+    // 4096 x 14336 22 / 32, 256 x 1000 x 14000 17.1 / 22.5, 128 x 1000 x 1000 4.2
+    // / 5.1; with two workgroups to a CU 100 x 2048 x 5632 12.1 / 10.9).
+    const int64_t m32 = (a.rows + 31) / 32;
+    if (m32 * ((b.rows + 15) / 16) <= kCus) return skinny<F32, 2, 1>(a, b, kp, out, row_bytes, st);
+    if (m32 * ((b.rows + 31) / 32) <= kCus) return skinny<F32, 2, 2>(a, b, kp, out, row_bytes, st);
     // The largest tile of which there are enough for the 256 CUs: a larger one
     // reads A and B less often, a smaller one leaves fewer CUs idle.  M x N x
     // K in us, tiles of 256 / 128: 5632 x 2048 x 8192 (176 tiles) 60.6 / 69.2;

@@ -190,7 +190,11 @@ def _pair(m, n, k, seed, low=127, high=128):
 PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 17, 129), (3, 100, 1000), (15, 33, 255), (16, 64, 4096), (17, 65, 384),
             (31, 300, 640), (32, 32, 32), (33, 64, 128), (40, 1, 100), (64, 64, 256), (65, 129, 333),
             (100, 1, 4096), (128, 128, 128), (200, 300, 500), (257, 513, 640), (1, 4099, 4096),
-            (2000, 1800, 200), (1793, 2049, 384), (3600, 3900, 130), (4097, 3500, 512)]
+            (2000, 1800, 200), (1793, 2049, 384), (3600, 3900, 130), (4097, 3500, 512),
+            # small tiles, every kind of end along K; rows that share a workgroup's K, at the rule's border
+            (300, 1100, 1), (300, 1100, 100), (301, 1101, 129), (300, 1100, 256), (299, 1100, 384), (300, 1100, 640),
+            (300, 1100, 897), (300, 1100, 1000), (70, 5000, 333), (33, 9000, 300), (1000, 40, 4100), (64, 2048, 500),
+            (64, 2049, 500), (128, 2048, 700), (129, 2048, 700), (8192, 16, 300), (8193, 16, 300)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
