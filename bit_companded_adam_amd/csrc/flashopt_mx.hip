@@ -619,7 +619,9 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
 }
 
 // Larger products: a workgroup computes a BN x BM tile of out^T, its
-// wavefronts in a WN x WM arrangement of 32 x 32 accumulator blocks.
+// wavefronts in a WN x WM arrangement of 32 x 32 accumulator blocks; with KS
+// > 1 that many such groups take a share of K each, and the first adds the
+// shares' sums in their order.
 //
 // Each K step of 256 elements is 128 bytes of every row, one cache line,
 // copied from global memory to LDS by the DMA (16 bytes to a lane, eight rows
@@ -701,22 +703,31 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_n, uint32_t t
     tn = in / width;
 }
 
-template <bool F32, int BN, int BM, int WN, int WM>
-__global__ void __launch_bounds__(WN *WM *kWaveLanes)
+template <bool F32, int BN, int BM, int WN, int WM, int KS>
+__global__ void __launch_bounds__(KS *WN *WM *kWaveLanes)
     __attribute__((amdgpu_waves_per_eu(Tile<BN, BM, WN, WM>::kWavesPerSimd)))
 mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, uint8_t *__restrict__ out,
                int64_t row_bytes)
 {
     using T = Tile<BN, BM, WN, WM>;
     constexpr int kTN = T::kTN, kTM = T::kTM;
-    __shared__ __align__(128) uint8_t s_buf[2][T::kBytes];
-    __shared__ u32x4 s_scales[2][T::kRows];
+    __shared__ __align__(128) uint8_t s_bufs[KS][2][T::kBytes];
+    __shared__ u32x4 s_scale_sets[KS][2][T::kRows];
     __shared__ __align__(16) uint8_t s_stage[T::kWaves][T::kStageRows(F32) * T::kPitch(F32)];
     const int lane = threadIdx.x & (kWaveLanes - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    const int wave = wave_all % T::kWaves, part_k = wave_all / T::kWaves;    // KS > 1: which share of K
+    const int thread = wave * kWaveLanes + lane;
     const int wn = wave % WN, wm = wave / WN, g = lane >> 5;
+    auto &s_buf = s_bufs[part_k];
+    auto &s_scales = s_scale_sets[part_k];
     const uint32_t code_stride = static_cast<uint32_t>(kp / 2), scale_stride = static_cast<uint32_t>(kp / 32);
-    const int steps = static_cast<int>((kp + 255) / 256);
+    // Steps of this share, and how far past its first one the row's last step
+    // is: with KS > 1 the last shares may run past it, repeating it as zeros
+    // (their scales are of the same row, so a NaN among them is one already).
+    const int all_steps = static_cast<int>((kp + 255) / 256), steps = (all_steps + KS - 1) / KS;
+    const int k_first = KS == 1 ? 0 : (part_k * steps < all_steps ? part_k * steps : all_steps - 1);
+    const int k_last = all_steps - 1 - k_first, k_count = KS == 1 ? steps : all_steps - part_k * steps;
     const bool half_end = (kp & 128) != 0;       // the last step has 128 elements
     const uint32_t total = tiles_n * tiles_m;
 
@@ -749,14 +760,15 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
             const int r = first + 8 * i;
             src[i] = __umul24(r < copy_last ? r : copy_last, code_stride) + (chunk ^ ((i & 1) * 64u));
         }
-        const int r = static_cast<int>(threadIdx.x) - (scale_b ? 0 : BN);
+        if constexpr (KS > 1) copy_base += static_cast<uint32_t>(k_first) * 128u;
+        const int r = thread - (scale_b ? 0 : BN);
         scale_src = __umul24(r < scale_last ? r : scale_last, scale_stride);
     };
     const uint32_t lds_to = lds_offset(s_buf) + wave * (T::kCopies * 1024);
     // Copy i of step pk into a buffer.  In a half step the second half of a
     // row, not used then, repeats the first.
     auto copy = [&](int i, int buf) {
-        const bool half = half_end && pk == steps - 1;
+        const bool half = half_end && (KS == 1 ? pk == steps - 1 : pk >= k_last);
         const uint32_t back = half ? ((chunk ^ ((i & 1) * 64u)) & 64u) : 0u;
         load_to_lds(copy_base, src[i] - back, lds_to + buf * T::kBytes + i * 1024);
     };
@@ -797,7 +809,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
         for (int x = from; x < to; ++x) {
             const int i = x / kTM, j = x % kTM;
             before(x);
-            if (q >= 2 && j == 0) v.n[i] &= mask;
+            if ((q >= 2 || KS > 1) && j == 0) v.n[i] &= mask;
             acc[i][j] = mfma32<q>(v.n[i], v.m[j], acc[i][j], sn[i], sm[j]);
             asm volatile("" : "+v"(acc[i][j]));
             __builtin_amdgcn_sched_barrier(0);
@@ -829,21 +841,24 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
             pset ^= 1;
             const uint8_t *row = scale_base + scale_src;
             if (scale_stride >= 16u) {
-                const uint32_t at = static_cast<uint32_t>(pk) * 8u, end = scale_stride - 16u;
+                const uint32_t at = static_cast<uint32_t>(k_first + pk) * 8u, end = scale_stride - 16u;
                 const uint32_t from = at < end ? at : end;
-                if (T::kRows == T::kTileThreads || threadIdx.x < T::kRows)
+                if (T::kRows == T::kTileThreads || thread < T::kRows)
                     next_scales = *reinterpret_cast<const u32x4_packed *>(row + from);
                 shift = (at - from) / 4u;
                 pending = true;
-            } else if (threadIdx.x < T::kRows) {
+            } else if (thread < T::kRows) {
                 for (uint32_t w = 0; w < 16; w += 4)
-                    reinterpret_cast<uint32_t *>(&s_scales[pset][threadIdx.x])[w / 4] =
+                    reinterpret_cast<uint32_t *>(&s_scales[pset][thread])[w / 4] =
                         w < scale_stride ? *reinterpret_cast<const uint32_t *>(row + w) : 0u;
             }
         }
-        copy_base += 128;
+        if (KS == 1 || pk < k_last) copy_base += 128;
         if (++pk == steps) {
-            if (pt + gridDim.x < total) {
+            if (KS > 1) {                        // one tile, and every share ends together
+                --pk;
+                if (pk < k_last) copy_base -= 128;
+            } else if (pt + gridDim.x < total) {
                 pk = 0;
                 pt += gridDim.x;
                 aim();
@@ -858,7 +873,7 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
         u32x4 v = next_scales;
         if (shift & 1) v = u32x4{v.y, v.z, v.w, v.w};
         if (shift & 2) v = u32x4{v.z, v.w, v.w, v.w};
-        if (threadIdx.x < T::kRows) s_scales[pset][threadIdx.x] = v;
+        if (thread < T::kRows) s_scales[pset][thread] = v;
         pending = false;
     };
 
@@ -906,11 +921,12 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
             const bool last = k == steps - 1;
             // a half step's second half counts as zeros (a branch around its
             // products would double the accumulators)
-            const uint32_t second = half_end && last ? 0u : 0xFFFFFFFFu;
-            multiply(v[0], q0, 0, kBlocks, second, [&](int x) {
+            const uint32_t whole = KS == 1 || k < k_count ? 0xFFFFFFFFu : 0u;
+            const uint32_t second = half_end && (KS == 1 ? last : k == k_count - 1) ? 0u : whole;
+            multiply(v[0], q0, 0, kBlocks, whole, [&](int x) {
                 share(kReads, kBlocks, x, [&](int c) { fetch(buf, 1, v[1], c); });
             });
-            multiply(v[1], q1, 0, kBlocks, second, [&](int x) {
+            multiply(v[1], q1, 0, kBlocks, whole, [&](int x) {
                 share(kReads, kBlocks, x, [&](int c) { fetch(buf, 2, v[0], c); });
             });
             multiply(v[0], q2, 0, kBlocks, second, [&](int x) {
@@ -927,6 +943,33 @@ mx_tile_kernel(MxIn a, MxIn b, int64_t kp, uint32_t tiles_n, uint32_t tiles_m, u
                 share(T::kCopies, kRest, x - kSplit, [&](int c) { copy(c, buf); });
             });
             advance();
+        }
+
+        if constexpr (KS > 1) {
+            // the shares' sums, added in their order by the first one's wavefronts
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            static_assert(kTN == 1 && kTM == 1 && T::kWaves * kWaveLanes * 64 <= 2 * T::kBytes, "shares of K");
+            if (part_k > 0) {
+                f32x4 *to = reinterpret_cast<f32x4 *>(&s_buf[0][0]) + wave * 4 * kWaveLanes + lane;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    to[e / 4 * kWaveLanes] = f32x4{acc[0][0][e], acc[0][0][e + 1], acc[0][0][e + 2], acc[0][0][e + 3]};
+            }
+            __syncthreads();
+            if (part_k > 0) return;
+#pragma unroll
+            for (int p = 1; p < KS; ++p) {
+                const f32x4 *from = reinterpret_cast<const f32x4 *>(&s_bufs[p][0][0]) + wave * 4 * kWaveLanes + lane;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const f32x4 y = from[e / 4 * kWaveLanes];
+                    acc[0][0][e] += y.x;
+                    acc[0][0][e + 1] += y.y;
+                    acc[0][0][e + 2] += y.z;
+                    acc[0][0][e + 3] += y.w;
+                }
+            }
         }
 
         // Block element e of a lane is m = lane % 32, n = 8 (e / 4) +
@@ -1047,7 +1090,7 @@ hipError_t skinny(const A &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t r
     return hipGetLastError();
 }
 
-template <bool F32, int BN, int BM, int WN, int WM>
+template <bool F32, int BN, int BM, int WN, int WM, int KS = 1>
 hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes, hipStream_t st)
 {
     const uint32_t tn = static_cast<uint32_t>((b.rows + BN - 1) / BN);
@@ -1057,9 +1100,10 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
     // as many workgroups as run at once (their LDS decides), each taking tiles
     // in turn; a multiple of the 8 XCDs
     constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds(F32));
+    if (KS > 1 && total > kCus) return hipErrorInvalidValue;     // one tile to a workgroup
     const unsigned grid = total < kAtOnce ? static_cast<unsigned>(total) : kAtOnce;
-    hipLaunchKernelGGL((mx_tile_kernel<F32, BN, BM, WN, WM>), dim3(grid),
-                       dim3(WN * WM * kWaveLanes), 0, st, a, b, kp, tn, tm, out, row_bytes);
+    hipLaunchKernelGGL((mx_tile_kernel<F32, BN, BM, WN, WM, KS>), dim3(grid),
+                       dim3(KS * WN * WM * kWaveLanes), 0, st, a, b, kp, tn, tm, out, row_bytes);
     return hipGetLastError();
 }
 
@@ -1069,6 +1113,12 @@ hipError_t tiles(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t
 // quantize on the way, 64.  (M x N x K in us, 16 / 32 / 64 rows of B: 1 x 4096 x 4096 4.4 / 6.2 / 8.9; 1 x
 // 14336 x 4096 10.0 / 9.5 / 9.3; 16 x 14336 x 4096 14.0 / 11.5 / 10.4.)
 constexpr int64_t kNarrow = 8192;
+
+// Elements of K from which small tiles, one or less to a CU, split it in four
+// within the workgroup.  M x N x K in us, split / not: 256 x 4096 x 14336 23.5 /
+// 34.6, 512 x 1000 x 14000 20.1 / 29.4, 256 x 2048 x 5632 10.6 / 11.0, 256 x 4096
+// x 4096 9.6 / 9.7, 256 x 4096 x 2048 7.8 / 6.6.
+constexpr int64_t kSplitInner = 6144;
 
 template <bool F32>
 hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
@@ -1097,6 +1147,10 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
     if (big >= 160) return tiles<F32, 256, 256, 4, 2>(a, b, kp, out, row_bytes, st);
     if (mid >= 160) return tiles<F32, 128, 128, 2, 2>(a, b, kp, out, row_bytes, st);
+    // a CU to each small tile leaves three of its wavefronts' places free: four
+    // shares of K take them
+    const int64_t small = ((a.rows + 63) / 64) * ((b.rows + 63) / 64);
+    if (small <= kCus && kp >= kSplitInner) return tiles<F32, 64, 64, 2, 2, 4>(a, b, kp, out, row_bytes, st);
     return tiles<F32, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 

@@ -194,7 +194,10 @@ PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 17, 129), (3, 100, 1000), (15, 33, 255)
             # small tiles, every kind of end along K; rows that share a workgroup's K, at the rule's border
             (300, 1100, 1), (300, 1100, 100), (301, 1101, 129), (300, 1100, 256), (299, 1100, 384), (300, 1100, 640),
             (300, 1100, 897), (300, 1100, 1000), (70, 5000, 333), (33, 9000, 300), (1000, 40, 4100), (64, 2048, 500),
-            (64, 2049, 500), (128, 2048, 700), (129, 2048, 700), (8192, 16, 300), (8193, 16, 300)]
+            (64, 2049, 500), (128, 2048, 700), (129, 2048, 700), (8192, 16, 300), (8193, 16, 300),
+            # K in four shares: every kind of end of the last one, and one that is left without
+            (300, 1100, 6017), (300, 1100, 6144), (300, 1101, 6272), (299, 1100, 6400), (300, 1100, 6500),
+            (300, 1100, 6700), (301, 1100, 6912), (300, 1100, 7000), (130, 5000, 12300), (1024, 1024, 6200)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -233,7 +236,8 @@ def test_product_far_scales():
             assert torch.equal(F.flashopt_mx_product(a, b, F32).double(), want), low
 
 
-@pytest.mark.parametrize("m,n,k", [(4, 50, 300), (50, 70, 300), (2000, 1800, 200), (3600, 3900, 130)])
+@pytest.mark.parametrize("m,n,k", [(4, 50, 300), (50, 70, 300), (2000, 1800, 200), (3600, 3900, 130), (300, 1100, 300),
+                                   (300, 1100, 6200)])
 def test_product_nan_scale(m, n, k):
     """A NaN scale reaches its row or column of the product and no other."""
     require_gpu()
