@@ -556,6 +556,17 @@ void fill_grad_table(const flashopt_grad *grads, int n, GradDesc *desc, int32_t 
     start[n] = acc;
 }
 
+// A staged table must not be captured: the graph would hold a copy from a slot
+// of the ring, which later calls rewrite, and its replays would follow the
+// addresses of whatever list is there then.
+flashopt_status check_not_captured(hipStream_t st)
+{
+    hipStreamCaptureStatus state = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(st, &state);
+    if (e != hipSuccess) return FLASHOPT_EHIP;
+    return state == hipStreamCaptureStatusNone ? FLASHOPT_OK : FLASHOPT_EINVAL;
+}
+
 // The arguments that a norm and a clip share, after the list's.
 flashopt_status check_norm(double max_norm, const float *out)
 {
@@ -583,6 +594,7 @@ flashopt_status grad_call(const flashopt_grad *grads, int n, double max_norm, bo
         fill_grad_table(grads, n, desc, start);
         return hip_status(flashopt::launch_grad_args(desc, start, n, chunks, max_norm, clip, sums, out, st));
     }
+    if ((cs = check_not_captured(st)) != FLASHOPT_OK) return cs;
     GradDesc *table = reinterpret_cast<GradDesc *>(sums + 1);
     const flashopt_status ss = stage_copy(table, grad_table_bytes(n), st, [&](void *host) {
         GradDesc *d = static_cast<GradDesc *>(host);
@@ -996,7 +1008,10 @@ flashopt_status flashopt_grad_plan(const flashopt_grad *grads, int n_tensors, vo
         const flashopt_status ds = check_disjoint(grads, n_tensors);
         if (ds == FLASHOPT_EHIP) return ds;
         out.overlap = ds != FLASHOPT_OK;
-        const flashopt_status ss = stage_copy(plan, need, static_cast<hipStream_t>(stream), [&](void *host) {
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        flashopt_status ss = check_not_captured(st);
+        if (ss != FLASHOPT_OK) return ss;
+        ss = stage_copy(plan, need, st, [&](void *host) {
             GradSums *sums = static_cast<GradSums *>(host);
             std::memset(sums, 0, sizeof(GradSums));
             GradDesc *d = reinterpret_cast<GradDesc *>(sums + 1);

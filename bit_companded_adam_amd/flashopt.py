@@ -599,10 +599,8 @@ _grad_workspaces = {}
 
 def _grad_workspace(n: int, device) -> torch.Tensor:
     """For the current stream."""
-    need = _GRAD_SHORT_BYTES if 0 < n <= 64 else max(16, flashopt_grad_workspace_bytes(n))
+    need = _GRAD_SHORT_BYTES if 0 < n <= _GRAD_SHORT else max(16, flashopt_grad_workspace_bytes(n))
     if torch.cuda.is_current_stream_capturing():
-        if n > 64:
-            raise ValueError("a list of more than 64 gradients is not captured as it is: use a GradPlan")
         return torch.zeros(need, dtype=torch.uint8, device=device)
     key = (device.index, _stream(None))
     ws = _grad_workspaces.get(key)
@@ -611,7 +609,8 @@ def _grad_workspace(n: int, device) -> torch.Tensor:
     return ws
 
 
-_GRAD_SHORT_BYTES = 128 + 512 * 8       # flashopt_grad_workspace_bytes of up to 64 tensors
+_GRAD_SHORT = 64                        # gradients that travel in the kernel arguments
+_GRAD_SHORT_BYTES = 128 + 512 * 8       # flashopt_grad_workspace_bytes of up to that many
 
 
 def _grad_out(out, device) -> torch.Tensor:
@@ -626,6 +625,8 @@ def _grad_call(name, grads, max_norm, out, workspace, stream):
     if device is None:
         device = out.device if out is not None else torch.device("cuda", torch.cuda.current_device())
     with _on(device, stream):
+        if len(arr) > _GRAD_SHORT and torch.cuda.is_current_stream_capturing():
+            raise ValueError("a list of more than 64 gradients is not captured as it is: use a GradPlan")
         out = _grad_out(out, device)
         ws = _grad_workspace(len(arr), device) if workspace is None else workspace
         if ws.device != device:
@@ -687,6 +688,8 @@ class GradPlan:
         arr, device = grad_array(self.grads)
         self.device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
         with _on(self.device, stream):
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError("a GradPlan is made before the capture, not in it")
             self.buffer = torch.empty(max(16, flashopt_grad_plan_bytes(len(arr))), dtype=torch.uint8,
                                       device=self.device)
             self.info = flashopt_grad_plan(arr, self.buffer)

@@ -443,8 +443,8 @@ size_t flashopt_grad_workspace_bytes(int n_tensors);
  *   out       DEVICE fp32[2], written; out + 1 is a grad_scale for the steps
  * A list of at most 64 tensors travels in the kernel arguments, and the call
  * can be captured into a graph.  A longer one is staged through a pinned
- * buffer of the library (see flashopt_adamw_step) and must not be captured:
- * use a plan.
+ * buffer of the library (see flashopt_adamw_step) and is refused on a stream
+ * that is being captured (EINVAL): use a plan.
  * Errors: EINVAL (n_tensors < 0, NULL grads/out, numel < 0, NULL data with
  * numel > 0, fp32 not 0 or 1, max_norm negative or NaN, more than 2^31 - 1
  * chunks of 8192 elements), EALIGN (data not aligned to its element, out to
@@ -469,7 +469,8 @@ flashopt_status flashopt_grad_clip(const flashopt_grad *grads, int n_tensors, do
  * enqueue kernels, with max_norm in their arguments (a captured launch keeps
  * it).  Launches that share a plan must be ordered.
  * Errors: as above (EWORKSPACE: plan NULL or too small; EINVAL also for a
- * NULL info, and from _clip for a list with overlapping gradients). */
+ * NULL info, from flashopt_grad_plan on a stream that is being captured, and
+ * from _clip for a list with overlapping gradients). */
 size_t flashopt_grad_plan_bytes(int n_tensors);
 typedef struct {
     int32_t n_tensors;        /* tensors in the plan's table                  */
