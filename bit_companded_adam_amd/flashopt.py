@@ -15,6 +15,7 @@ import contextlib
 import ctypes
 import math
 import os
+import threading
 from array import array
 
 import torch
@@ -591,10 +592,13 @@ def flashopt_grad_workspace_bytes(n_tensors: int) -> int:
     return lib().flashopt_grad_workspace_bytes(n_tensors)
 
 
-# One zeroed workspace per device and stream: launches on one stream are
-# ordered, and each leaves its workspace ready for the next.  A captured
-# launch gets one of its own (replays may run next to anything else).
-_grad_workspaces = {}
+# One zeroed workspace per host thread, device and stream: a thread's launches
+# on one stream are ordered, and each leaves its workspace ready for the next.
+# (Two threads' calls on one stream are not: a long list's table copy and its
+# kernels are enqueued one after another, and another thread's copy into the
+# same workspace could fall between them.)  A captured launch gets one of its
+# own (replays may run next to anything else).
+_grad_workspaces = threading.local()
 
 
 def _grad_workspace(n: int, device) -> torch.Tensor:
@@ -602,10 +606,14 @@ def _grad_workspace(n: int, device) -> torch.Tensor:
     need = _GRAD_SHORT_BYTES if 0 < n <= _GRAD_SHORT else max(16, flashopt_grad_workspace_bytes(n))
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(need, dtype=torch.uint8, device=device)
+    try:
+        mine = _grad_workspaces.mine
+    except AttributeError:
+        mine = _grad_workspaces.mine = {}
     key = (device.index, _stream(None))
-    ws = _grad_workspaces.get(key)
+    ws = mine.get(key)
     if ws is None or ws.numel() < need:
-        ws = _grad_workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=device)
+        ws = mine[key] = torch.zeros(need, dtype=torch.uint8, device=device)
     return ws
 
 

@@ -426,9 +426,11 @@ typedef struct {
 
 /* Device workspace bytes of flashopt_grad_norm / flashopt_grad_clip.  The
  * caller ZEROES the workspace once, before its first use; every call leaves
- * it ready for the next.  Calls that share a workspace must be ordered (one
- * stream); calls that may overlap, captured graphs among them, need one
- * each.  Returns 0 for n_tensors <= 0. */
+ * it ready for the next.  Calls that share a workspace must be ordered, on
+ * the device (one stream) and on the host (a call enqueues up to three
+ * operations, so two threads' calls on one stream may interleave); calls that
+ * may overlap, captured graphs among them, need one each.  Returns 0 for
+ * n_tensors <= 0. */
 size_t flashopt_grad_workspace_bytes(int n_tensors);
 
 /* The global norm of a list of gradients, bf16 and fp32 mixed, in one pass

@@ -1,11 +1,13 @@
 """Norm and clipping called in the less usual ways: with the caller's own
 workspace under capture, and from several host threads at once."""
 import ctypes
+import threading
 
 import pytest
 import torch
 
 from bit_companded_adam_amd import flashopt as F
+from bit_companded_adam_amd import workloads as W
 from tests._gpu import require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +47,44 @@ def test_capture_of_a_long_list_with_a_workspace_is_refused():
         assert out[0].item() == float(torch.tensor(64 * 8 * 4.0).sqrt())
         assert again[0].item() == float(torch.tensor(65 * 8 * 4.0).sqrt())
     assert all((g == 2.0).all() for g in grads) and not buf.any()
+
+
+def test_threads_on_one_stream():
+    """Norms and clips of lists of different lengths, each with its table in
+    a workspace, from several host threads on the default stream: every thread
+    sees its own list."""
+    require_gpu()
+    sizes = (70, 201, 90, 3, 130)
+    lists = [[W.make_grad(500 + 37 * i, k, device="cuda", stream_id=i) for i in range(n)]
+             for k, n in enumerate(sizes)]
+    copies = [[g.clone() for g in grads] for grads in lists]
+    bounds = [0.9 ** (i + 1) * float(F.flashopt_grad_norm(lists[0])[0]) for i in range(12)]
+
+    def run(grads):                      # norm and clip in turn, every clip scaling
+        out = []
+        for bound in bounds:
+            out += [F.flashopt_grad_norm(grads, bound), F.flashopt_grad_clip(grads, bound)]
+        return out
+    want = [run(grads) for grads in copies]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(lists), []
+    start = threading.Barrier(len(lists))
+
+    def work(k):
+        try:
+            start.wait(30)
+            got[k] = run(lists[k])
+        except Exception as e:           # raised again below
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(lists))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for k in range(len(lists)):
+        assert all(torch.equal(a, b) for a, b in zip(got[k], want[k])), k
+        # the three tensors' norm, a ninth of the first list's, is below the last bound, 0.28 of it
+        assert (float(got[k][-1][1]) < 1.0) == (sizes[k] > 3)
+        assert all(torch.equal(a, b) for a, b in zip(lists[k], copies[k])), k
