@@ -1251,11 +1251,12 @@ class _MXLinear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        if ctx.weight is not None and ctx.weight.version != ctx.version:
+        need_x, need_w = ctx.needs_input_grad[:2]
+        # only the input's gradient reads the weight's copies
+        if need_x and ctx.weight is not None and ctx.weight.version != ctx.version:
             raise RuntimeError("the MXWeight was refreshed between the forward and the backward pass")
         saved = list(ctx.saved_tensors)
         x_cols, w_cols = [None if k is None else MXTensor._over(saved.pop(0), *k) for k in ctx.kept]
-        need_x, need_w = ctx.needs_input_grad[:2]
         flat = _flat(dy)
         layout = "both" if need_x and need_w else "rows" if need_x else "cols"
         q = flashopt_mx_quantize(flat, layout)
