@@ -1081,6 +1081,12 @@ class MXTensor:
             self._scales = self._buffer[16 * self.rows * width:].view(self.rows, width)
         return self._scales
 
+    def _written(self):
+        """Tell autograd that the codes and scales change under it, as an
+        in-place operation does: a backward pass that has kept them refuses."""
+        for t in (self._codes, self._scales) if self._buffer is None else (self._buffer,):
+            torch.autograd.graph.increment_version(t)
+
     def __repr__(self):
         return f"MXTensor({self.rows} x {self.cols}, {self.device})"
 
@@ -1123,6 +1129,7 @@ def _mx_target(q, rows, cols, device):
     if (q.rows, q.cols) != (rows, cols):
         raise ValueError(f"out is {q.rows} x {q.cols}, {rows} x {cols} needed")
     _same_device(device, q, "out")
+    q._written()
     return q
 
 

@@ -29,3 +29,27 @@ def test_refresh_does_not_touch_a_weight_gradient():
         w.mul_(2)
     weight.refresh()
     assert torch.equal(torch.autograd.grad(y, w, dy)[0], want)
+
+
+def test_copies_rewritten_through_quantize_are_refused():
+    """The copies written by another call than refresh(), in the MXWeight's own
+    tensors or in others over the same memory."""
+    require_gpu()
+    x, dy = _random(40, 100, 1), _random(40, 50, 2)
+    w = _random(50, 100, 3)
+    weight = F.MXWeight(w)
+    alias = F.MXTensor(weight.cols.codes, weight.cols.scales, 100, 50)
+    for layout, out in (("both", (weight.rows, weight.cols)), ("cols", weight.cols), ("cols", alias)):
+        y = F.mx_linear(x.clone().requires_grad_(), weight)
+        F.flashopt_mx_quantize(w, layout, out)
+        with pytest.raises(RuntimeError, match="modified"):
+            y.backward(dy)
+    y = F.mx_linear(x.clone().requires_grad_(), weight)
+    F.flashopt_mx_quantize(w, out=weight.rows)               # which no backward pass reads
+    y.backward(dy)
+    with torch.inference_mode():                             # buffers without versions
+        served = F.MXWeight(w)
+        served.refresh()
+        assert torch.equal(F.mx_linear(x, served), F.mx_linear(x, weight))
+    served.refresh()
+    assert torch.equal(served.rows.codes, weight.rows.codes)
