@@ -1038,7 +1038,7 @@ class MXTensor:
     """A rows x cols matrix in MXFP4: uint8 tensors of packed codes (two to a
     byte, rows padded to 128 elements) and of E8M0 scales (one for 32)."""
 
-    __slots__ = ("rows", "cols", "device", "code_ptr", "scale_ptr", "_codes", "_scales", "_buffer")
+    __slots__ = ("rows", "cols", "device", "code_ptr", "scale_ptr", "_codes", "_scales", "_buffer", "replayed")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         blocks = rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
@@ -1051,7 +1051,7 @@ class MXTensor:
             raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
         self.rows, self.cols, self.device = rows, cols, codes.device
         self.code_ptr, self.scale_ptr = codes.data_ptr(), scales.data_ptr()
-        self._codes, self._scales, self._buffer = codes, scales, None
+        self._codes, self._scales, self._buffer, self.replayed = codes, scales, None, False
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "MXTensor":
@@ -1065,6 +1065,7 @@ class MXTensor:
         q.rows, q.cols, q.device, q._buffer, q._codes, q._scales = rows, cols, buffer.device, buffer, None, None
         q.code_ptr = buffer.data_ptr()
         q.scale_ptr = q.code_ptr + 64 * rows * ((cols + MX_BLOCK - 1) // MX_BLOCK)
+        q.replayed = False
         return q
 
     @property
@@ -1083,9 +1084,13 @@ class MXTensor:
 
     def _written(self):
         """Tell autograd that the codes and scales change under it, as an
-        in-place operation does: a backward pass that has kept them refuses."""
+        in-place operation does: a backward pass that has kept them refuses.
+        From a captured write on they change with replays, which neither
+        autograd nor anything else on the host sees."""
         for t in (self._codes, self._scales) if self._buffer is None else (self._buffer,):
             torch.autograd.graph.increment_version(t)
+        if torch.cuda.is_current_stream_capturing():
+            self.replayed = True
 
     def __repr__(self):
         return f"MXTensor({self.rows} x {self.cols}, {self.device})"
@@ -1213,7 +1218,9 @@ class MXWeight:
     """A weight parameter (bf16 or fp32, [out, in]) with its MXFP4 copies:
     `rows` for the forward product, `cols` (transposed) for the input's
     gradient.  refresh() requantizes into the same buffers, after each step of
-    the optimizer."""
+    the optimizer; between a forward and a backward pass that reads them the
+    backward pass refuses.  Replays of a captured refresh() pass unnoticed, so
+    after the capture each eager forward keeps its own transposed copy."""
 
     def __init__(self, param: torch.Tensor):
         self.param = param
@@ -1244,6 +1251,10 @@ class _MXLinear(torch.autograd.Function):
             w_rows, w_cols = q if need_x else (q, None)
         else:
             w_rows, w_cols = weight.rows, weight.cols
+            if need_x and w_cols.replayed and not torch.cuda.is_current_stream_capturing():
+                # a replay may rewrite the copy before the backward pass: keep
+                # one of this call's own (captured, both are in one order)
+                w_cols, weight = MXTensor._over(w_cols._buffer.clone(), w_cols.rows, w_cols.cols), None
         flat = _flat(x)
         q = flashopt_mx_quantize(flat, "both" if need_w else "rows")
         x_rows, x_cols = q if need_w else (q, None)

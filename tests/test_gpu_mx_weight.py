@@ -53,3 +53,37 @@ def test_copies_rewritten_through_quantize_are_refused():
         assert torch.equal(F.mx_linear(x, served), F.mx_linear(x, weight))
     served.refresh()
     assert torch.equal(served.rows.codes, weight.rows.codes)
+
+
+@pytest.mark.parametrize("how", ["refresh", "quantize"])
+def test_replayed_refresh_between_forward_and_backward(how):
+    """A replay rewrites the copies without the host's knowledge: an eager
+    backward pass still multiplies by those of its own forward pass."""
+    require_gpu()
+    dy = _random(40, 50, 2)
+    w = _random(50, 100, 3)
+    weight = F.MXWeight(w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if how == "refresh":
+            weight.refresh()
+        else:
+            F.flashopt_mx_quantize(w, "both", (weight.rows, weight.cols))
+    seen = []
+    for i in range(4):
+        w.copy_(_random(50, 100, 10 + i))
+        graph.replay()
+        x = _random(40, 100, 20 + i)
+        a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+        want = torch.autograd.grad(F.mx_linear(a, w.clone()), a, dy)[0]
+        y = F.mx_linear(b, weight)
+        w.copy_(_random(50, 100, 30 + i))
+        graph.replay()
+        again = F.mx_linear(x, weight)
+        y.backward(dy)
+        torch.cuda.synchronize()
+        assert torch.equal(b.grad, want), i
+        assert torch.equal(again, F.mx_linear(x, w)) and not torch.equal(again, y), i
+        seen.append(want)
+    assert not torch.equal(seen[0], seen[1])
