@@ -1244,8 +1244,9 @@ class _MXLinear(torch.autograd.Function):
     4 bits."""
 
     @staticmethod
-    def forward(ctx, x, w, weight):
-        need_x, need_w = ctx.needs_input_grad[:2]
+    def forward(ctx, x, w, weight, grad):
+        # needs_input_grad is set where gradients are off altogether, too
+        need_x, need_w = [need and grad for need in ctx.needs_input_grad[:2]]
         if weight is None:
             q = flashopt_mx_quantize(w, "both" if need_x else "rows")
             w_rows, w_cols = q if need_x else (q, None)
@@ -1281,7 +1282,7 @@ class _MXLinear(torch.autograd.Function):
         dy_rows, dy_cols = q if layout == "both" else (q, q)
         dx = flashopt_mx_product(dy_rows, w_cols, ctx.x_dtype).view(ctx.x_shape) if need_x else None
         dw = flashopt_mx_product(dy_cols, x_cols, ctx.w_dtype) if need_w else None
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
@@ -1294,4 +1295,4 @@ def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
     w, held = (weight.param, weight) if isinstance(weight, MXWeight) else (weight, None)
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")
-    return _MXLinear.apply(x, w, held)
+    return _MXLinear.apply(x, w, held, torch.is_grad_enabled())
