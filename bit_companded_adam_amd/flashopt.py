@@ -570,6 +570,11 @@ def grad_array(grads):
         wide = [_GRAD_FP32[g.dtype] for g in grads]
     except KeyError as e:
         raise ValueError(f"gradients must be bf16 or fp32, got {e.args[0]}") from None
+    except AttributeError:
+        missing = [i for i, g in enumerate(grads) if g is None]
+        if not missing:
+            raise
+        raise ValueError(f"gradient {missing[0]} is None: leave out parameters without one") from None
     devices = {g.device for g in grads}
     device = next(iter(devices))
     if any(d.type != "cuda" for d in devices):

@@ -1,6 +1,7 @@
 """The binding's side of the gradient norm, without a GPU."""
 import threading
 
+import pytest
 import torch
 
 from bit_companded_adam_amd import flashopt as F
@@ -27,3 +28,11 @@ def test_a_workspace_belongs_to_one_host_thread(monkeypatch):
     assert len({ws[0].data_ptr() for ws in got.values()}) == 4
     grown = F._grad_workspace(5000, device)
     assert grown.numel() >= F.flashopt_grad_workspace_bytes(5000) and not grown.any()
+
+
+@pytest.mark.parametrize("call", [lambda g: F.flashopt_grad_norm(g), lambda g: F.flashopt_grad_clip(g, 1.0),
+                                  lambda g: F.GradPlan(g)])
+def test_a_missing_gradient_is_named(call):
+    """Parameters that took no part in the loss have a .grad of None."""
+    with pytest.raises(ValueError, match="gradient 1 is None"):
+        call([torch.zeros(8), None, torch.zeros(3)])
