@@ -652,6 +652,24 @@ flashopt_status check_codes(const void *codes, const void *scales, int64_t rows,
     return aligned(codes, 16) && aligned(scales, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
 }
 
+// Whether two of the buffers that a quantization writes share memory (a buffer
+// of NULL is not written).
+bool outputs_overlap(const void *codes, const void *scales, const void *codes_t, const void *scales_t,
+                     int64_t rows, int64_t cols)
+{
+    const struct { uintptr_t first; size_t bytes; } b[4] = {
+        {reinterpret_cast<uintptr_t>(codes), flashopt_mx_code_bytes(rows, cols)},
+        {reinterpret_cast<uintptr_t>(scales), flashopt_mx_scale_bytes(rows, cols)},
+        {reinterpret_cast<uintptr_t>(codes_t), flashopt_mx_code_bytes(cols, rows)},
+        {reinterpret_cast<uintptr_t>(scales_t), flashopt_mx_scale_bytes(cols, rows)}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (b[i].first && b[j].first && b[i].first < b[j].first + b[j].bytes &&
+                b[j].first < b[i].first + b[i].bytes)
+                return true;
+    return false;
+}
+
 // Most elements that a product sums over: its kernels multiply rows of a tile
 // by a row's bytes of codes in 24 bits.
 constexpr int64_t kMaxInner = (int64_t{1} << 25) - 128;
@@ -1056,6 +1074,7 @@ flashopt_status flashopt_mx_quantize(const void *x, int x_fp32, int64_t rows, in
         return FLASHOPT_EINVAL;
     if (codes && (cs = check_codes(codes, scales, rows, cols)) != FLASHOPT_OK) return cs;
     if (codes_t && (cs = check_codes(codes_t, scales_t, cols, rows)) != FLASHOPT_OK) return cs;
+    if (outputs_overlap(codes, scales, codes_t, scales_t, rows, cols)) return FLASHOPT_EINVAL;
     return hip_status(flashopt::launch_mx_quantize(
         in, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), static_cast<uint8_t *>(codes_t),
         static_cast<uint8_t *>(scales_t), static_cast<hipStream_t>(stream)));

@@ -493,7 +493,8 @@ flashopt_status flashopt_grad_plan_clip(const flashopt_grad_plan_info *info, voi
  *   codes   R rows of Cp / 2 bytes, the even column in the low nibble
  *   scales  R rows of Cp / 32 bytes
  * Padding is code 0 and scale byte 0.  codes 16-byte aligned, scales 4-byte.
- * Rows and columns: 0 to 2^31 - 1 (memory ends earlier).
+ * Rows and columns: 0 to 2^31 - 1 (memory ends earlier).  What a call writes
+ * shares no memory with what it reads, unless the call says otherwise.
  *
  * Bytes of an R x C matrix's codes and of its scales (0 for an empty one): */
 size_t flashopt_mx_code_bytes(int64_t rows, int64_t cols);
@@ -509,8 +510,8 @@ size_t flashopt_mx_scale_bytes(int64_t rows, int64_t cols);
  *                      columns; or both NULL.  Both pairs come from one read
  *   x                  aligned to its element; row_stride >= 0
  * Errors: EINVAL (negative or too large sizes, x_fp32 not 0 or 1, NULL x, no
- * or half an output pair, 2^24 tiles of 32 x 256 or more), EALIGN, EHIP.  An
- * empty matrix is a no-op. */
+ * or half an output pair, outputs that overlap, 2^24 tiles of 32 x 256 or
+ * more), EALIGN, EHIP.  An empty matrix is a no-op. */
 flashopt_status flashopt_mx_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols,
                                      int64_t row_stride, void *codes, void *scales,
                                      void *codes_t, void *scales_t, void *stream);
