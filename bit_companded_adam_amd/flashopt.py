@@ -858,7 +858,7 @@ RELEASE_STREAMS = 4
 
 
 def attach_grad_release(opt, params, batch_below: int = RELEASE_BATCH_BELOW,
-                        streams: int = RELEASE_STREAMS):
+                        streams: int = RELEASE_STREAMS, grad_scale=None):
     """Gradient release: register a post-accumulate-grad hook on every
     parameter that runs that tensor's step as soon as its gradient is
     complete and then frees the gradient, so a full set of gradients is never
@@ -881,7 +881,14 @@ def attach_grad_release(opt, params, batch_below: int = RELEASE_BATCH_BELOW,
     gradient's memory is kept until its side stream has used it
     (record_stream), and when the backward pass ends the backward stream
     waits for every side stream, so later work sees the updated parameters.
+
+    grad_scale: a device fp32 tensor whose first element multiplies every
+    gradient as its step loads it, say the reciprocal of a loss scale.  It may
+    be rewritten between backward passes, on the backward stream.  (A clipping
+    factor is no use here: it is known when every gradient is, and by then the
+    steps have run.)
     Returns the hook handles."""
+    _scale_ptr(grad_scale, opt.device)
     index = {id(p): i for i, p in enumerate(params)}
     pending = []
     side = [torch.cuda.Stream(device=opt.device) for _ in range(streams)] if streams > 1 else []
@@ -893,7 +900,7 @@ def attach_grad_release(opt, params, batch_below: int = RELEASE_BATCH_BELOW,
         if pending:
             idx, grads = zip(*pending)
             pending.clear()
-            opt.step_tensors(idx, grads)
+            opt.step_tensors(idx, grads, grad_scale=grad_scale)
         if side:
             cur = torch.cuda.current_stream(opt.device)
             for s in side:
@@ -910,10 +917,10 @@ def attach_grad_release(opt, params, batch_below: int = RELEASE_BATCH_BELOW,
             s = side[turn[0] % len(side)]
             turn[0] += 1
             s.wait_stream(torch.cuda.current_stream(opt.device))
-            opt.step_tensor(i, p.grad, stream=s)
+            opt.step_tensor(i, p.grad, stream=s, grad_scale=grad_scale)
             p.grad.record_stream(s)
         else:
-            opt.step_tensor(i, p.grad)
+            opt.step_tensor(i, p.grad, grad_scale=grad_scale)
         p.grad = None
 
     return [p.register_post_accumulate_grad_hook(hook) for p in params]
