@@ -1154,14 +1154,22 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
     return tiles<F32, 64, 64, 2, 2>(a, b, kp, out, row_bytes, st);
 }
 
-// Rows of A, and elements of W, up to which the linear layer's product
-// quantizes A itself, every workgroup all of it, instead of in a launch
-// before.  N x K of W, in us, in the product / before: 4096 x 4096 5.6 / 7.0
-// with one row, 6.2 / 7.4 with four, 6.8 / 7.6 with eight; 14336 x 4096 11.3 /
-// 12.9, 11.9 / 13.5 and 13.6 / 12.5; 32000 x 2048 10.9 / 13.1 and 11.3 / 13.6;
-// 4096 x 14336 11.9 / 11.5 and 13.4 / 12.8; 20480 x 5120 20.0 / 19.9 and 21.6 /
-// 19.6; 28672 x 8192 35.8 / 33.5 and 37.3 / 35.1.
-constexpr int64_t kRawRows = 4, kRawWeight = 1 << 26;
+// Up to four rows of bf16 the linear layer's product may quantize A itself,
+// every workgroup all of it, instead of in a launch before.  That costs K for
+// each workgroup that a CU runs one after another, and saves a launch, so the
+// rule bounds the product of the two; workgroups of 64 rows of W, which quantize
+// as much for more of it, by less than those of 16.  N x K of W, in us, in the
+// product / before, one row and four: 4096 x 4096 4.8 / 6.3 and 5.4 / 6.7, 4096 x
+// 8192 7.7 / 8.7 and 8.7 / 9.5, 4096 x 10240 9.0 / 8.8 and 10.0 / 9.6, 4096 x
+// 14336 11.9 / 10.8 and 13.0 / 12.1; two workgroups to a CU: 8192 x 4096 7.4 / 7.8
+// and 8.4 / 8.5, 8192 x 5120 8.9 / 8.8 and 10.2 / 9.6, 8192 x 8192 13.7 / 12.5 and
+// 15.7 / 13.7; of 64 rows: 14336 x 4096 10.4 / 11.4 and 11.0 / 12.2, 16384 x 7168
+// 16.1 / 16.3 and 16.6 / 17.2; two of them: 32000 x 2048 9.7 / 11.6 and 10.2 /
+// 12.2, 18000 x 4096 15.9 / 14.5 and 17.6 / 15.6, 20480 x 5120 19.4 / 16.7 and
+// 20.5 / 17.9.  (Of the sizes tried the rule is wrong just above 8192 rows with a
+// long K, where workgroups of 64 leave half of the CUs idle: one row of 8200 x
+// 4096 10.1 / 9.8, of 8200 x 7168 15.3 / 12.8, but of 9000 x 6144 13.5 / 14.1.)
+constexpr int64_t kRawRows = 4, kRawNarrow = 8192, kRawWide = 7168;
 
 template <bool F32>
 hipError_t linear_type(const MxRaw &a, const MxIn &b, int64_t kp, uint8_t *out, int64_t row_bytes,
@@ -1175,8 +1183,10 @@ hipError_t linear_type(const MxRaw &a, const MxIn &b, int64_t kp, uint8_t *out, 
 
 bool mx_linear_direct(const MxMatrix &x, int64_t n)
 {
-    return !x.fp32 && x.rows <= kRawRows && x.cols > 0 && n * x.cols <= kRawWeight && aligned_to(x.data, 16) &&
-           x.row_stride % 8 == 0 && x.cols % 8 == 0;
+    const bool narrow = n <= kNarrow;
+    const int64_t rows_at_once = kCus * (narrow ? 16 : 64), turns = (n + rows_at_once - 1) / rows_at_once;
+    return !x.fp32 && x.rows <= kRawRows && x.cols > 0 && x.cols * turns <= (narrow ? kRawNarrow : kRawWide) &&
+           aligned_to(x.data, 16) && x.row_stride % 8 == 0 && x.cols % 8 == 0;
 }
 
 hipError_t launch_mx_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
