@@ -1129,6 +1129,12 @@ hipError_t product_type(const MxIn &a, const MxIn &b, int64_t kp, uint8_t *out, 
                             : skinny<F32, 2, 1>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 4) return skinny<F32, 1, 2>(a, b, kp, out, row_bytes, st);
     if (a.rows <= 16) return skinny<F32, 1, 4>(a, b, kp, out, row_bytes, st);
+    // (17 to 32 rows over more than 8192 of B take the tiles.  The tiles / 64
+    // rows of B to a skinny workgroup, from cache and, with weights in turn that
+    // no cache holds, from memory: 32 x 14336 x 4096 10.9 / 11.3 and 16.0 / 12.8,
+    // 32 x 28672 x 8192 27.7 / 36.7 and 39.2 / 40.0, 32 x 32000 x 2048 9.7 / 13.0
+    // and 13.2 / 14.7, 17 x 9000 x 2048 5.4 / 6.1 and 9.1 / 7.2.)
+    //
     // More rows, but so few tiles that each workgroup may have a CU: these split
     // K among wavefronts, which the tiles below run along (M x N x K in us, here
     // / there: 33 x 1000 x 14000 12.7 / 21.9, 64 x 2048 x 5632 7.5 / 10.7, 64 x
