@@ -479,11 +479,13 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa
 // Within a step a lane holds groups 2 g and 2 g + 1 of its row (g = lane / 16):
 // 32 consecutive bytes, and any assignment of groups to the instruction's
 // four K slots is the same sum as long as both operands and their scales
-// agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.  1 x
-// 14336 x 4096 takes 9.4 us (31 MB, 3.3 TB/s), 1 x 4096 x 4096 4.4 (8.9 MB),
-// 1 x 28672 x 8192 30 (125 MB, 4.2 TB/s): latency, of the launch, one pass
-// over K and the sum across wavefronts.  (Two steps' loads ahead are level;
-// nontemporal ones, or 64 contiguous bytes of a row in each, 10-20% slower.)
+// agree.  Eight wavefronts, so that 4096 rows of B still fill the chip.  With
+// the weight in cache from the call before / with weights in turn that no cache
+// holds, 1 x 4096 x 4096 takes 3.6 / 5.0 us (8.9 MB), 1 x 14336 x 4096 8.4 / 9.4
+// (31 MB, 3.7 / 3.3 TB/s), 1 x 28672 x 8192 26.5 / 28.1 (125 MB, 4.7 / 4.5 TB/s):
+// latency, of the launch, one pass over K and the sum across wavefronts.  (Two
+// steps' loads ahead are level; nontemporal ones, or 64 contiguous bytes of a
+// row in each, 10-20% slower.)
 constexpr int kSkinnyWaves = 8;
 
 struct Step {
@@ -640,8 +642,8 @@ mx_skinny_kernel(A a, MxIn b, int64_t kp, uint8_t *__restrict__ out, int64_t row
 //
 // What bounds it: 8192^3 takes 256-261 us (4.2-4.3 PFLOP/s) on random codes
 // and 190 us (5.8) on zeros, where the bare instructions on registers reach 6.4
-// and 9.1 PFLOP/s: random operands cost clock, the rest is waiting for copies
-// (150 us without them) and about 5 us a tile for storing out, while every CU
+// and 9.1 PFLOP/s, 172 and 121 us: random operands cost clock, the rest is
+// waiting for copies and about 5 us a tile for storing out, while every CU
 // stores.  Four wavefronts of 128 x 128 instead of eight of 64 x 128 (a third
 // fewer LDS reads, accumulators in AGPRs) take 275 us: nothing runs beside a
 // wavefront's own waits then.
