@@ -1238,6 +1238,8 @@ class MXWeight:
         self.param = param
         self.version = 0
         self.rows, self.cols = flashopt_mx_quantize(param.detach(), "both")
+        if torch.cuda.is_current_stream_capturing():        # replays write these as well
+            self.rows.replayed = self.cols.replayed = True
 
     def refresh(self, stream=None):
         self.version += 1

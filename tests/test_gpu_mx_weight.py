@@ -87,3 +87,25 @@ def test_replayed_refresh_between_forward_and_backward(how):
         assert torch.equal(again, F.mx_linear(x, w)) and not torch.equal(again, y), i
         seen.append(want)
     assert not torch.equal(seen[0], seen[1])
+
+
+def test_weight_made_in_a_capture():
+    """Its copies are the graph's, written by every replay."""
+    require_gpu()
+    dy, x = _random(40, 50, 2), _random(40, 100, 4)
+    w = _random(50, 100, 3)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        weight = F.MXWeight(w)
+    for i in range(3):
+        w.copy_(_random(50, 100, 10 + i))
+        graph.replay()
+        a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+        want = torch.autograd.grad(F.mx_linear(a, w.clone()), a, dy)[0]
+        y = F.mx_linear(b, weight)
+        w.copy_(_random(50, 100, 30 + i))
+        graph.replay()
+        y.backward(dy)
+        torch.cuda.synchronize()
+        assert torch.equal(b.grad, want), i

@@ -23,6 +23,7 @@ def calls(monkeypatch):
         return torch.zeros(a.rows, b.rows, dtype=dtype)
     monkeypatch.setattr(F, "flashopt_mx_quantize", quantize)
     monkeypatch.setattr(F, "flashopt_mx_product", product)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return seen
 
 
