@@ -694,7 +694,8 @@ class GradPlan:
     """Norm and clipping of a fixed list of gradient buffers, of any length,
     with the table staged once: norm() and clip() enqueue kernels only and can
     be recorded into a graph.  The plan keeps references to the gradients;
-    launches of one plan must be ordered with each other."""
+    launches of one plan must be ordered with each other and after its making,
+    which copies the table on `stream` (the current one if None)."""
 
     def __init__(self, grads, stream=None):
         self.grads = list(grads)
