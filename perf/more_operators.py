@@ -228,18 +228,18 @@ def _plain(state):
 def _calls(state):
     F, op, x = _library(), state["op"], state["x"]
     if op == "codec":
-        rows, cols = F.flashopt_fp8_quantize(x, "both", block=state["block"], dtype=E5M2 if state["wide"] else E4M3)
-        return F.flashopt_fp8_dequantize(rows, BF16), F.flashopt_fp8_dequantize(cols, BF16)
+        rows, cols = F.flashopt_byte_quantize(x, "both", block=state["block"], dtype=E5M2 if state["wide"] else E4M3)
+        return F.flashopt_byte_dequantize(rows, BF16), F.flashopt_byte_dequantize(cols, BF16)
     if op in ("serve", "linear"):
         w = F.FP8Tensor(state["codes"], state["scales"], state["outer"], state["inner"])
         if op == "linear":
-            return F.flashopt_fp8_linear(x, w)
+            return F.flashopt_byte_linear(x, w)
         q, h = F.flashopt_rms_norm(x, state["gain"], state["residual"], eps=state["eps"], output="rows")
-        return F.flashopt_fp8_product(q, w), h
+        return F.flashopt_byte_product(q, w), h
     if op == "norm8":
         q, h = F.flashopt_rms_norm(x, state["gain"], state["residual"], eps=state["eps"],
                                    output="both" if state["both"] else "rows")
-        return [F.flashopt_fp8_dequantize(t, BF16) for t in (q if state["both"] else (q,))] + [h]
+        return [F.flashopt_byte_dequantize(t, BF16) for t in (q if state["both"] else (q,))] + [h]
     # a layer without a residual has no gradient of the sum from elsewhere
     sides = ((state["dy"], state["dh"]) if "dh" in state else (state["dy"],))
     if op == "norm":
