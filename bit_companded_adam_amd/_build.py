@@ -9,7 +9,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflashopt.so")
 SOURCES = [os.path.join(CSRC, name) for name in ("flashopt_kernels.hip", "flashopt_grad.hip",
-                                                 "flashopt_mx.hip", "flashopt_api.cpp")]
+                                                 "flashopt_mx.hip", "flashopt_fp8.hip",
+                                                 "flashopt_norm.hip", "flashopt_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",

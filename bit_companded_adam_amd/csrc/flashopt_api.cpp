@@ -690,6 +690,87 @@ size_t rounded(size_t bytes) { return (bytes + 15) & ~static_cast<size_t>(15); }
 std::mutex g_noalloc_mutex;
 alignas(64) unsigned char g_noalloc_table[flashopt::kScratchBytes];
 
+// ---- 8-bit matrices and the norm
+
+using flashopt::Fp8Out;
+
+bool known_format(int format) { return format == FLASHOPT_E4M3 || format == FLASHOPT_E5M2; }
+static_assert(FLASHOPT_E4M3 == flashopt::kE4M3 && FLASHOPT_E5M2 == flashopt::kE5M2, "formats");
+
+flashopt_status check_fp8(const void *codes, const void *scales, int64_t rows, int64_t cols)
+{
+    const flashopt_status cs = check_codes(codes, scales, rows, cols);
+    if (cs != FLASHOPT_OK || rows == 0 || cols == 0) return cs;
+    return aligned(scales, 16) ? FLASHOPT_OK : FLASHOPT_EALIGN;
+}
+
+// Workgroups of a quantization that writes codes along columns or of blocks:
+// tiles of 128 x 128, whose work-items a dispatch counts in 32 bits.
+bool fp8_quantizable(int64_t rows, int64_t cols)
+{
+    return ((rows + 127) / 128) * ((cols + 127) / 128) < (int64_t{1} << 24);
+}
+
+// Most elements that a product sums over: its kernels multiply rows of a tile
+// by a row's bytes of codes in 24 bits.
+constexpr int64_t kMaxFp8Inner = (int64_t{1} << 24) - 128;
+
+// Rows of bytes that a call reads or writes (data NULL or no rows: nothing).
+struct Region {
+    uintptr_t data;
+    int64_t rows, row_bytes, stride_bytes;
+};
+
+Region region(const MxMatrix &x)
+{
+    const int64_t esz = x.fp32 ? 4 : 2;
+    return {reinterpret_cast<uintptr_t>(x.data), x.rows, x.cols * esz, x.row_stride * esz};
+}
+
+Region flat(const void *p, size_t bytes)
+{
+    return {reinterpret_cast<uintptr_t>(p), 1, static_cast<int64_t>(bytes), 0};
+}
+
+// Whether two regions share a byte.  Of regions that reach over each other, only
+// those of one stride whose rows lie side by side within it share none.
+bool shared(const Region &a, const Region &b)
+{
+    if (!a.data || !b.data || a.rows <= 0 || b.rows <= 0 || a.row_bytes <= 0 || b.row_bytes <= 0) return false;
+    auto end = [](const Region &r) {
+        return static_cast<__int128>(r.data) + static_cast<__int128>(r.rows - 1) * r.stride_bytes + r.row_bytes;
+    };
+    if (end(a) <= b.data || end(b) <= a.data) return false;
+    const int64_t stride = a.rows > 1 ? a.stride_bytes : b.stride_bytes;
+    if (stride <= 0 || (b.rows > 1 && b.stride_bytes != stride)) return true;
+    const int64_t apart = static_cast<int64_t>(b.data - a.data), at = ((apart % stride) + stride) % stride;
+    return at < a.row_bytes || at + b.row_bytes > stride;
+}
+
+bool same(const Region &a, const Region &b)
+{
+    return a.data == b.data && (a.rows <= 1 || a.stride_bytes == b.stride_bytes);
+}
+
+flashopt_status check_norm_sizes(int64_t rows, int64_t cols, int32_t fp32, int32_t gain_fp32)
+{
+    if ((fp32 != 0 && fp32 != 1) || (gain_fp32 != 0 && gain_fp32 != 1)) return FLASHOPT_EINVAL;
+    return check_size(rows, cols);
+}
+
+// An optional matrix of a norm: not looked at where it is NULL.
+flashopt_status check_optional(const MxMatrix &x, bool written)
+{
+    return x.data ? check_matrix(x, x.fp32, written) : FLASHOPT_OK;
+}
+
+// A norm's gain, and its fp32 values of the rows (or NULL).
+flashopt_status check_vectors(const void *gain, int gain_fp32, const float *rstd)
+{
+    if (!gain) return FLASHOPT_EINVAL;
+    return aligned(gain, gain_fp32 ? 4 : 2) && aligned(rstd, 4) ? FLASHOPT_OK : FLASHOPT_EALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1144,6 +1225,204 @@ flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t
     }
     return hip_status(flashopt::launch_mx_product(codes, scales, static_cast<const uint8_t *>(w_codes),
                                                   static_cast<const uint8_t *>(w_scales), k, o, st));
+}
+
+size_t flashopt_byte_code_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || check_size(rows, cols) != FLASHOPT_OK) return 0;
+    return static_cast<size_t>(rows) * static_cast<size_t>(flashopt::mx_padded(cols));
+}
+
+size_t flashopt_byte_scale_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || check_size(rows, cols) != FLASHOPT_OK) return 0;
+    return static_cast<size_t>(rows) * static_cast<size_t>(flashopt::fp8_scale_stride(cols));
+}
+
+flashopt_status flashopt_byte_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols, int64_t row_stride,
+                                      int format, int block, void *codes, void *scales, void *codes_t,
+                                      void *scales_t, void *stream)
+{
+    const MxMatrix in{const_cast<void *>(x), rows, cols, row_stride, x_fp32 != 0};
+    if (!known_format(format) || (block != 0 && block != 1)) return FLASHOPT_EINVAL;
+    flashopt_status cs = check_matrix(in, x_fp32, false);
+    if (cs != FLASHOPT_OK || rows == 0 || cols == 0) return cs;
+    if ((!codes && !codes_t) || (!codes != !scales) || (!codes_t != !scales_t) || !fp8_quantizable(rows, cols))
+        return FLASHOPT_EINVAL;
+    if (codes && (cs = check_fp8(codes, scales, rows, cols)) != FLASHOPT_OK) return cs;
+    if (codes_t && (cs = check_fp8(codes_t, scales_t, cols, rows)) != FLASHOPT_OK) return cs;
+    const Region out[4] = {flat(codes, flashopt_byte_code_bytes(rows, cols)),
+                           flat(scales, flashopt_byte_scale_bytes(rows, cols)),
+                           flat(codes_t, flashopt_byte_code_bytes(cols, rows)),
+                           flat(scales_t, flashopt_byte_scale_bytes(cols, rows))};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (shared(out[i], out[j])) return FLASHOPT_EINVAL;
+    const Fp8Out q{static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), static_cast<uint8_t *>(codes_t),
+                   static_cast<uint8_t *>(scales_t)};
+    return hip_status(flashopt::launch_fp8_quantize(in, format, block != 0, q, static_cast<hipStream_t>(stream)));
+}
+
+flashopt_status flashopt_byte_dequantize(const void *codes, const void *scales, int format, int64_t rows, int64_t cols,
+                                        void *out, int out_fp32, int64_t row_stride, void *stream)
+{
+    const MxMatrix o{out, rows, cols, row_stride, out_fp32 != 0};
+    if (!known_format(format)) return FLASHOPT_EINVAL;
+    flashopt_status cs = check_matrix(o, out_fp32, true);
+    if (cs != FLASHOPT_OK || rows == 0 || cols == 0) return cs;
+    if ((cs = check_fp8(codes, scales, rows, cols)) != FLASHOPT_OK) return cs;
+    return hip_status(flashopt::launch_fp8_dequantize(static_cast<const uint8_t *>(codes),
+                                                      static_cast<const uint8_t *>(scales), format, o,
+                                                      static_cast<hipStream_t>(stream)));
+}
+
+flashopt_status flashopt_byte_product(const void *a_codes, const void *a_scales, int a_format, const void *b_codes,
+                                     const void *b_scales, int64_t m, int64_t n, int64_t k, void *out, int out_fp32,
+                                     int64_t row_stride, void *stream)
+{
+    const MxMatrix o{out, m, n, row_stride, out_fp32 != 0};
+    if (!known_format(a_format)) return FLASHOPT_EINVAL;
+    flashopt_status cs = check_matrix(o, out_fp32, true);
+    if (cs != FLASHOPT_OK) return cs;
+    if ((cs = check_size(m, k)) != FLASHOPT_OK) return cs;
+    if (k > kMaxFp8Inner) return FLASHOPT_EINVAL;
+    if (m == 0 || n == 0) return FLASHOPT_OK;
+    if ((cs = check_fp8(a_codes, a_scales, m, k)) != FLASHOPT_OK) return cs;
+    if ((cs = check_fp8(b_codes, b_scales, n, k)) != FLASHOPT_OK) return cs;
+    return hip_status(flashopt::launch_fp8_product(
+        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), a_format,
+        static_cast<const uint8_t *>(b_codes), static_cast<const uint8_t *>(b_scales), k, o,
+        static_cast<hipStream_t>(stream)));
+}
+
+size_t flashopt_byte_linear_workspace_bytes(int64_t m, int64_t k)
+{
+    return flashopt_byte_code_bytes(m, k) + flashopt_byte_scale_bytes(m, k);
+}
+
+flashopt_status flashopt_byte_linear(const void *x, int x_fp32, int64_t m, int64_t k, int64_t x_stride,
+                                    const void *w_codes, const void *w_scales, int64_t n, void *out, int out_fp32,
+                                    int64_t out_stride, void *workspace, size_t ws_bytes, void *stream)
+{
+    const MxMatrix in{const_cast<void *>(x), m, k, x_stride, x_fp32 != 0};
+    const MxMatrix o{out, m, n, out_stride, out_fp32 != 0};
+    flashopt_status cs = check_matrix(in, x_fp32, false);
+    if (cs != FLASHOPT_OK) return cs;
+    if ((cs = check_matrix(o, out_fp32, true)) != FLASHOPT_OK) return cs;
+    if (k > kMaxFp8Inner) return FLASHOPT_EINVAL;
+    if (m == 0 || n == 0) return FLASHOPT_OK;
+    if (!fp8_quantizable(m, k)) return FLASHOPT_EINVAL;
+    if ((cs = check_fp8(w_codes, w_scales, n, k)) != FLASHOPT_OK) return cs;
+    const size_t need = flashopt_byte_linear_workspace_bytes(m, k);
+    if (need > 0 && (!workspace || ws_bytes < need)) return FLASHOPT_EWORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return FLASHOPT_EALIGN;
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + flashopt_byte_code_bytes(m, k);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (k > 0) {
+        const Fp8Out q{codes, scales, nullptr, nullptr};
+        const hipError_t e = flashopt::launch_fp8_quantize(in, FLASHOPT_E4M3, false, q, st);
+        if (e != hipSuccess) return hip_status(e);
+    }
+    return hip_status(flashopt::launch_fp8_product(codes, scales, FLASHOPT_E4M3, static_cast<const uint8_t *>(w_codes),
+                                                   static_cast<const uint8_t *>(w_scales), k, o, st));
+}
+
+flashopt_status flashopt_rms_norm(const flashopt_norm_args *args, void *stream)
+{
+    if (!args) return FLASHOPT_EINVAL;
+    const flashopt_norm_args &p = *args;
+    flashopt_status cs = check_norm_sizes(p.rows, p.cols, p.fp32, p.gain_fp32);
+    if (cs != FLASHOPT_OK) return cs;
+    if (!(p.eps >= 0.0) || !std::isfinite(p.eps) || !known_format(p.format) || p.reserved != 0) return FLASHOPT_EINVAL;
+    const bool wide = p.fp32 != 0;
+    const flashopt::NormCall n{{const_cast<void *>(p.x), p.rows, p.cols, p.x_stride, wide},
+                               {const_cast<void *>(p.residual), p.rows, p.cols, p.residual_stride, wide},
+                               {p.h, p.rows, p.cols, p.h_stride, wide},
+                               {p.y, p.rows, p.cols, p.y_stride, wide},
+                               p.gain,
+                               p.gain_fp32 != 0,
+                               p.eps,
+                               p.format,
+                               {static_cast<uint8_t *>(p.codes), static_cast<uint8_t *>(p.scales),
+                                static_cast<uint8_t *>(p.codes_t), static_cast<uint8_t *>(p.scales_t)},
+                               p.rstd};
+    if (p.rows == 0 || p.cols == 0) return FLASHOPT_OK;
+    if ((cs = check_matrix(n.x, p.fp32, false)) != FLASHOPT_OK) return cs;
+    if (!p.residual != !p.h || !p.codes != !p.scales || !p.codes_t != !p.scales_t ||
+        (!p.y && !p.codes && !p.codes_t) || (p.codes_t && (!p.rstd || !fp8_quantizable(p.rows, p.cols))))
+        return FLASHOPT_EINVAL;
+    if ((cs = check_vectors(p.gain, p.gain_fp32, p.rstd)) != FLASHOPT_OK) return cs;
+    if ((cs = check_optional(n.residual, false)) != FLASHOPT_OK) return cs;
+    if ((cs = check_optional(n.h, true)) != FLASHOPT_OK) return cs;
+    if ((cs = check_optional(n.y, true)) != FLASHOPT_OK) return cs;
+    if (p.codes && (cs = check_fp8(p.codes, p.scales, p.rows, p.cols)) != FLASHOPT_OK) return cs;
+    if (p.codes_t && (cs = check_fp8(p.codes_t, p.scales_t, p.cols, p.rows)) != FLASHOPT_OK) return cs;
+    const Region written[7] = {region(n.h),
+                               region(n.y),
+                               flat(p.codes, flashopt_byte_code_bytes(p.rows, p.cols)),
+                               flat(p.scales, flashopt_byte_scale_bytes(p.rows, p.cols)),
+                               flat(p.codes_t, flashopt_byte_code_bytes(p.cols, p.rows)),
+                               flat(p.scales_t, flashopt_byte_scale_bytes(p.cols, p.rows)),
+                               flat(p.rstd, static_cast<size_t>(p.rows) * 4)};
+    const Region read[3] = {region(n.x), region(n.residual), flat(p.gain, static_cast<size_t>(p.cols) * (p.gain_fp32 ? 4 : 2))};
+    for (int i = 0; i < 7; ++i) {
+        for (int j = i + 1; j < 7; ++j)
+            if (shared(written[i], written[j])) return FLASHOPT_EINVAL;
+        for (int j = 0; j < 3; ++j)
+            if (shared(written[i], read[j]) && !(i == 0 && j < 2 && same(written[i], read[j]))) return FLASHOPT_EINVAL;
+    }
+    return hip_status(flashopt::launch_rms_norm(n, static_cast<hipStream_t>(stream)));
+}
+
+size_t flashopt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0 || check_size(rows, cols) != FLASHOPT_OK) return 0;
+    return static_cast<size_t>(cols) * flashopt::kNormPartials * sizeof(float);
+}
+
+flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, void *stream)
+{
+    if (!args) return FLASHOPT_EINVAL;
+    const flashopt_norm_grad_args &p = *args;
+    flashopt_status cs = check_norm_sizes(p.rows, p.cols, p.fp32, p.gain_fp32);
+    if (cs != FLASHOPT_OK) return cs;
+    if (p.cols > flashopt::kNormGradCols || (!p.dx && !p.dgain)) return FLASHOPT_EINVAL;
+    if (p.cols == 0 || (p.rows == 0 && !p.dgain)) return FLASHOPT_OK;
+    const bool wide = p.fp32 != 0;
+    const flashopt::NormGradCall n{{const_cast<void *>(p.dy), p.rows, p.cols, p.dy_stride, wide},
+                                   {const_cast<void *>(p.dh), p.rows, p.cols, p.dh_stride, wide},
+                                   {const_cast<void *>(p.h), p.rows, p.cols, p.h_stride, wide},
+                                   {p.dx, p.rows, p.cols, p.dx_stride, wide},
+                                   p.gain,
+                                   p.gain_fp32 != 0,
+                                   p.rstd,
+                                   p.dgain,
+                                   static_cast<float *>(p.workspace)};
+    if (!aligned(p.dgain, p.gain_fp32 ? 4 : 2)) return FLASHOPT_EALIGN;
+    if (p.rows > 0) {
+        if ((cs = check_matrix(n.dy, p.fp32, false)) != FLASHOPT_OK) return cs;
+        if ((cs = check_matrix(n.h, p.fp32, false)) != FLASHOPT_OK) return cs;
+        if (!p.rstd) return FLASHOPT_EINVAL;
+        if ((cs = check_vectors(p.gain, p.gain_fp32, p.rstd)) != FLASHOPT_OK) return cs;
+        if ((cs = check_optional(n.dh, false)) != FLASHOPT_OK) return cs;
+        if ((cs = check_optional(n.dx, true)) != FLASHOPT_OK) return cs;
+        const size_t need = p.dgain ? flashopt_rms_norm_backward_workspace_bytes(p.rows, p.cols) : 0;
+        if (need > 0 && (!p.workspace || p.workspace_bytes < need)) return FLASHOPT_EWORKSPACE;
+        if (need > 0 && !aligned(p.workspace, 16)) return FLASHOPT_EALIGN;
+        const size_t gain_bytes = static_cast<size_t>(p.cols) * (p.gain_fp32 ? 4 : 2);
+        const Region written[3] = {region(n.dx), flat(p.dgain, gain_bytes), flat(p.workspace, need)};
+        const Region read[5] = {region(n.dy), region(n.dh), region(n.h), flat(p.gain, gain_bytes),
+                                flat(p.rstd, static_cast<size_t>(p.rows) * 4)};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = i + 1; j < 3; ++j)
+                if (shared(written[i], written[j])) return FLASHOPT_EINVAL;
+            for (int j = 0; j < 5; ++j)
+                if (shared(written[i], read[j]) && !(i == 0 && j < 2 && same(written[i], read[j])))
+                    return FLASHOPT_EINVAL;
+        }
+    }
+    return hip_status(flashopt::launch_rms_norm_backward(n, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -195,4 +195,54 @@ hipError_t launch_mx_product(const uint8_t *a_codes, const uint8_t *a_scales, co
                              const uint8_t *b_scales, int64_t inner, const MxMatrix &out,
                              hipStream_t stream);
 
+// ---- 8-bit matrices (flashopt_fp8.hip) and the norm (flashopt_norm.hip)
+
+// Formats of codes, as the matrix instructions number them.
+constexpr int kE4M3 = 0, kE5M2 = 1;
+
+// Bytes of a row of scales: one for each 128 elements, padded to a multiple of
+// 16.  (Rows of codes are mx_padded(cols) bytes.)
+__host__ __device__ inline int64_t fp8_scale_stride(int64_t cols) { return (cols + 2047) / 2048 * 16; }
+
+// A quantization's outputs: along rows, of the transpose, or both.
+struct Fp8Out {
+    uint8_t *codes, *scales, *codes_t, *scales_t;
+};
+
+hipError_t launch_fp8_quantize(const MxMatrix &x, int format, bool block, const Fp8Out &q, hipStream_t stream);
+// Of (h rstd) gain, both layouts or the transpose.
+hipError_t launch_fp8_normed(const MxMatrix &h, const float *rstd, const void *gain, bool gain_fp32, int format,
+                             const Fp8Out &q, hipStream_t stream);
+hipError_t launch_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, int format, const MxMatrix &out,
+                                 hipStream_t stream);
+// out = A B^T with A of out.rows and B of out.cols rows; B is E4M3.
+hipError_t launch_fp8_product(const uint8_t *a_codes, const uint8_t *a_scales, int a_format, const uint8_t *b_codes,
+                              const uint8_t *b_scales, int64_t inner, const MxMatrix &out, hipStream_t stream);
+
+// x, residual, h and y are of one size and type; what is not wanted is nullptr.
+struct NormCall {
+    MxMatrix x, residual, h, y;
+    const void *gain;
+    bool gain_fp32;
+    double eps;
+    int format;
+    Fp8Out q;
+    float *rstd;
+};
+hipError_t launch_rms_norm(const NormCall &n, hipStream_t stream);
+
+// Most columns of a backward pass: a row stays in registers.
+constexpr int64_t kNormGradCols = 32768;
+// Workgroups of a backward pass that sums dgain, one partial row each.
+constexpr unsigned kNormPartials = 512;
+struct NormGradCall {
+    MxMatrix dy, dh, h, dx;
+    const void *gain;
+    bool gain_fp32;
+    const float *rstd;
+    void *dgain;
+    float *partial;          // [kNormPartials][cols]
+};
+hipError_t launch_rms_norm_backward(const NormGradCall &n, hipStream_t stream);
+
 }  // namespace flashopt

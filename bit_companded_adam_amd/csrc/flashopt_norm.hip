@@ -1,0 +1,394 @@
+// Root-mean-square norm with the residual's addition (flashopt_rms_norm), its
+// output in the input's type or in 8 bits with scales, and its backward pass
+// (flashopt_rms_norm_backward).
+//
+//   h = x + residual, rounded to their type       r = 1 / sqrt(mean h^2 + eps)
+//   y = (h r) gain, in fp32, rounded once
+//   with u = dy gain, t = h r, c = mean(u t):
+//   dx = r (u - t c) + dh                          dgain = sum over rows dy t
+//
+// Squares and their sum are fp64, and r is rounded to fp32 once: bf16 and fp32
+// squares leave fp32's range at both ends, and y is then the same three fp32
+// roundings whatever the order of the sum.
+//
+// Each pass reads every row once and is bound by memory.  A group of TPR
+// threads takes a row, NV vectors of eight columns to a thread, and keeps it in
+// registers between the sum and the output.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "flashopt.h"
+#include "flashopt_fp8.h"
+#include "flashopt_internal.h"
+
+namespace flashopt {
+namespace {
+
+__device__ __forceinline__ double shuffled(double x, int mask)
+{
+    return __shfl_xor(x, mask, kWaveLanes);
+}
+__device__ __forceinline__ float shuffled(float x, int mask)
+{
+    return __shfl_xor(x, mask, kWaveLanes);
+}
+
+// Sum over the TPR threads of a row, known to all of them.  With more than a
+// wavefront to a row the workgroup is that row's, and `scratch` (TPR / 64
+// values) is free again after the next barrier.
+template <int TPR, typename T>
+__device__ __forceinline__ T row_sum(T x, T *scratch)
+{
+#pragma unroll
+    for (int m = 1; m < kWaveLanes; m *= 2) x += shuffled(x, m);
+    if constexpr (TPR > kWaveLanes) {
+        constexpr int kWaves = TPR / kWaveLanes;
+        if ((threadIdx.x & (kWaveLanes - 1)) == 0) scratch[threadIdx.x / kWaveLanes] = x;
+        __syncthreads();
+        x = scratch[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) x += scratch[w];
+    }
+    return x;
+}
+
+struct NormIn {
+    const uint8_t *x, *residual, *gain;      // residual: or nullptr
+    int64_t x_bytes, residual_bytes;         // of a row's stride
+    int64_t rows, cols;
+    double eps;
+    bool gain_fp32;
+};
+struct NormOut {
+    uint8_t *h, *y, *codes, *scales;         // each, or nullptr
+    float *rstd;
+    int64_t h_bytes, y_bytes;
+    bool e5m2;
+};
+
+__device__ __forceinline__ void gains(const uint8_t *gain, bool fp32, int64_t c, int64_t cols, float (&g)[8])
+{
+    if (fp32) {
+        const Eight<true> f = load8<true, false>(gain + c * 4, cols - c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = value(f, j);
+    } else {
+        const Eight<false> f = load8<false, false>(gain + c * 2, cols - c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = value(f, j);
+    }
+}
+
+// Eight normed values to wherever they go: y, and codes under the scale of
+// their group's sixteen lanes (values past the row's end are zeros).
+template <bool F32>
+__device__ __forceinline__ void emit(const NormOut &o, int64_t row, int64_t c, int64_t cols, const float (&v)[8])
+{
+    if (o.y && c < cols) store8<F32>(o.y + row * o.y_bytes + c * (F32 ? 4 : 2), rounded8<F32>(v), cols - c);
+    if (o.codes) {
+        const Eight<true> f = rounded8<true>(v);
+        const uint32_t top = max16(largest_of(f));
+        const uint32_t scale = o.e5m2 ? fp8_scale<kE5M2>(top) : fp8_scale<kE4M3>(top);
+        u32x2 q = o.e5m2 ? row_codes<true, kE5M2>(f, scale) : row_codes<true, kE4M3>(f, scale);
+        uint32_t b = scale >> 23;
+        if (top >= kInfinite) {
+            q = u32x2{0u, 0u};
+            b = kNanByte;
+        }
+        if (c < mx_padded(cols)) {
+            *reinterpret_cast<u32x2 *>(o.codes + row * mx_padded(cols) + c) = q;
+            if ((threadIdx.x & 15) == 0) o.scales[row * fp8_scale_stride(cols) + c / 128] = static_cast<uint8_t>(b);
+        }
+    }
+}
+
+// x + residual in fp32, rounded to their type.
+template <bool F32>
+__device__ __forceinline__ Eight<F32> added(const Eight<F32> &a, const Eight<F32> &b)
+{
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = value(a, j) + value(b, j);
+    return rounded8<F32>(v);
+}
+
+// NV = 0: a row of any length, read again for the output (h where there is
+// one: x otherwise).
+template <bool F32, int TPR, int NV>
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
+rms_norm_kernel(NormIn in, NormOut out)
+{
+    constexpr int kGroup = TPR > kThreads ? TPR : kThreads, kRowsAtOnce = TPR > kWaveLanes ? 1 : kGroup / TPR;
+    constexpr int kEsz = F32 ? 4 : 2;
+    static_assert(TPR == kWaveLanes || TPR == kGroup, "a wavefront or a workgroup to a row");
+    __shared__ double s_sum[2][kGroup / kWaveLanes];
+    const int t = threadIdx.x % TPR;
+    const int64_t cols = in.cols;
+    int turn = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsAtOnce + threadIdx.x / TPR; row < in.rows;
+         row += static_cast<int64_t>(gridDim.x) * kRowsAtOnce, turn ^= 1) {
+        const uint8_t *x = in.x + row * in.x_bytes, *residual = in.residual + row * in.residual_bytes;
+        uint8_t *h = out.h + row * out.h_bytes;
+        double sum = 0.0;
+        Eight<F32> keep[NV > 0 ? NV : 1];
+        auto take = [&](int64_t c) {
+            Eight<F32> f = load8<F32, false>(x + c * kEsz, cols - c);
+            if (in.residual) {
+                f = added(f, load8<F32, false>(residual + c * kEsz, cols - c));
+                if (c < cols) store8<F32>(h + c * kEsz, f, cols - c);
+            }
+            return f;
+        };
+        auto square = [&](const Eight<F32> &f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double v = static_cast<double>(value(f, j));
+                sum = __builtin_fma(v, v, sum);
+            }
+        };
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) keep[v] = take((static_cast<int64_t>(v) * TPR + t) * 8);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) square(keep[v]);
+        } else {
+            for (int64_t c = t * 8; c < cols; c += TPR * 8) square(take(c));
+        }
+        sum = row_sum<TPR>(sum, s_sum[turn]);
+        const float r = static_cast<float>(1.0 / __builtin_sqrt(sum / static_cast<double>(cols) + in.eps));
+        if (out.rstd && t == 0) out.rstd[row] = r;
+        if (!out.y && !out.codes) continue;
+        auto give = [&](int64_t c, const Eight<F32> &f) {
+            float g[8], y[8];
+            gains(in.gain, in.gain_fp32, c, cols, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = c + j < cols ? (value(f, j) * r) * g[j] : 0.0f;
+            emit<F32>(out, row, c, cols, y);
+        };
+        // a group's sixteen lanes take part together, to the end of the padded row
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) give((static_cast<int64_t>(v) * TPR + t) * 8, keep[v]);
+        } else {
+            const uint8_t *from = in.residual ? h : x;
+            for (int64_t c = t * 8; c < mx_padded(cols); c += TPR * 8)
+                give(c, load8<F32, false>(from + c * kEsz, cols - c));
+        }
+        if (out.codes)                        // the rest of the padded row of scales
+            for (int64_t i = (cols + 127) / 128 + t; i < fp8_scale_stride(cols); i += TPR)
+                out.scales[row * fp8_scale_stride(cols) + i] = 0;
+    }
+}
+
+// -------------------------------------------------------------- backward
+
+struct GradIn {
+    const uint8_t *dy, *dh, *h, *gain;       // dh: or nullptr
+    const float *rstd;
+    int64_t dy_bytes, dh_bytes, h_bytes;
+    int64_t rows, cols;
+    bool gain_fp32;
+};
+
+// A workgroup takes rows in turn, as the forward pass does, and keeps its
+// threads' columns of dgain in registers over all of them; partial[workgroup]
+// is added up in order by norm_gain_kernel.
+template <bool F32, int TPR, int NV>
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
+rms_norm_backward_kernel(GradIn in, uint8_t *__restrict__ dx, int64_t dx_bytes, float *__restrict__ partial)
+{
+    constexpr int kGroup = TPR > kThreads ? TPR : kThreads, kRowsAtOnce = TPR > kWaveLanes ? 1 : kGroup / TPR;
+    constexpr int kEsz = F32 ? 4 : 2;
+    __shared__ float s_sum[2][kGroup / kWaveLanes];
+    __shared__ float s_gain[kRowsAtOnce > 1 ? kRowsAtOnce * TPR * 8 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t cols = in.cols;
+    float dgain[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dgain[v][j] = 0.0f;
+    int turn = 0;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsAtOnce + threadIdx.x / TPR; row < in.rows;
+         row += static_cast<int64_t>(gridDim.x) * kRowsAtOnce, turn ^= 1) {
+        const float r = in.rstd[row];
+        Eight<F32> dy[NV], h[NV];
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int64_t c = (static_cast<int64_t>(v) * TPR + t) * 8;
+            dy[v] = load8<F32, false>(in.dy + row * in.dy_bytes + c * kEsz, cols - c);
+            h[v] = load8<F32, false>(in.h + row * in.h_bytes + c * kEsz, cols - c);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float g[8];
+            gains(in.gain, in.gain_fp32, (static_cast<int64_t>(v) * TPR + t) * 8, cols, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = value(dy[v], j), x = value(h[v], j) * r;
+                dgain[v][j] = __builtin_fmaf(d, x, dgain[v][j]);
+                sum = __builtin_fmaf(d * g[j], x, sum);
+            }
+        }
+        if (!dx) continue;
+        const float c1 = row_sum<TPR>(sum, s_sum[turn]) / static_cast<float>(cols);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int64_t c = (static_cast<int64_t>(v) * TPR + t) * 8;
+            if (c >= cols) continue;
+            float g[8], o[8];
+            gains(in.gain, in.gain_fp32, c, cols, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = r * (value(dy[v], j) * g[j] - (value(h[v], j) * r) * c1);
+            if (in.dh) {
+                const Eight<F32> e = load8<F32, false>(in.dh + row * in.dh_bytes + c * kEsz, cols - c);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += value(e, j);
+            }
+            store8<F32>(dx + row * dx_bytes + c * kEsz, rounded8<F32>(o), cols - c);
+        }
+    }
+    if (!partial) return;
+    float *p = partial + static_cast<int64_t>(blockIdx.x) * cols;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c = (static_cast<int64_t>(v) * TPR + t) * 8;
+        if constexpr (kRowsAtOnce > 1) {      // the wavefronts' sums, in their order
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s_gain[(threadIdx.x / TPR * 8 + j) * TPR + t] = dgain[v][j];
+            __syncthreads();
+            if (threadIdx.x < TPR) {
+#pragma unroll
+                for (int w = 1; w < kRowsAtOnce; ++w)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dgain[v][j] += s_gain[(w * 8 + j) * TPR + t];
+            }
+        }
+        if (kRowsAtOnce == 1 || threadIdx.x < TPR) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < cols) p[c + j] = dgain[v][j];
+        }
+    }
+}
+
+// dgain = the sum of the partial rows, in fp64 and in their order; 64 columns
+// to a workgroup, its wavefronts taking rows in turn.
+constexpr int kGainWaves = 16;
+__global__ void __launch_bounds__(kGainWaves *kWaveLanes)
+norm_gain_kernel(const float *__restrict__ partial, int count, int64_t cols, uint8_t *__restrict__ dgain, bool fp32)
+{
+    __shared__ double s_sum[kGainWaves][kWaveLanes];
+    const int lane = threadIdx.x & (kWaveLanes - 1), wave = threadIdx.x / kWaveLanes;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kWaveLanes + lane;
+    double sum = 0.0;
+    if (c < cols)
+        for (int i = wave; i < count; i += kGainWaves) sum += static_cast<double>(partial[i * cols + c]);
+    s_sum[wave][lane] = sum;
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+#pragma unroll
+        for (int w = 1; w < kGainWaves; ++w) sum += s_sum[w][lane];
+        if (fp32) reinterpret_cast<float *>(dgain)[c] = static_cast<float>(sum);
+        else reinterpret_cast<uint16_t *>(dgain)[c] = bf16_rne(static_cast<float>(sum));
+    }
+}
+
+// ------------------------------------------------------------- launching
+
+// The launch for rows of so many columns: f(TPR, NV) of the smallest registers
+// that hold one.
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <typename F>
+hipError_t by_columns(int64_t cols, F &&f)
+{
+    if (cols <= 512) return f(Int<64>{}, Int<1>{});
+    if (cols <= 1024) return f(Int<64>{}, Int<2>{});
+    if (cols <= 2048) return f(Int<256>{}, Int<1>{});
+    if (cols <= 4096) return f(Int<256>{}, Int<2>{});
+    if (cols <= 8192) return f(Int<256>{}, Int<4>{});
+    if (cols <= 16384) return f(Int<1024>{}, Int<2>{});
+    if (cols <= 32768) return f(Int<1024>{}, Int<4>{});
+    return f(Int<1024>{}, Int<0>{});
+}
+
+template <int TPR>
+unsigned row_groups(int64_t rows)
+{
+    return static_cast<unsigned>(TPR > kWaveLanes ? rows : (rows + kThreads / TPR - 1) / (kThreads / TPR));
+}
+
+template <bool F32>
+hipError_t norm_type(const NormIn &in, const NormOut &out, hipStream_t st)
+{
+    return by_columns(in.cols, [&](auto tpr, auto nv) {
+        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+        const unsigned groups = row_groups<TPR>(in.rows);
+        hipLaunchKernelGGL((rms_norm_kernel<F32, TPR, NV>), dim3(groups < (1u << 20) ? groups : (1u << 20)),
+                           dim3(TPR > kThreads ? TPR : kThreads), 0, st, in, out);
+        return hipGetLastError();
+    });
+}
+
+template <bool F32>
+hipError_t backward_type(const GradIn &in, uint8_t *dx, int64_t dx_bytes, uint8_t *dgain, float *partial,
+                         hipStream_t st)
+{
+    return by_columns(in.cols, [&](auto tpr, auto nv) -> hipError_t {
+        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+        if constexpr (NV == 0) {
+            return hipErrorInvalidValue;
+        } else {
+            const unsigned groups = row_groups<TPR>(in.rows);
+            const unsigned grid = groups < kNormPartials ? groups : kNormPartials;
+            if (grid > 0) {
+                hipLaunchKernelGGL((rms_norm_backward_kernel<F32, TPR, NV>), dim3(grid),
+                                   dim3(TPR > kThreads ? TPR : kThreads), 0, st, in, dx, dx_bytes, partial);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess || !dgain) return e;
+            }
+            hipLaunchKernelGGL(norm_gain_kernel, dim3(static_cast<unsigned>((in.cols + kWaveLanes - 1) / kWaveLanes)),
+                               dim3(kGainWaves * kWaveLanes), 0, st, partial, static_cast<int>(grid), in.cols, dgain,
+                               in.gain_fp32);
+            return hipGetLastError();
+        }
+    });
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormCall &n, hipStream_t st)
+{
+    const int esz = n.x.fp32 ? 4 : 2;
+    const NormIn in{static_cast<const uint8_t *>(n.x.data), static_cast<const uint8_t *>(n.residual.data),
+                    static_cast<const uint8_t *>(n.gain), n.x.row_stride * esz, n.residual.row_stride * esz,
+                    n.x.rows, n.x.cols, n.eps, n.gain_fp32};
+    // codes along columns need the statistics of 128 rows first: then both
+    // layouts come from a second launch, which reads h again
+    const bool tiles = n.q.codes_t != nullptr;
+    const NormOut out{static_cast<uint8_t *>(n.h.data), static_cast<uint8_t *>(n.y.data),
+                      tiles ? nullptr : n.q.codes, n.q.scales, n.rstd, n.h.row_stride * esz, n.y.row_stride * esz,
+                      n.format == kE5M2};
+    hipError_t e = n.x.fp32 ? norm_type<true>(in, out, st) : norm_type<false>(in, out, st);
+    if (e != hipSuccess || !tiles) return e;
+    return launch_fp8_normed(n.residual.data ? n.h : n.x, n.rstd, n.gain, n.gain_fp32, n.format, n.q, st);
+}
+
+hipError_t launch_rms_norm_backward(const NormGradCall &n, hipStream_t st)
+{
+    const int esz = n.h.fp32 ? 4 : 2;
+    const GradIn in{static_cast<const uint8_t *>(n.dy.data), static_cast<const uint8_t *>(n.dh.data),
+                    static_cast<const uint8_t *>(n.h.data), static_cast<const uint8_t *>(n.gain), n.rstd,
+                    n.dy.row_stride * esz, n.dh.row_stride * esz, n.h.row_stride * esz, n.h.rows, n.h.cols,
+                    n.gain_fp32};
+    uint8_t *dx = static_cast<uint8_t *>(n.dx.data), *dgain = static_cast<uint8_t *>(n.dgain);
+    return n.h.fp32 ? backward_type<true>(in, dx, n.dx.row_stride * esz, dgain, dgain ? n.partial : nullptr, st)
+                    : backward_type<false>(in, dx, n.dx.row_stride * esz, dgain, dgain ? n.partial : nullptr, st);
+}
+
+}  // namespace flashopt

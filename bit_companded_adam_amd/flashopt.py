@@ -1,7 +1,8 @@
 """Thin ctypes binding of libflashopt.so with the C entry points' names
 (FlashAdamW and FlashSGD steps, the codec and the weight split; the gradient
-norm and clipping; MXFP4 quantization and products, and mx_linear on top of
-them for autograd).
+norm and clipping; MXFP4 and 8-bit quantization and products and the
+root-mean-square norm, and on top of them, for autograd, mx_linear, fp8_linear,
+rms_norm and fp8_norm_linear).
 
 Argument marshalling only: every computation runs in the HIP kernels of the
 library.  Tensors are torch CUDA (HIP) tensors; outputs are allocated with
@@ -47,7 +48,10 @@ EXPORTS = ("flashopt_quantize", "flashopt_dequantize", "flashopt_split",
            "flashopt_grad_plan_bytes", "flashopt_grad_plan", "flashopt_grad_plan_norm",
            "flashopt_grad_plan_clip", "flashopt_mx_code_bytes", "flashopt_mx_scale_bytes",
            "flashopt_mx_quantize", "flashopt_mx_dequantize", "flashopt_mx_product",
-           "flashopt_mx_linear_workspace_bytes", "flashopt_mx_linear")
+           "flashopt_mx_linear_workspace_bytes", "flashopt_mx_linear", "flashopt_byte_code_bytes",
+           "flashopt_byte_scale_bytes", "flashopt_byte_quantize", "flashopt_byte_dequantize",
+           "flashopt_byte_product", "flashopt_byte_linear_workspace_bytes", "flashopt_byte_linear",
+           "flashopt_rms_norm", "flashopt_rms_norm_backward_workspace_bytes", "flashopt_rms_norm_backward")
 
 
 class FlashoptError(RuntimeError):
@@ -103,6 +107,23 @@ class flashopt_grad(ctypes.Structure):
 class flashopt_grad_plan_info(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("total_chunks", ctypes.c_int32),
                 ("overlap", ctypes.c_int32)]
+
+
+class flashopt_norm_args(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("x", "residual", "gain", "h", "y", "codes", "scales", "codes_t", "scales_t", "rstd")] + [
+               (name, ctypes.c_int64) for name in ("rows", "cols", "x_stride", "residual_stride", "h_stride",
+                                                   "y_stride")] + [
+               ("eps", ctypes.c_double), ("fp32", ctypes.c_int32), ("gain_fp32", ctypes.c_int32),
+               ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class flashopt_norm_grad_args(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("dy", "dh", "h", "gain", "rstd", "dx", "dgain", "workspace")] + [
+               ("workspace_bytes", ctypes.c_size_t)] + [
+               (name, ctypes.c_int64) for name in ("rows", "cols", "dy_stride", "dh_stride", "h_stride",
+                                                   "dx_stride")] + [
+               ("fp32", ctypes.c_int32), ("gain_fp32", ctypes.c_int32)]
 
 
 _lib = None
@@ -165,13 +186,22 @@ def lib() -> ctypes.CDLL:
         L.flashopt_grad_plan_norm.argtypes = [info, vp, dbl, vp, vp]
         L.flashopt_grad_plan_clip.argtypes = [info, vp, dbl, vp, vp]
         for name, args in (("flashopt_mx_code_bytes", [i64, i64]), ("flashopt_mx_scale_bytes", [i64, i64]),
-                           ("flashopt_mx_linear_workspace_bytes", [i64, i64])):
+                           ("flashopt_mx_linear_workspace_bytes", [i64, i64]),
+                           ("flashopt_byte_code_bytes", [i64, i64]), ("flashopt_byte_scale_bytes", [i64, i64]),
+                           ("flashopt_byte_linear_workspace_bytes", [i64, i64]),
+                           ("flashopt_rms_norm_backward_workspace_bytes", [i64, i64])):
             getattr(L, name).argtypes, getattr(L, name).restype = args, ctypes.c_size_t
         L.flashopt_mx_quantize.argtypes = [vp, i, i64, i64, i64, vp, vp, vp, vp, vp]
         L.flashopt_mx_dequantize.argtypes = [vp, vp, i64, i64, vp, i, i64, vp]
         L.flashopt_mx_product.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i, i64, vp]
         L.flashopt_mx_linear.argtypes = [vp, i, i64, i64, i64, vp, vp, i64, vp, i, i64, vp,
                                          ctypes.c_size_t, vp]
+        L.flashopt_byte_quantize.argtypes = [vp, i, i64, i64, i64, i, i, vp, vp, vp, vp, vp]
+        L.flashopt_byte_dequantize.argtypes = [vp, vp, i, i64, i64, vp, i, i64, vp]
+        L.flashopt_byte_product.argtypes = [vp, vp, i, vp, vp, i64, i64, i64, vp, i, i64, vp]
+        L.flashopt_byte_linear.argtypes = [vp, i, i64, i64, i64, vp, vp, i64, vp, i, i64, vp, ctypes.c_size_t, vp]
+        L.flashopt_rms_norm.argtypes = [ctypes.POINTER(flashopt_norm_args), vp]
+        L.flashopt_rms_norm_backward.argtypes = [ctypes.POINTER(flashopt_norm_grad_args), vp]
         L.flashopt_status_str.argtypes = [i]
         L.flashopt_status_str.restype = ctypes.c_char_p
         L.flashopt_abi_version.argtypes = []
@@ -183,7 +213,9 @@ def lib() -> ctypes.CDLL:
                      "flashopt_sgd_plan", "flashopt_sgd_plan_set_step", "flashopt_sgd_plan_launch",
                      "flashopt_grad_norm", "flashopt_grad_clip", "flashopt_grad_plan",
                      "flashopt_grad_plan_norm", "flashopt_grad_plan_clip", "flashopt_mx_quantize",
-                     "flashopt_mx_dequantize", "flashopt_mx_product", "flashopt_mx_linear"):
+                     "flashopt_mx_dequantize", "flashopt_mx_product", "flashopt_mx_linear",
+                     "flashopt_byte_quantize", "flashopt_byte_dequantize", "flashopt_byte_product",
+                     "flashopt_byte_linear", "flashopt_rms_norm", "flashopt_rms_norm_backward"):
             getattr(L, name).restype = i
         _lib = L
     return _lib
@@ -1081,6 +1113,10 @@ class MXTensor:
         q.replayed = False
         return q
 
+    def _size(self):
+        """_over's arguments after the buffer."""
+        return self.rows, self.cols
+
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
@@ -1252,52 +1288,82 @@ def _flat(x: torch.Tensor) -> torch.Tensor:
     return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
 
 
-class _MXLinear(torch.autograd.Function):
+class _MX:
+    """MXFP4 as a linear layer uses it."""
+    name, tensor = "MXWeight", MXTensor
+
+    def quantize(self, x, layout, weight=False, grad=False):
+        return flashopt_mx_quantize(x, layout)
+
+    def product(self, a, b, dtype):
+        return flashopt_mx_product(a, b, dtype)
+
+
+def _weight_copies(kind, w, weight, need_x):
+    """A weight's quantized copies for a forward pass, the transposed one for the
+    input's gradient, and the held weight whose refresh would make that stale."""
+    if weight is None:
+        q = kind.quantize(w, "both" if need_x else "rows", weight=True)
+        return (*q, None) if need_x else (q, None, None)
+    cols = weight.cols
+    if need_x and cols.replayed and not torch.cuda.is_current_stream_capturing():
+        # a replay may rewrite the copy before the backward pass: keep one of
+        # this call's own (captured, both are in one order)
+        return weight.rows, kind.tensor._over(cols._buffer.clone(), *cols._size()), None
+    return weight.rows, cols, weight
+
+
+def _check_fresh(ctx, kind):
+    if ctx.weight is not None and ctx.weight.version != ctx.version:
+        raise RuntimeError(f"the {kind.name} was refreshed between the forward and the backward pass")
+
+
+class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T with straight-through gradients: dx = Q(dy) Q'(w) and
     dw = Q'(dy)^T Q'(x), Q along rows and Q' along columns (the axis each
-    product sums over).  The activation is kept for the backward pass in
-    4 bits."""
+    product sums over).  The activation is kept for the backward pass in its
+    quantized form."""
 
     @staticmethod
-    def forward(ctx, x, w, weight, grad):
+    def forward(ctx, x, w, weight, grad, kind):
         # needs_input_grad is set where gradients are off altogether, too
         need_x, need_w = [need and grad for need in ctx.needs_input_grad[:2]]
-        if weight is None:
-            q = flashopt_mx_quantize(w, "both" if need_x else "rows")
-            w_rows, w_cols = q if need_x else (q, None)
-        else:
-            w_rows, w_cols = weight.rows, weight.cols
-            if need_x and w_cols.replayed and not torch.cuda.is_current_stream_capturing():
-                # a replay may rewrite the copy before the backward pass: keep
-                # one of this call's own (captured, both are in one order)
-                w_cols, weight = MXTensor._over(w_cols._buffer.clone(), w_cols.rows, w_cols.cols), None
+        w_rows, w_cols, weight = _weight_copies(kind, w, weight, need_x)
         flat = _flat(x)
-        q = flashopt_mx_quantize(flat, "both" if need_w else "rows")
+        q = kind.quantize(flat, "both" if need_w else "rows")
         x_rows, x_cols = q if need_w else (q, None)
-        ctx.weight, ctx.version = weight, None if weight is None else weight.version
+        ctx.kind, ctx.weight, ctx.version = kind, weight, None if weight is None else weight.version
         ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
-        # the transposed copies are this call's own buffers, or the MXWeight's
-        ctx.kept = [None if t is None else (t.rows, t.cols) for t in (x_cols, w_cols if need_x else None)]
-        ctx.save_for_backward(*[t._buffer for t, k in zip((x_cols, w_cols), ctx.kept) if k])
-        y = flashopt_mx_product(x_rows, w_rows, x.dtype)
+        # the transposed copies are this call's own buffers, or the held weight's
+        kept = (x_cols, w_cols if need_x else None)
+        ctx.kept = [None if t is None else t._size() for t in kept]
+        ctx.save_for_backward(*[t._buffer for t in kept if t is not None])
+        y = kind.product(x_rows, w_rows, x.dtype)
         return y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        need_x, need_w = ctx.needs_input_grad[:2]
-        # only the input's gradient reads the weight's copies
-        if need_x and ctx.weight is not None and ctx.weight.version != ctx.version:
-            raise RuntimeError("the MXWeight was refreshed between the forward and the backward pass")
+        kind, (need_x, need_w) = ctx.kind, ctx.needs_input_grad[:2]
+        if need_x:                                   # only the input's gradient reads the weight's copies
+            _check_fresh(ctx, kind)
         saved = list(ctx.saved_tensors)
-        x_cols, w_cols = [None if k is None else MXTensor._over(saved.pop(0), *k) for k in ctx.kept]
+        x_cols, w_cols = [None if k is None else kind.tensor._over(saved.pop(0), *k) for k in ctx.kept]
         flat = _flat(dy)
         layout = "both" if need_x and need_w else "rows" if need_x else "cols"
-        q = flashopt_mx_quantize(flat, layout)
+        q = kind.quantize(flat, layout, grad=True)
         dy_rows, dy_cols = q if layout == "both" else (q, q)
-        dx = flashopt_mx_product(dy_rows, w_cols, ctx.x_dtype).view(ctx.x_shape) if need_x else None
-        dw = flashopt_mx_product(dy_cols, x_cols, ctx.w_dtype) if need_w else None
-        return dx, dw, None, None
+        dx = kind.product(dy_rows, w_cols, ctx.x_dtype).view(ctx.x_shape) if need_x else None
+        dw = kind.product(dy_cols, x_cols, ctx.w_dtype) if need_w else None
+        return dx, dw, None, None, None
+
+
+def _operands(x, weight, held_type):
+    """(weight parameter, its holder or None) of a linear layer's call."""
+    w, held = (weight.param, weight) if isinstance(weight, held_type) else (weight, None)
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")
+    return w, held
 
 
 def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
@@ -1307,7 +1373,445 @@ def mx_linear(x: torch.Tensor, weight) -> torch.Tensor:
     current stream.  In a graph, capture forward and backward together, with no
     eager graph of the same parameters alive (autograd would reach for that
     one's stream)."""
-    w, held = (weight.param, weight) if isinstance(weight, MXWeight) else (weight, None)
-    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
-        raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")
-    return _MXLinear.apply(x, w, held, torch.is_grad_enabled())
+    w, held = _operands(x, weight, MXWeight)
+    return _Linear.apply(x, w, held, torch.is_grad_enabled(), _MX())
+
+
+# --------------------------------------------------------------- 8 bits
+
+FP8_BLOCK = 128
+FORMATS = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def flashopt_byte_code_bytes(rows: int, cols: int) -> int:
+    return lib().flashopt_byte_code_bytes(rows, cols)
+
+
+def flashopt_byte_scale_bytes(rows: int, cols: int) -> int:
+    return lib().flashopt_byte_scale_bytes(rows, cols)
+
+
+def _fp8_widths(cols: int):
+    """Bytes of a row of codes, and of its scales."""
+    return FP8_BLOCK * ((cols + FP8_BLOCK - 1) // FP8_BLOCK), 16 * ((cols + 2047) // 2048)
+
+
+class FP8Tensor:
+    """A rows x cols matrix in 8 bits: a float8_e4m3fn or float8_e5m2 tensor of
+    codes, rows padded to 128, and a uint8 one of E8M0 scales, one for each 128
+    codes, rows padded to 16."""
+
+    __slots__ = ("rows", "cols", "dtype", "format", "device", "code_ptr", "scale_ptr", "_codes", "_scales",
+                 "_buffer", "replayed")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        if codes.dtype not in FORMATS:
+            raise ValueError(f"codes must be float8_e4m3fn or float8_e5m2, got {codes.dtype}")
+        if scales.dtype != torch.uint8:
+            raise ValueError(f"scales must be uint8, got {scales.dtype}")
+        for t, name, width in zip((codes, scales), ("codes", "scales"), _fp8_widths(cols)):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous device tensor")
+            if t.numel() < rows * width:
+                raise ValueError(f"{name} holds {t.numel()} bytes, {rows * width} needed")
+        if codes.device != scales.device:
+            raise ValueError(f"codes are on {codes.device}, scales on {scales.device}")
+        self.rows, self.cols, self.device = rows, cols, codes.device
+        self.dtype, self.format = codes.dtype, FORMATS[codes.dtype]
+        self.code_ptr, self.scale_ptr = codes.data_ptr(), scales.data_ptr()
+        self._codes, self._scales, self._buffer, self.replayed = codes, scales, None, False
+
+    @staticmethod
+    def empty(rows: int, cols: int, device, dtype=torch.float8_e4m3fn) -> "FP8Tensor":
+        """Uninitialized, codes and then scales in one buffer."""
+        buffer = torch.empty(rows * sum(_fp8_widths(cols)), dtype=torch.uint8, device=device)
+        return FP8Tensor._over(buffer, rows, cols, dtype)
+
+    @staticmethod
+    def _over(buffer: torch.Tensor, rows: int, cols: int, dtype) -> "FP8Tensor":
+        q = object.__new__(FP8Tensor)
+        q.rows, q.cols, q.device, q._buffer, q._codes, q._scales = rows, cols, buffer.device, buffer, None, None
+        q.dtype, q.format = dtype, FORMATS[dtype]
+        q.code_ptr = buffer.data_ptr()
+        q.scale_ptr = q.code_ptr + rows * _fp8_widths(cols)[0]
+        q.replayed = False
+        return q
+
+    def _size(self):
+        return self.rows, self.cols, self.dtype
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            width = _fp8_widths(self.cols)[0]
+            self._codes = self._buffer[:self.rows * width].view(self.dtype).view(self.rows, width)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            width, scales = _fp8_widths(self.cols)
+            self._scales = self._buffer[self.rows * width:].view(self.rows, scales)
+        return self._scales
+
+    _written = MXTensor._written
+
+    def __repr__(self):
+        return f"FP8Tensor({self.rows} x {self.cols}, {self.dtype}, {self.device})"
+
+
+def _format(dtype) -> int:
+    if dtype not in FORMATS:
+        raise ValueError(f"dtype must be float8_e4m3fn or float8_e5m2, got {dtype}")
+    return FORMATS[dtype]
+
+
+def _fp8_target(q, rows, cols, device, dtype):
+    if q is None:
+        return FP8Tensor.empty(rows, cols, device, dtype)
+    if (q.rows, q.cols, q.dtype) != (rows, cols, dtype):
+        raise ValueError(f"out is {q.rows} x {q.cols} of {q.dtype}, {rows} x {cols} of {dtype} needed")
+    _same_device(device, q, "out")
+    q._written()
+    return q
+
+
+def _fp8_targets(out, layout, rows, cols, device, dtype):
+    """(along rows, of the transpose) for a layout, each or None, and their four
+    addresses."""
+    first, second = out if layout == "both" and out is not None else (out, out)
+    q = None if layout == "cols" else _fp8_target(first, rows, cols, device, dtype)
+    t = None if layout == "rows" else _fp8_target(second, cols, rows, device, dtype)
+    pointers = [p for one in (q, t) for p in ((one.code_ptr, one.scale_ptr) if one else (None, None))]
+    return q, t, *pointers
+
+
+def flashopt_byte_quantize(x: torch.Tensor, layout: str = "rows", block: bool = False, dtype=torch.float8_e4m3fn,
+                          out=None, stream=None):
+    """8 bits of a bf16 or fp32 matrix, one scale for each 128 elements: layout
+    "rows", along its rows; "cols", x transposed, along x's columns; "both", the
+    pair of them from one read.  block: one scale for each 128 x 128, as for a
+    weight.  out: an FP8Tensor (a pair for "both") to write to."""
+    ptr, wide, rows, cols, stride = _matrix(x, "x")
+    if layout not in ("rows", "cols", "both"):
+        raise ValueError("layout must be 'rows', 'cols' or 'both'")
+    fmt = _format(dtype)
+    with _on(x.device, stream):
+        q, t, c, sc, ct, sct = _fp8_targets(out, layout, rows, cols, x.device, dtype)
+        status = lib().flashopt_byte_quantize(ptr, wide, rows, cols, stride, fmt, int(block), c, sc, ct, sct,
+                                             _stream(None))
+    _check(status, "flashopt_byte_quantize")
+    return (q, t) if layout == "both" else (q or t)
+
+
+def flashopt_byte_dequantize(q: FP8Tensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """The bf16 or fp32 values of an FP8Tensor."""
+    with _on(q.device, stream):
+        out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
+        ptr, wide, rows, cols, stride = _matrix(out, "out")
+        status = lib().flashopt_byte_dequantize(q.code_ptr, q.scale_ptr, q.format, rows, cols, ptr, wide, stride,
+                                               _stream(None))
+    _check(status, "flashopt_byte_dequantize")
+    return out
+
+
+def flashopt_byte_product(a: FP8Tensor, b: FP8Tensor, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """a b^T of two FP8Tensors with the same number of columns, b in E4M3, in
+    bf16 or fp32."""
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+    if b.format != 0:
+        raise ValueError("b must be float8_e4m3fn")
+    dev = a.device
+    _same_device(dev, b, "b")
+    with _on(dev, stream):
+        out = _out_matrix(out, a.rows, b.rows, dtype, dev)
+        ptr, wide, m, n, stride = _matrix(out, "out")
+        status = lib().flashopt_byte_product(a.code_ptr, a.scale_ptr, a.format, b.code_ptr, b.scale_ptr, m, n, a.cols,
+                                            ptr, wide, stride, _stream(None))
+    _check(status, "flashopt_byte_product")
+    return out
+
+
+def flashopt_byte_linear_workspace_bytes(m: int, k: int) -> int:
+    return lib().flashopt_byte_linear_workspace_bytes(m, k)
+
+
+def flashopt_byte_linear(x: torch.Tensor, w: FP8Tensor, dtype=None, out=None, workspace=None, stream=None):
+    """x w^T of a bf16 or fp32 matrix, quantized to E4M3 on the way, and 8-bit
+    weights (no gradients: fp8_linear has them); in x's dtype unless given.  out
+    must not share elements with x."""
+    ptr, wide, m, k, stride = _matrix(x, "x")
+    if k != w.cols:
+        raise ValueError(f"x has {k} columns, w {w.cols}")
+    if w.format != 0:
+        raise ValueError("w must be float8_e4m3fn")
+    dev = x.device
+    _same_device(dev, w, "w")
+    with _on(dev, stream):
+        out = _out_matrix(out, m, w.rows, dtype or x.dtype, dev)
+        optr, owide, _, n, ostride = _matrix(out, "out")
+        if workspace is None:
+            workspace = torch.empty(m * sum(_fp8_widths(k)), dtype=torch.uint8, device=dev)
+        else:
+            _same_device(dev, workspace, "workspace")
+        status = lib().flashopt_byte_linear(ptr, wide, m, k, stride, w.code_ptr, w.scale_ptr, n, optr, owide, ostride,
+                                           _dev(workspace, "workspace"),
+                                           workspace.numel() * workspace.element_size(), _stream(None))
+    _check(status, "flashopt_byte_linear")
+    return out
+
+
+class FP8Weight:
+    """A weight parameter (bf16 or fp32, [out, in]) with its E4M3 copies, one
+    scale for each 128 x 128: `rows` for the forward product, `cols`
+    (transposed, of the same values) for the input's gradient.  refresh() and
+    replays as for MXWeight."""
+
+    def __init__(self, param: torch.Tensor):
+        self.param = param
+        self.version = 0
+        self.rows, self.cols = flashopt_byte_quantize(param.detach(), "both", block=True)
+        if torch.cuda.is_current_stream_capturing():        # replays write these as well
+            self.rows.replayed = self.cols.replayed = True
+
+    def refresh(self, stream=None):
+        self.version += 1
+        flashopt_byte_quantize(self.param.detach(), "both", block=True, out=(self.rows, self.cols), stream=stream)
+
+
+class _FP8:
+    """8 bits as a linear layer uses them: output gradients in `grad_dtype`."""
+    name, tensor = "FP8Weight", FP8Tensor
+
+    def __init__(self, grad_dtype):
+        _format(grad_dtype)
+        self.grad_dtype = grad_dtype
+
+    def quantize(self, x, layout, weight=False, grad=False):
+        return flashopt_byte_quantize(x, layout, block=weight, dtype=self.grad_dtype if grad else torch.float8_e4m3fn)
+
+    def product(self, a, b, dtype):
+        return flashopt_byte_product(a, b, dtype)
+
+
+def fp8_linear(x: torch.Tensor, weight, grad_dtype=torch.float8_e4m3fn) -> torch.Tensor:
+    """A linear layer in 8 bits with gradients: x [..., in] and a weight
+    parameter [out, in] or an FP8Weight.  grad_dtype: the format of the output's
+    gradient (float8_e5m2 where its range within 128 elements is wide).
+    Otherwise as mx_linear."""
+    w, held = _operands(x, weight, FP8Weight)
+    return _Linear.apply(x, w, held, torch.is_grad_enabled(), _FP8(grad_dtype))
+
+
+# --------------------------------------------------------------- norm
+
+def _vector(t: torch.Tensor, name: str, cols: int, device):
+    """(address, fp32 flag) of a contiguous bf16 or fp32 vector."""
+    if t.dtype != torch.bfloat16 and t.dtype != torch.float32:
+        raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != cols:
+        raise ValueError(f"{name} must be a vector of {cols}, got {tuple(t.shape)}")
+    _same_device(device, t, name)
+    return _dev(t, name), int(t.dtype == torch.float32)
+
+
+def _alike(t: torch.Tensor, name: str, x: torch.Tensor):
+    """(address, row stride) of a matrix of x's size, type and device."""
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(t.shape)}")
+    if t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {x.dtype}, got {t.dtype}")
+    ptr, _, _, _, stride = _matrix(t, name)
+    _same_device(x.device, t, name)
+    return ptr, stride
+
+
+def flashopt_rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: float = 1e-6, output: str = "values",
+                      dtype=torch.float8_e4m3fn, out=None, h=None, rstd=None, stream=None):
+    """(y, h) with h = x + residual (x itself without one) and y the
+    root-mean-square norm of h's rows times gain [cols].  output: "values", y in
+    x's dtype; "rows", "cols" or "both", the FP8Tensors of flashopt_byte_quantize
+    in their place.  out: a tensor (or FP8Tensors) for y; h: one for the sum,
+    which may be x or residual itself; rstd: an fp32 tensor for the rows' 1 / root,
+    which flashopt_rms_norm_backward takes."""
+    xp, wide, rows, cols, stride = _matrix(x, "x")
+    if output not in ("values", "rows", "cols", "both"):
+        raise ValueError("output must be 'values', 'rows', 'cols' or 'both'")
+    fmt, dev = _format(dtype), x.device
+    gp, gwide = _vector(gain, "gain", cols, dev)
+    rp, rstride = (None, 0) if residual is None else _alike(residual, "residual", x)
+    if h is not None and residual is None:
+        raise ValueError("without a residual there is no sum to write to h")
+    with _on(dev, stream):
+        hp, hstride, yp, ystride, q, t, c, sc, ct, sct = None, 0, None, 0, None, None, None, None, None, None
+        if residual is not None:
+            h = torch.empty((rows, cols), dtype=x.dtype, device=dev) if h is None else h
+            hp, hstride = _alike(h, "h", x)
+        if output == "values":
+            out = torch.empty((rows, cols), dtype=x.dtype, device=dev) if out is None else out
+            yp, ystride = _alike(out, "out", x)
+        else:
+            q, t, c, sc, ct, sct = _fp8_targets(out, output, rows, cols, dev, dtype)
+            out = (q, t) if output == "both" else (q or t)
+        if rstd is None and t is not None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        args = flashopt_norm_args(xp, rp, gp, hp, yp, c, sc, ct, sct,
+                                  None if rstd is None else _buf(rstd, "rstd", dev, (4,), rows, float32=True),
+                                  rows, cols, stride, rstride, hstride, ystride, eps, wide, gwide, fmt, 0)
+        status = lib().flashopt_rms_norm(ctypes.byref(args), _stream(None))
+    _check(status, "flashopt_rms_norm")
+    return out, x if residual is None else h
+
+
+def flashopt_rms_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return lib().flashopt_rms_norm_backward_workspace_bytes(rows, cols)
+
+
+def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Tensor, rstd: torch.Tensor, dh=None,
+                               need_dx: bool = True, need_dgain: bool = True, dx=None, dgain=None, workspace=None,
+                               stream=None):
+    """(dx, dgain) of flashopt_rms_norm from its h and rstd: dx, in h's dtype, is
+    the gradient of x and of the residual, with dh, h's own gradient, added;
+    None for one that is not needed.  dx may be dy or dh itself."""
+    hp, wide, rows, cols, hstride = _matrix(h, "h")
+    dev = h.device
+    gp, gwide = _vector(gain, "gain", cols, dev)
+    yp, ystride = _alike(dy, "dy", h)
+    ep, estride = (None, 0) if dh is None else _alike(dh, "dh", h)
+    sp = _buf(rstd, "rstd", dev, (4,), rows, float32=True)
+    with _on(dev, stream):
+        xp, xstride, dp, nbytes = None, 0, None, 0
+        if need_dx:
+            dx = torch.empty((rows, cols), dtype=h.dtype, device=dev) if dx is None else dx
+            xp, xstride = _alike(dx, "dx", h)
+        if need_dgain:
+            dgain = torch.empty(cols, dtype=gain.dtype, device=dev) if dgain is None else dgain
+            dp, dwide = _vector(dgain, "dgain", cols, dev)
+            if dwide != gwide:
+                raise ValueError(f"dgain must be {gain.dtype}, got {dgain.dtype}")
+            if workspace is None:
+                workspace = torch.empty(flashopt_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
+                                        device=dev)
+            _same_device(dev, workspace, "workspace")
+            nbytes = workspace.numel() * workspace.element_size()
+        args = flashopt_norm_grad_args(yp, ep, hp, gp, sp, xp, dp,
+                                       _dev(workspace, "workspace") if need_dgain else None, nbytes, rows, cols,
+                                       ystride, estride, hstride, xstride, wide, gwide)
+        status = lib().flashopt_rms_norm_backward(ctypes.byref(args), _stream(None))
+    _check(status, "flashopt_rms_norm_backward")
+    return dx if need_dx else None, dgain if need_dgain else None
+
+
+def _norm_operands(x, gain, residual):
+    if x.dim() < 1 or gain.dim() != 1 or x.shape[-1] != gain.shape[0]:
+        raise ValueError(f"x {tuple(x.shape)} and gain {tuple(gain.shape)} do not match")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError(f"residual must be {tuple(x.shape)} of {x.dtype}, got {tuple(residual.shape)} of "
+                         f"{residual.dtype}")
+
+
+def _norm_backward(ctx, dy, dh, h, gain, rstd, need_dx, need_gain):
+    """(dx in x's shape, dgain) from the gradients of the norm's outputs, either
+    of which may be missing."""
+    if dy is None:
+        return dh if need_dx else None, None
+    dx, dgain = flashopt_rms_norm_backward(dy, _flat(h), gain, rstd, None if dh is None else _flat(dh), need_dx,
+                                           need_gain)
+    return None if dx is None else dx.view(ctx.x_shape), dgain
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gain, residual, eps):
+        ctx.set_materialize_grads(False)
+        flat = _flat(x)
+        rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        y, h = flashopt_rms_norm(flat, gain, None if residual is None else _flat(residual), eps, rstd=rstd)
+        ctx.x_shape = x.shape
+        y = y.view(x.shape)
+        if residual is None:
+            ctx.save_for_backward(x, gain, rstd)
+            return y
+        h = h.view(x.shape)
+        ctx.save_for_backward(h, gain, rstd)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        need_x, need_gain, need_residual = ctx.needs_input_grad[:3]
+        h, gain, rstd = ctx.saved_tensors
+        dx, dgain = _norm_backward(ctx, None if dy is None else _flat(dy), dh, h, gain, rstd,
+                                   need_x or need_residual, need_gain)
+        return dx if need_x else None, dgain, dx if need_residual else None, None
+
+
+def rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: float = 1e-6):
+    """(y, h) with gradients: h = x + residual (x itself without one), x [...,
+    cols], and y the root-mean-square norm of h times gain [cols], in x's dtype.
+    Work goes to the current stream; graphs as for mx_linear."""
+    _norm_operands(x, gain, residual)
+    if residual is None:
+        return _RMSNorm.apply(x, gain, None, eps), x
+    return _RMSNorm.apply(x, gain, residual, eps)
+
+
+class _FP8NormLinear(torch.autograd.Function):
+    """rms_norm, then _Linear on its output, which exists in 8 bits only."""
+
+    @staticmethod
+    def forward(ctx, x, gain, w, residual, weight, eps, grad, kind):
+        ctx.set_materialize_grads(False)
+        need_x, need_gain, need_w, need_residual = [need and grad for need in ctx.needs_input_grad[:4]]
+        need_dy = need_x or need_gain or need_residual
+        w_rows, w_cols, weight = _weight_copies(kind, w, weight, need_dy)
+        flat = _flat(x)
+        rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        q, h = flashopt_rms_norm(flat, gain, None if residual is None else _flat(residual), eps,
+                                 "both" if need_w else "rows", rstd=rstd)
+        rows, cols = q if need_w else (q, None)
+        ctx.kind, ctx.weight, ctx.version = kind, weight, None if weight is None else weight.version
+        ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
+        h = x if residual is None else h.view(x.shape)
+        kept = (cols, w_cols if need_dy else None)
+        ctx.kept = [None if t is None else t._size() for t in kept]
+        ctx.save_for_backward(h, gain, rstd, *[t._buffer for t in kept if t is not None])
+        y = kind.product(rows, w_rows, x.dtype).view(*x.shape[:-1], w.shape[0])
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        kind, (need_x, need_gain, need_w, need_residual) = ctx.kind, ctx.needs_input_grad[:4]
+        need_dx = need_x or need_residual
+        h, gain, rstd, *saved = ctx.saved_tensors
+        cols, w_cols = [None if k is None else kind.tensor._over(saved.pop(0), *k) for k in ctx.kept]
+        dn = dw = None
+        if dy is not None:
+            layouts = [name for name, need in (("rows", need_dx or need_gain), ("cols", need_w)) if need]
+            if layouts[0] == "rows":
+                _check_fresh(ctx, kind)
+            layout = "both" if len(layouts) == 2 else layouts[0]
+            q = kind.quantize(_flat(dy), layout, grad=True)
+            dy_rows, dy_cols = q if layout == "both" else (q, q)
+            if "rows" in layouts:
+                dn = kind.product(dy_rows, w_cols, ctx.x_dtype)
+            if "cols" in layouts:
+                dw = kind.product(dy_cols, cols, ctx.w_dtype)
+        dx, dgain = (None, None) if not need_dx and not need_gain else _norm_backward(
+            ctx, dn, dh, h, gain, rstd, need_dx, need_gain)
+        return dx if need_x else None, dgain, dw, dx if need_residual else None, None, None, None, None
+
+
+def fp8_norm_linear(x: torch.Tensor, gain: torch.Tensor, weight, residual=None, eps: float = 1e-6,
+                    grad_dtype=torch.float8_e4m3fn):
+    """(out, h): rms_norm and fp8_linear on its output in one, with gradients.
+    The norm writes its output in 8 bits, along rows for the product and along
+    columns for the weight's gradient, and in no other form.  weight: a
+    parameter [out, in] (several projections stacked share one norm) or an
+    FP8Weight."""
+    w, held = _operands(x, weight, FP8Weight)
+    _norm_operands(x, gain, residual)
+    args = (x, gain, w, residual, held, eps, torch.is_grad_enabled(), _FP8(grad_dtype))
+    return (_FP8NormLinear.apply(*args), x) if residual is None else _FP8NormLinear.apply(*args)

@@ -1,7 +1,8 @@
 /*
  * flashopt.h -- C ABI of libflashopt.so, the MI355X (gfx950) FlashAdamW and
  * FlashSGD steps, and what a training step around them needs: the gradient
- * norm and clipping, and matrix products in 4 bits (MXFP4).
+ * norm and clipping, matrix products in 4 bits (MXFP4) and in 8, and the
+ * root-mean-square norm in front of them.
  *
  * The steps' method is described on the pages
  *   "code/flashsim/quantization.py"    (group-32 companded int8/uint8 state codec,
@@ -35,8 +36,8 @@
  *   - Alignment: every element stream (fp32, bf16, codes, rho) must start on a
  *     16-byte boundary, scale arrays on a 2-byte boundary; otherwise
  *     FLASHOPT_EALIGN.  Allocations from hipMalloc / torch satisfy this.
- *     Gradients of a norm and matrices of the MXFP4 calls may start at any
- *     element; those calls state their own rules, and what they do with
+ *     Gradients of a norm and matrices of the MXFP4, 8-bit and root-mean-square
+ *     norm calls may start at any element; those calls state their own rules, and what they do with
  *     non-finite values.
  *   - A step call launches its step kernel once.  A list (or tensor) of more
  *     than 2^25 - 2 chunks of 1024 elements (2^24 - 1 with fp32 states or
@@ -55,7 +56,7 @@
 extern "C" {
 #endif
 
-#define FLASHOPT_ABI_VERSION 9
+#define FLASHOPT_ABI_VERSION 10
 
 typedef enum {
     FLASHOPT_OK = 0,
@@ -550,6 +551,135 @@ flashopt_status flashopt_mx_linear(const void *x, int x_fp32, int64_t m, int64_t
                                    int64_t x_stride, const void *w_codes, const void *w_scales,
                                    int64_t n, void *out, int out_fp32, int64_t out_stride,
                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Matrices of byte floats: E4M3 (to 448) or E5M2 (to 57344) codes with one E8M0
+ * scale byte, 2^(byte - 127), for each 128 elements along a row.  Storage of an
+ * R x C matrix:
+ *   codes   R rows of 128 ceil(C / 128) bytes
+ *   scales  R rows of ceil(C / 128) bytes, padded to a multiple of 16
+ * Padding is code 0 and scale byte 0.  codes and scales 16-byte aligned.  Sizes
+ * and shared memory as for MXFP4.
+ *
+ * Bytes of an R x C matrix's codes and of its scales (0 for an empty one): */
+enum {
+    FLASHOPT_E4M3 = 0,
+    FLASHOPT_E5M2 = 1
+};
+size_t flashopt_byte_code_bytes(int64_t rows, int64_t cols);
+size_t flashopt_byte_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantization of a row-major bf16 or fp32 matrix, rows row_stride elements
+ * apart.  Per group: the scale is the smallest power of two, at least 2^-127,
+ * under which max |x| is at most the format's largest value; codes = x / scale
+ * rounded half to even (none saturates).  A group of zeros has byte 0.  A group
+ * with an infinity or NaN has byte 255, which stands for NaN, and codes 0.
+ *   block              0: groups of 128 elements; 1: blocks of 128 x 128 (a
+ *                      weight), whose byte is stored for each of their rows:
+ *                      x and its transpose then stand for the same values
+ *   codes, scales      of x, groups along its rows; or both NULL
+ *   codes_t, scales_t  of x transposed (cols x rows), groups along x's
+ *                      columns; or both NULL.  Both pairs come from one read
+ *   x                  aligned to its element; row_stride >= 0
+ * Errors: EINVAL (negative or too large sizes, x_fp32 or block not 0 or 1, an
+ * unknown format, NULL x, no or half an output pair, outputs that overlap, 2^24
+ * tiles of 128 x 128 or more), EALIGN, EHIP.  An empty matrix is a no-op. */
+flashopt_status flashopt_byte_quantize(const void *x, int x_fp32, int64_t rows, int64_t cols,
+                                      int64_t row_stride, int format, int block, void *codes,
+                                      void *scales, void *codes_t, void *scales_t, void *stream);
+
+/* The values codes and scales stand for, to bf16 or fp32 (fp32 holds them
+ * exactly up to its largest value; bf16 also rounds those below 2^-126).  out:
+ * aligned to its element, row_stride >= cols.  Errors: as above. */
+flashopt_status flashopt_byte_dequantize(const void *codes, const void *scales, int format,
+                                        int64_t rows, int64_t cols, void *out, int out_fp32,
+                                        int64_t row_stride, void *stream);
+
+/* out[i, j] = sum over k of a[i, k] b[j, k]: the product of an m x k matrix of
+ * either format and an n x k one of E4M3, accumulated in fp32 by the matrix
+ * instructions and rounded once to out's type (bf16 to nearest even).  The
+ * instructions form each sum of eight consecutive products to 2^-13 of the
+ * largest one's binade (a relative 2e-5 of an output on normally distributed
+ * operands, a hundredth of bf16's own rounding).  One launch.  A NaN scale makes its row's (or column's) outputs NaN.  k == 0
+ * writes zeros.  A linear layer takes three of these, as for MXFP4.
+ * Errors: EINVAL (sizes, k above 2^24 - 128, out_fp32, a_format, row_stride <
+ * n, NULL), EALIGN, EHIP. */
+flashopt_status flashopt_byte_product(const void *a_codes, const void *a_scales, int a_format,
+                                     const void *b_codes, const void *b_scales, int64_t m, int64_t n,
+                                     int64_t k, void *out, int out_fp32, int64_t row_stride,
+                                     void *stream);
+
+/* y = quantize(x) w^T for serving: x [m, k] bf16 or fp32, quantized to E4M3
+ * along its rows, w [n, k] laid out once.  The result is that of
+ * flashopt_byte_quantize and flashopt_byte_product.
+ *   workspace  DEVICE, 16-byte aligned, holds x's codes until the call has run
+ *   out        may lie between x's columns (the same bytes from row to row),
+ *              but shares no element with x
+ * Errors: as those calls; EWORKSPACE. */
+size_t flashopt_byte_linear_workspace_bytes(int64_t m, int64_t k);
+flashopt_status flashopt_byte_linear(const void *x, int x_fp32, int64_t m, int64_t k,
+                                    int64_t x_stride, const void *w_codes, const void *w_scales,
+                                    int64_t n, void *out, int out_fp32, int64_t out_stride,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Root-mean-square norm of each row, with the residual's addition and an output
+ * in the input's type, in 8 bits, or both:
+ *   h = x + residual          fp32, rounded to their type (x without a residual)
+ *   r = 1 / sqrt(mean h^2 + eps)      in fp64, rounded to fp32
+ *   y = (h r) gain            fp32 products, rounded to the type of x
+ *   codes, codes_t            of the fp32 y, as flashopt_byte_quantize (block 0)
+ * Rows are their stride in elements apart and start at any element.  What is
+ * written shares no memory with what is read, but for h, which may be x or
+ * residual itself (the same address and stride).  One launch; two with codes_t,
+ * whose scales need the statistics of 128 rows.  An infinity or NaN in a row
+ * makes its y what the formula says (zeros and NaN, or all NaN). */
+typedef struct {
+    const void *x;            /* [rows, cols] bf16 or fp32 (fp32 below)       */
+    const void *residual;     /* the same, or NULL                            */
+    const void *gain;         /* [cols] bf16 or fp32 (gain_fp32 below)        */
+    void *h;                  /* [rows, cols] written; NULL without residual  */
+    void *y;                  /* [rows, cols] written, or NULL                */
+    void *codes, *scales;     /* y in 8 bits along rows; or both NULL         */
+    void *codes_t, *scales_t; /* y transposed in 8 bits; or both NULL         */
+    float *rstd;              /* [rows] r, written; or NULL.  With codes_t it
+                                 is needed                                    */
+    int64_t rows, cols;
+    int64_t x_stride, residual_stride, h_stride, y_stride;
+    double eps;               /* >= 0, finite                                 */
+    int32_t fp32, gain_fp32;  /* 0: bf16, 1: fp32                             */
+    int32_t format;           /* FLASHOPT_E4M3 | FLASHOPT_E5M2, of the codes  */
+    int32_t reserved;         /* 0                                            */
+} flashopt_norm_args;
+/* Errors: EINVAL (NULL args, sizes, strides, eps, types, reserved, NULL x or
+ * gain, h without residual or the reverse, no or half an output pair, codes_t
+ * without rstd, memory shared other than as above, 2^24 tiles of 128 x 128 or
+ * more with codes_t), EALIGN, EHIP.  An empty matrix is a no-op. */
+flashopt_status flashopt_rms_norm(const flashopt_norm_args *args, void *stream);
+
+/* The backward pass, from the h and rstd that flashopt_rms_norm left: with u =
+ * dy gain, t = h r, c = mean(u t) of a row,
+ *   dx    = r (u - t c) + dh  fp32, rounded to the type of h: the gradient of
+ *                             x and of the residual
+ *   dgain = sum over rows of dy t, in an order that depends only on the sizes
+ * What is written shares no memory with what is read, but for dx, which may be
+ * dy or dh itself. */
+typedef struct {
+    const void *dy;           /* [rows, cols], of h's type                    */
+    const void *dh;           /* h's own gradient, or NULL                    */
+    const void *h;            /* [rows, cols] bf16 or fp32                    */
+    const void *gain;         /* [cols]                                       */
+    const float *rstd;        /* [rows]                                       */
+    void *dx;                 /* [rows, cols] written, or NULL                */
+    void *dgain;              /* [cols] of gain's type, written, or NULL      */
+    void *workspace;          /* DEVICE, 16-byte aligned, for dgain           */
+    size_t workspace_bytes;
+    int64_t rows, cols;       /* cols at most 32768                           */
+    int64_t dy_stride, dh_stride, h_stride, dx_stride;
+    int32_t fp32, gain_fp32;
+} flashopt_norm_grad_args;
+/* Errors: as flashopt_rms_norm (EINVAL also for neither dx nor dgain and for
+ * more than 32768 columns); EWORKSPACE.  No rows: dgain is zeros. */
+size_t flashopt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, void *stream);
 
 /* Static string naming a status code. */
 const char *flashopt_status_str(flashopt_status status);
