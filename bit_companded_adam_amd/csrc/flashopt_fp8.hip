@@ -406,6 +406,304 @@ fp8_skinny_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restr
     }
 }
 
+// Accumulators of 32 x 32 blocks, TN along out's rows and TM of them, to out.
+// Block element e of a lane is m = lane % 32, n = 8 (e / 4) + 4 (lane / 32) + e
+// % 4: 16 bytes of a row at most, where a store of part of a line costs L2 as
+// much as one of a whole line.  Each wavefront turns a few rows at a time over
+// in LDS of its own and stores them in 16-byte pieces, whole lines of bf16; the
+// next tile's copies run meanwhile.
+__host__ __device__ constexpr int stage_rows(bool f32) { return f32 ? 8 : 16; }
+__host__ __device__ constexpr int stage_bytes(bool f32, int tn) { return stage_rows(f32) * tn * 32 * (f32 ? 4 : 2); }
+
+template <bool F32, int TN, int TM>
+__device__ __forceinline__ void store_blocks(const f32x16 (&acc)[TN][TM], uint8_t *stage, int lane, int64_t m_first,
+                                             int64_t n_first, int64_t rows, int64_t cols, uint8_t *out,
+                                             int64_t row_bytes)
+{
+    constexpr int kEsz = F32 ? 4 : 2, kPitch = TN * 32 * kEsz, kR = stage_rows(F32), kPieces = kPitch / 16;
+    const int g = lane >> 5;
+    // where piece c of row r lies in the row, so that 16 rows' pieces c fall on
+    // all banks
+    auto turned = [](int r, int c) { return (c ^ ((r * kPieces / 16) & (kPieces - 1))) * 16; };
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kR) {
+            if ((lane & (32 - kR)) == r0) {
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const f32x16 &x = acc[i][j];
+                        const int r = lane & (kR - 1), n = i * 32 + 2 * e + 4 * g;
+                        uint8_t *p = stage + r * kPitch + turned(r, n * kEsz / 16) + n * kEsz % 16;
+                        if constexpr (F32)
+                            *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                        else
+                            *reinterpret_cast<u32x2 *>(p) =
+                                u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
+                    }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int u0 = 0; u0 < kR * kPieces; u0 += kWaveLanes) {
+                const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
+                const int64_t m = m_first + j * 32 + r0 + r, n = n_first + c * (16 / kEsz);
+                if (u < kR * kPieces && m < rows && n < cols) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + turned(r, c));
+                    uint8_t *o = out + m * row_bytes + n * kEsz;
+                    // (nontemporal stores save 1-4% here and cost as much where
+                    // out is read next)
+                    if (n + 16 / kEsz <= cols) {
+                        *reinterpret_cast<u32x4_packed *>(o) = w;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 16 / kEsz; ++x) {
+                            if (n + x >= cols) break;
+                            if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
+                            else
+                                reinterpret_cast<uint16_t *>(o)[x] =
+                                    static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
+                        }
+                    }
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+}
+
+// Larger products: a workgroup computes a BN x BM tile of out^T, its
+// wavefronts in a WN x WM arrangement of 32 x 32 accumulator blocks.
+//
+// Each K step is one group of 128 elements, one 128-byte line of every row,
+// copied from global memory to LDS by the DMA (16 bytes to a lane, eight rows
+// an instruction).  LDS holds row r's 16-byte chunk c at slot c ^ (r / 2 & 7)
+// of the row's 128 bytes: the DMA writes lanes in order, so each lane fetches
+// the chunk that belongs to its slot, and the 32 rows that an operand read
+// takes at one c then fall on all banks.  Two buffers, and one barrier past the
+// middle of a step: by then its buffer has been read, so the copy of the step
+// after next goes there, and the next step's first operands are fetched, under
+// the remaining products.
+//
+// A step is two products of 64 elements on each block.  They run along A's
+// blocks, each with all of B's: a wavefront holds B's operands of both halves
+// and a ring of A's, of eight registers each, which leaves room for 128
+// accumulators among 256 registers.
+//
+// Scales: each thread carries 16 bytes of one row, sixteen steps' worth, through
+// a register to LDS; a lane fetches a word, four steps' worth, of each of its
+// rows and shifts it by a byte a step.
+template <int BN, int BM, int WN, int WM>
+struct Tile {
+    static constexpr int kWaves = WN * WM;
+    static constexpr int kTileThreads = kWaves * kWaveLanes;
+    static constexpr int kRows = BN + BM;                  // rows of B, then of A
+    static constexpr int kBytes = kRows * 128;             // one buffer
+    static constexpr int kCopies = kRows / 8 / kWaves;     // DMA instructions of a wavefront and step
+    static constexpr int kTN = BN / WN / 32, kTM = BM / WM / 32;
+    static constexpr int kWavesPerSimd = BN * BM >= 128 * 128 ? 2 : 4;
+    // A's operands of a step in their order, the ring that holds them, and how
+    // far ahead of its products one is fetched
+    static constexpr int kSeq = 2 * kTM, kRing = kSeq < 4 ? kSeq : 4, kAhead = kRing - 1;
+    static constexpr int kLds(bool f32) { return 2 * kBytes + 2 * kRows * 16 + kWaves * stage_bytes(f32, kTN); }
+    static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 && kSeq % kRing == 0 &&
+                      kRows <= kTileThreads && BN % (8 * kCopies) == 0 && BN % kWaveLanes == 0, "tile");
+};
+
+template <bool F32, int FMT, int BN, int BM, int WN, int WM>
+__global__ void __launch_bounds__(WN *WM *kWaveLanes)
+    __attribute__((amdgpu_waves_per_eu(Tile<BN, BM, WN, WM>::kWavesPerSimd)))
+fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, uint32_t tiles_m,
+                uint8_t *__restrict__ out, int64_t row_bytes)
+{
+    using T = Tile<BN, BM, WN, WM>;
+    constexpr int kTN = T::kTN, kTM = T::kTM;
+    __shared__ __align__(128) uint8_t s_buf[2][T::kBytes];
+    __shared__ uint32_t s_scales[2][4][T::kRows];
+    __shared__ __align__(16) uint8_t s_stage[T::kWaves][stage_bytes(F32, kTN)];
+    const int thread = threadIdx.x, lane = thread & (kWaveLanes - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(thread / kWaveLanes);
+    const int wn = wave % WN, wm = wave / WN, g = lane >> 5;
+    const uint32_t code_stride = static_cast<uint32_t>(kp), scale_stride = static_cast<uint32_t>(stride);
+    const int steps = static_cast<int>(kp / 128);
+    const uint32_t total = tiles_n * tiles_m;
+
+    // The copies run two steps ahead of the products, through the tiles in
+    // turn: tile pt, step pk is copied next.  A wavefront copies rows of one
+    // matrix only, and thread t the scales of buffer row t: uniform bases, and
+    // 32-bit offsets of the lane, row x stride (24 bits each, kp being below
+    // 2^24).  Rows are clamped to the matrix: a row past the end repeats the
+    // last one, unstored.
+    uint32_t pt = blockIdx.x;
+    int pk = 0;
+    const bool copy_b = wave * (8 * T::kCopies) < BN, scale_b = wave * kWaveLanes < BN;
+    const uint8_t *copy_base = nullptr, *scale_base = nullptr;
+    uint32_t src[T::kCopies], scale_src = 0;
+    // slot s of row r holds chunk s ^ ((r / 2) & 7): for rows 0 to 7 of 16
+    // here, for rows 8 to 15 with bit 2 of the chunk turned
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;
+    auto aim = [&] {
+        uint32_t tile_n, tile_m;
+        tile_at(pt, tiles_n, tiles_m, tile_n, tile_m);
+        const int64_t n0 = static_cast<int64_t>(tile_n) * BN, m0 = static_cast<int64_t>(tile_m) * BM;
+        const int n_last = static_cast<int>(b.rows - n0 < BN ? b.rows - n0 : BN) - 1;
+        const int m_last = static_cast<int>(a.rows - m0 < BM ? a.rows - m0 : BM) - 1;
+        copy_base = copy_b ? b.codes + n0 * code_stride : a.codes + m0 * code_stride;
+        scale_base = scale_b ? b.scales + n0 * scale_stride : a.scales + m0 * scale_stride;
+        const int copy_last = copy_b ? n_last : m_last, scale_last = scale_b ? n_last : m_last;
+        const int first = wave * (8 * T::kCopies) - (copy_b ? 0 : BN) + (lane >> 3);
+#pragma unroll
+        for (int i = 0; i < T::kCopies; ++i) {
+            const int r = first + 8 * i;
+            src[i] = __umul24(r < copy_last ? r : copy_last, code_stride) + (chunk ^ ((i & 1) * 64u));
+        }
+        const int r = thread - (scale_b ? 0 : BN);
+        scale_src = __umul24(r < scale_last ? r : scale_last, scale_stride);
+    };
+    const uint32_t lds_to = lds_offset(s_buf) + wave * (T::kCopies * 1024);
+    auto copy = [&](int i, int buf) { load_to_lds(copy_base, src[i], lds_to + buf * T::kBytes + i * 1024); };
+
+    // Quarter q of a lane's row: its chunk 2 q + g; a product takes two.
+    const uint32_t off = (lane & 31) * 128 + ((g ^ ((lane >> 1) & 7)) << 4);
+    auto operand = [&](int buf, int half, int row) {
+        const uint8_t *p = &s_buf[buf][row * 128];
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(p + (off ^ (64 * half)));
+        const u32x4 y = *reinterpret_cast<const u32x4 *>(p + (off ^ (64 * half + 32)));
+        return i32x8{static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z), static_cast<int>(x.w),
+                     static_cast<int>(y.x), static_cast<int>(y.y), static_cast<int>(y.z), static_cast<int>(y.w)};
+    };
+    i32x8 vn[2][kTN], vm[T::kRing];
+    auto fetch_n = [&](int buf, int half, int i) { vn[half][i] = operand(buf, half, (wn * kTN + i) * 32); };
+    auto fetch_m = [&](int buf, int s) {
+        vm[s % T::kRing] = operand(buf, s / kTM, BN + (wm * kTM + s % kTM) * 32);
+    };
+
+    f32x16 acc[kTN][kTM];
+    uint32_t word_n[kTN], word_m[kTM];           // four steps' scales of a row
+
+    // After the copies of step pk: with the first of sixteen steps, their
+    // scales go to a register, and before the next barrier settle() moves them
+    // to LDS.  Past the last tile its last copies are repeated, unused.
+    u32x4 next_scales{0u, 0u, 0u, 0u};
+    bool pending = false;
+    int pset = 1, set = 0;       // sets of scales: the last one filled, the one in use
+    auto advance = [&] {
+        if (!(pk & 15)) {
+            pset ^= 1;
+            if (T::kRows == T::kTileThreads || thread < T::kRows)
+                next_scales = *reinterpret_cast<const u32x4 *>(scale_base + scale_src + pk);
+            pending = true;
+        }
+        copy_base += 128;
+        if (++pk == steps) {
+            if (pt + gridDim.x < total) {
+                pk = 0;
+                pt += gridDim.x;
+                aim();
+            } else {
+                --pk;
+                copy_base -= 128;
+            }
+        }
+    };
+    auto settle = [&] {
+        if (!pending) return;
+        if (T::kRows == T::kTileThreads || thread < T::kRows) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) s_scales[pset][w][thread] = next_scales[w];
+        }
+        pending = false;
+    };
+    auto fetch_scales = [&](int k) {
+        const uint32_t *from = s_scales[set][(k >> 2) & 3] + (lane & 31);
+#pragma unroll
+        for (int i = 0; i < kTN; ++i) word_n[i] = from[(wn * kTN + i) * 32];
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) word_m[i] = from[BN + (wm * kTM + i) * 32];
+    };
+
+    uint32_t t = blockIdx.x;
+    if (t >= total) return;
+    aim();
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) copy(i, 0);
+    advance();
+    __builtin_amdgcn_s_waitcnt(0);       // this wavefront's copies have reached LDS
+    settle();
+    __syncthreads();                     // everyone's have
+#pragma unroll
+    for (int i = 0; i < T::kCopies; ++i) copy(i, 1);
+    advance();
+#pragma unroll
+    for (int i = 0; i < kTN; ++i) fetch_n(0, 0, i);
+#pragma unroll
+    for (int s = 0; s < T::kAhead; ++s) fetch_m(0, s);
+    fetch_scales(0);
+    int buf = 0;
+    for (; t < total; t += gridDim.x) {
+#pragma unroll
+        for (int i = 0; i < kTN; ++i)
+#pragma unroll
+            for (int j = 0; j < kTM; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int k = 0; k < steps; ++k, buf ^= 1) {
+            const bool last = k == steps - 1;
+            uint32_t sn[kTN], sm[kTM];
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) sn[i] = word_n[i] >> (8 * (k & 3));
+#pragma unroll
+            for (int i = 0; i < kTM; ++i) sm[i] = word_m[i] >> (8 * (k & 3));
+            // Product x: A's operand s with B's block i.  Each is pinned in its
+            // place, with the reads of LDS and copies that go before it.
+            constexpr int kSwap = T::kSeq - T::kAhead;     // the operand before which the buffers change
+#pragma unroll
+            for (int x = 0; x < T::kSeq * kTN; ++x) {
+                const int s = x / kTN, i = x % kTN, half = s / kTM, j = s % kTM;
+                if (s < kSwap) {
+                    if (i == 0) fetch_m(buf, s + T::kAhead);
+                    // B's second half, as soon as that leaves room
+                    if (x < kTN) fetch_n(buf, 1, x);
+                }
+                if (x == kSwap * kTN) {
+                    __builtin_amdgcn_s_waitcnt(0);
+                    settle();
+                    __syncthreads();
+                    if ((k & 15) == 15 || last) set ^= 1;
+                    if ((k & 3) == 3 || last) fetch_scales(last ? 0 : k + 1);
+                }
+                if (s >= kSwap) {
+                    const int y = x - kSwap * kTN, left = (T::kSeq - kSwap) * kTN;
+                    // the next step's first operands: B's once the first half's
+                    // products are done, A's as the ring frees them
+                    const int z = x - (kSwap > kTM ? kSwap : kTM) * kTN;
+                    if (z >= 0 && z < kTN) fetch_n(buf ^ 1, 0, z);
+                    if (i == 0 && s > kSwap) fetch_m(buf ^ 1, s - kSwap - 1);
+                    const int per = (T::kCopies + left - 1) / left;
+#pragma unroll
+                    for (int c = y * per; c < (y + 1) * per && c < T::kCopies; ++c) copy(c, buf);
+                }
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    vn[half][i], vm[s % T::kRing], acc[i][j], kE4M3, FMT, 0, static_cast<int>(sn[i]), 0,
+                    static_cast<int>(sm[j]));
+                asm volatile("" : "+v"(acc[i][j]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            fetch_m(buf ^ 1, T::kAhead - 1);
+            advance();
+        }
+        uint32_t tile_n, tile_m;
+        tile_at(t, tiles_n, tiles_m, tile_n, tile_m);
+        store_blocks<F32, kTN, kTM>(acc, s_stage[wave], lane, static_cast<int64_t>(tile_m) * BM + wm * (kTM * 32),
+                                    static_cast<int64_t>(tile_n) * BN + wn * (kTN * 32), a.rows, b.rows, out,
+                                    row_bytes);
+    }
+    __builtin_amdgcn_s_waitcnt(0);       // no copy outlives the workgroup's LDS
+}
+
 // ------------------------------------------------------------- launching
 
 template <bool F32, int FMT, bool BLOCK, bool NORM>
@@ -451,11 +749,34 @@ hipError_t skinny(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64
     return hipGetLastError();
 }
 
+template <bool F32, int FMT, int BN, int BM, int WN, int WM>
+hipError_t tiles(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_t row_bytes, hipStream_t st)
+{
+    const uint32_t tn = static_cast<uint32_t>((b.rows + BN - 1) / BN);
+    const uint32_t tm = static_cast<uint32_t>((a.rows + BM - 1) / BM);
+    const uint64_t total = static_cast<uint64_t>(tn) * tm;
+    if (total > UINT32_MAX / 2) return hipErrorInvalidValue;
+    // as many workgroups as run at once (their LDS decides), each taking tiles
+    // in turn; a multiple of the 8 XCDs
+    constexpr unsigned kAtOnce = kCus * static_cast<unsigned>(160 * 1024 / Tile<BN, BM, WN, WM>::kLds(F32));
+    const unsigned grid = total < kAtOnce ? static_cast<unsigned>(total) : kAtOnce;
+    hipLaunchKernelGGL((fp8_tile_kernel<F32, FMT, BN, BM, WN, WM>), dim3(grid), dim3(WN * WM * kWaveLanes), 0, st, a,
+                       b, mx_padded(k), fp8_scale_stride(k), tn, tm, out, row_bytes);
+    return hipGetLastError();
+}
+
 template <bool F32, int FMT>
 hipError_t product_type(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_t row_bytes, hipStream_t st)
 {
     if (a.rows <= 16) return skinny<F32, FMT, 1, 1>(a, b, k, out, row_bytes, st);
-    return skinny<F32, FMT, 2, 4>(a, b, k, out, row_bytes, st);
+    const int64_t m32 = (a.rows + 31) / 32;
+    if (m32 * ((b.rows + 15) / 16) <= kCus) return skinny<F32, FMT, 2, 1>(a, b, k, out, row_bytes, st);
+    if (m32 * ((b.rows + 31) / 32) <= kCus) return skinny<F32, FMT, 2, 2>(a, b, k, out, row_bytes, st);
+    const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
+    const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
+    if (big >= 160) return tiles<F32, FMT, 256, 256, 4, 2>(a, b, k, out, row_bytes, st);
+    if (mid >= 160) return tiles<F32, FMT, 128, 128, 2, 2>(a, b, k, out, row_bytes, st);
+    return tiles<F32, FMT, 64, 64, 2, 2>(a, b, k, out, row_bytes, st);
 }
 
 }  // namespace

@@ -1,0 +1,27 @@
+"""The 8-bit tile kernels in the assembly of the built library: as for the
+MXFP4 ones, only their copies to LDS may use M0; and no accumulator leaves its
+registers for memory between the products."""
+import os
+import re
+
+import pytest
+
+from tests.test_mx_assembly import IMPLICIT, OBJDUMP, _kernels
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no llvm-objdump")
+def test_only_the_copies_use_m0(tmp_path):
+    kernels = _kernels(tmp_path, "fp8_tile_kernel")
+    assert len(kernels) >= 12                    # three tile shapes, two formats, two output types
+    for symbol, code in kernels.items():
+        copies = 0
+        for i, line in enumerate(code):
+            if line.startswith("global_load_lds_dwordx4 "):
+                assert code[i - 1] == "s_nop 0" and re.fullmatch(r"s_mov_b32 m0, s\d+", code[i - 2]), symbol
+                copies += 1
+            else:
+                assert not IMPLICIT.search(line), (symbol, line)
+        assert copies > 0 and sum("m0" in line for line in code) == copies, symbol
+        # the main loop: from the first product to the last, no scratch access
+        products = [i for i, line in enumerate(code) if line.startswith("v_mfma_scale_f32_32x32x64")]
+        assert not any("scratch" in line for line in code[products[0]:products[-1]]), symbol
