@@ -406,74 +406,9 @@ fp8_skinny_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restr
     }
 }
 
-// Accumulators of 32 x 32 blocks, TN along out's rows and TM of them, to out.
-// Block element e of a lane is m = lane % 32, n = 8 (e / 4) + 4 (lane / 32) + e
-// % 4: 16 bytes of a row at most, where a store of part of a line costs L2 as
-// much as one of a whole line.  Each wavefront turns a few rows at a time over
-// in LDS of its own and stores them in 16-byte pieces, whole lines of bf16; the
-// next tile's copies run meanwhile.
+// A wavefront's turned-over rows of out: so many at a time.
 __host__ __device__ constexpr int stage_rows(bool f32) { return f32 ? 8 : 16; }
 __host__ __device__ constexpr int stage_bytes(bool f32, int tn) { return stage_rows(f32) * tn * 32 * (f32 ? 4 : 2); }
-
-template <bool F32, int TN, int TM>
-__device__ __forceinline__ void store_blocks(const f32x16 (&acc)[TN][TM], uint8_t *stage, int lane, int64_t m_first,
-                                             int64_t n_first, int64_t rows, int64_t cols, uint8_t *out,
-                                             int64_t row_bytes)
-{
-    constexpr int kEsz = F32 ? 4 : 2, kPitch = TN * 32 * kEsz, kR = stage_rows(F32), kPieces = kPitch / 16;
-    const int g = lane >> 5;
-    // where piece c of row r lies in the row, so that 16 rows' pieces c fall on
-    // all banks
-    auto turned = [](int r, int c) { return (c ^ ((r * kPieces / 16) & (kPieces - 1))) * 16; };
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-#pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kR) {
-            if ((lane & (32 - kR)) == r0) {
-#pragma unroll
-                for (int i = 0; i < TN; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const f32x16 &x = acc[i][j];
-                        const int r = lane & (kR - 1), n = i * 32 + 2 * e + 4 * g;
-                        uint8_t *p = stage + r * kPitch + turned(r, n * kEsz / 16) + n * kEsz % 16;
-                        if constexpr (F32)
-                            *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
-                        else
-                            *reinterpret_cast<u32x2 *>(p) =
-                                u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
-                    }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int u0 = 0; u0 < kR * kPieces; u0 += kWaveLanes) {
-                const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
-                const int64_t m = m_first + j * 32 + r0 + r, n = n_first + c * (16 / kEsz);
-                if (u < kR * kPieces && m < rows && n < cols) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + turned(r, c));
-                    uint8_t *o = out + m * row_bytes + n * kEsz;
-                    // (nontemporal stores save 1-4% here and cost as much where
-                    // out is read next)
-                    if (n + 16 / kEsz <= cols) {
-                        *reinterpret_cast<u32x4_packed *>(o) = w;
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 16 / kEsz; ++x) {
-                            if (n + x >= cols) break;
-                            if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
-                            else
-                                reinterpret_cast<uint16_t *>(o)[x] =
-                                    static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
-                        }
-                    }
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-        }
-    }
-}
 
 // Larger products: a workgroup computes a BN x BM tile of out^T, its
 // wavefronts in a WN x WM arrangement of 32 x 32 accumulator blocks.
@@ -496,6 +431,16 @@ __device__ __forceinline__ void store_blocks(const f32x16 (&acc)[TN][TM], uint8_
 // Scales: each thread carries 16 bytes of one row, sixteen steps' worth, through
 // a register to LDS; a lane fetches a word, four steps' worth, of each of its
 // rows and shifts it by a byte a step.
+//
+// What bounds it: 8192^3 takes 408 us (2.7 PFLOP/s) with random operands, where
+// the bare instruction on registers reaches 4.05 (4.95 on zeros): the card's
+// power.  The matrix units are busy 71% of the cycles at a clock that is held
+// to 1.9 GHz; without the copies, or without the reads of LDS, a copy of the
+// kernel keeps the same cycles' share at 2.0 and 2.3 GHz.  Two groups of
+// wavefronts in turn, one reading while the other multiplies, are busy 79% at
+// 1.78 GHz and 3% faster on 8192^3, 5% slower over short K; four wavefronts of
+// 128 x 128, a third fewer reads, 5% faster on 8192^3 and as much slower on
+// 8192 x 14336 x 4096.
 template <int BN, int BM, int WN, int WM>
 struct Tile {
     static constexpr int kWaves = WN * WM;
@@ -652,11 +597,6 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
         for (int k = 0; k < steps; ++k, buf ^= 1) {
             const bool last = k == steps - 1;
-            uint32_t sn[kTN], sm[kTM];
-#pragma unroll
-            for (int i = 0; i < kTN; ++i) sn[i] = word_n[i] >> (8 * (k & 3));
-#pragma unroll
-            for (int i = 0; i < kTM; ++i) sm[i] = word_m[i] >> (8 * (k & 3));
             // Product x: A's operand s with B's block i.  Each is pinned in its
             // place, with the reads of LDS and copies that go before it.
             constexpr int kSwap = T::kSeq - T::kAhead;     // the operand before which the buffers change
@@ -673,7 +613,6 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
                     settle();
                     __syncthreads();
                     if ((k & 15) == 15 || last) set ^= 1;
-                    if ((k & 3) == 3 || last) fetch_scales(last ? 0 : k + 1);
                 }
                 if (s >= kSwap) {
                     const int y = x - kSwap * kTN, left = (T::kSeq - kSwap) * kTN;
@@ -687,19 +626,84 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
                     for (int c = y * per; c < (y + 1) * per && c < T::kCopies; ++c) copy(c, buf);
                 }
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    vn[half][i], vm[s % T::kRing], acc[i][j], kE4M3, FMT, 0, static_cast<int>(sn[i]), 0,
-                    static_cast<int>(sm[j]));
+                    vn[half][i], vm[s % T::kRing], acc[i][j], kE4M3, FMT, 0, static_cast<int>(word_n[i]), 0,
+                    static_cast<int>(word_m[j]));
                 asm volatile("" : "+v"(acc[i][j]));
                 __builtin_amdgcn_sched_barrier(0);
+            }
+            if ((k & 3) == 3 || last) {
+                fetch_scales(last ? 0 : k + 1);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTN; ++i) word_n[i] >>= 8;
+#pragma unroll
+                for (int i = 0; i < kTM; ++i) word_m[i] >>= 8;
             }
             fetch_m(buf ^ 1, T::kAhead - 1);
             advance();
         }
+        // Block element e of a lane is m = lane % 32, n = 8 (e / 4) +
+        // 4 (lane / 32) + e % 4: 16 bytes of a row at most, where a store of
+        // part of a line costs L2 as much as one of a whole line.  Each
+        // wavefront turns a few rows at a time over in LDS of its own and
+        // stores them in 16-byte pieces, whole lines of bf16; the next tile's
+        // copies run meanwhile.  (As a function of its own this takes 1-2%
+        // more of the whole kernel's time.)
+        constexpr int kEsz = F32 ? 4 : 2, kPitch = kTN * 32 * kEsz, kR = stage_rows(F32), kPieces = kPitch / 16;
         uint32_t tile_n, tile_m;
         tile_at(t, tiles_n, tiles_m, tile_n, tile_m);
-        store_blocks<F32, kTN, kTM>(acc, s_stage[wave], lane, static_cast<int64_t>(tile_m) * BM + wm * (kTM * 32),
-                                    static_cast<int64_t>(tile_n) * BN + wn * (kTN * 32), a.rows, b.rows, out,
-                                    row_bytes);
+        const int64_t m_first = static_cast<int64_t>(tile_m) * BM + wm * (kTM * 32);
+        const int64_t n_first = static_cast<int64_t>(tile_n) * BN + wn * (kTN * 32);
+        uint8_t *stage = s_stage[wave];
+        // where piece c of row r lies in the row, so that 16 rows' pieces c
+        // fall on all banks
+        auto turned = [](int r, int c) { return (c ^ ((r * kPieces / 16) & (kPieces - 1))) * 16; };
+#pragma unroll
+        for (int j = 0; j < kTM; ++j) {
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += kR) {
+                if ((lane & (32 - kR)) == r0) {
+#pragma unroll
+                    for (int i = 0; i < kTN; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const f32x16 &x = acc[i][j];
+                            const int r = lane & (kR - 1), n = i * 32 + 2 * e + 4 * g;
+                            uint8_t *p = stage + r * kPitch + turned(r, n * kEsz / 16) + n * kEsz % 16;
+                            if constexpr (F32)
+                                *reinterpret_cast<f32x4 *>(p) = f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+                            else
+                                *reinterpret_cast<u32x2 *>(p) =
+                                    u32x2{bf16_pair(x[e], x[e + 1]), bf16_pair(x[e + 2], x[e + 3])};
+                        }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int u0 = 0; u0 < kR * kPieces; u0 += kWaveLanes) {
+                    const int u = u0 + lane, r = u / kPieces, c = u % kPieces;
+                    const int64_t m = m_first + j * 32 + r0 + r, n = n_first + c * (16 / kEsz);
+                    if (u < kR * kPieces && m < a.rows && n < b.rows) {
+                        const u32x4 w = *reinterpret_cast<const u32x4 *>(stage + r * kPitch + turned(r, c));
+                        uint8_t *o = out + m * row_bytes + n * kEsz;
+                        if (n + 16 / kEsz <= b.rows) {
+                            *reinterpret_cast<u32x4_packed *>(o) = w;
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 16 / kEsz; ++x) {
+                                if (n + x >= b.rows) break;
+                                if constexpr (F32) reinterpret_cast<uint32_t *>(o)[x] = w[x];
+                                else
+                                    reinterpret_cast<uint16_t *>(o)[x] =
+                                        static_cast<uint16_t>(w[x / 2] >> (16 * (x & 1)));
+                            }
+                        }
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
     }
     __builtin_amdgcn_s_waitcnt(0);       // no copy outlives the workgroup's LDS
 }
