@@ -1319,6 +1319,9 @@ flashopt_status flashopt_byte_linear(const void *x, int x_fp32, int64_t m, int64
     uint8_t *codes = static_cast<uint8_t *>(workspace);
     uint8_t *scales = codes + flashopt_byte_code_bytes(m, k);
     hipStream_t st = static_cast<hipStream_t>(stream);
+    if (flashopt::fp8_linear_direct(in))
+        return hip_status(flashopt::launch_fp8_linear_direct(in, static_cast<const uint8_t *>(w_codes),
+                                                             static_cast<const uint8_t *>(w_scales), o, st));
     if (k > 0) {
         const Fp8Out q{codes, scales, nullptr, nullptr};
         const hipError_t e = flashopt::launch_fp8_quantize(in, FLASHOPT_E4M3, false, q, st);

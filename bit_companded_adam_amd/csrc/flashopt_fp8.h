@@ -11,6 +11,8 @@
 #ifndef FLASHOPT_FP8_H
 #define FLASHOPT_FP8_H
 
+#include <type_traits>
+
 #include "flashopt_device.h"
 
 namespace flashopt {
@@ -189,6 +191,21 @@ __device__ __forceinline__ uint32_t across16(uint32_t x, F &&combine)
     x = combine(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
     const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
     return combine(static_cast<uint32_t>(b[0]), static_cast<uint32_t>(b[1]));
+}
+
+// Sum over a wavefront, known to all of its lanes.
+__device__ __forceinline__ float wave_sum(float x)
+{
+    auto turned = [](float v, auto by) {
+        return __uint_as_float(rotated<decltype(by)::value>(__float_as_uint(v)));
+    };
+    x += turned(x, std::integral_constant<int, 1>{});
+    x += turned(x, std::integral_constant<int, 2>{});
+    x += turned(x, std::integral_constant<int, 4>{});
+    x += turned(x, std::integral_constant<int, 8>{});
+    return __uint_as_float(across16(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 
 }  // namespace

@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "flashopt.h"
 #include "flashopt_fp8.h"
 #include "flashopt_internal.h"
@@ -270,6 +272,24 @@ __device__ __forceinline__ float scale_value(uint32_t b)
     return __uint_as_float(b == kNanByte ? 0x7FC00000u : b << 23);
 }
 
+// The four values of a word of codes.
+template <int FMT>
+__device__ __forceinline__ void values4(uint32_t w, float (&v)[4])
+{
+    f32x2 lo, hi;
+    if constexpr (FMT == kE5M2) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, 1.0f, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, 1.0f, true);
+    } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, 1.0f, true);
+    }
+    v[0] = lo.x;
+    v[1] = lo.y;
+    v[2] = hi.x;
+    v[3] = hi.y;
+}
+
 // One thread per eight columns.
 template <bool F32, int FMT>
 __global__ void __launch_bounds__(kThreads)
@@ -286,18 +306,10 @@ fp8_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restri
         float v[8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            f32x2 lo, hi;
-            if constexpr (FMT == kE5M2) {
-                lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w[k], 1.0f, false);
-                hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w[k], 1.0f, true);
-            } else {
-                lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[k], 1.0f, false);
-                hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[k], 1.0f, true);
-            }
-            v[4 * k] = lo.x * s;
-            v[4 * k + 1] = lo.y * s;
-            v[4 * k + 2] = hi.x * s;
-            v[4 * k + 3] = hi.y * s;
+            float four[4];
+            values4<FMT>(w[k], four);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * k + e] = four[e] * s;
         }
         store8<F32>(out + r * row_bytes + c * (F32 ? 4 : 2), rounded8<F32>(v), cols - c);
     }
@@ -322,85 +334,281 @@ __device__ __forceinline__ f32x4 mfma16(i32x8 b, i32x8 a, f32x4 c, uint32_t sb, 
                                                             static_cast<int>(sa));
 }
 
-__device__ __forceinline__ i32x8 load32(const uint8_t *p)
+// One row of A: a plain sum of products, without the matrix instructions, so
+// that a wavefront reads 1024 consecutive bytes of a row of B at a time, sixteen
+// to a lane.  A workgroup takes two rows of B, its wavefronts take such pieces
+// in turn and add their sums in order.  A lane's sixteen products are added in
+// fp32 unscaled and then scaled by both scales' exponents together.
+//
+// Bound by memory: with the weight in cache / with weights in turn that no cache
+// holds 14336 x 4096 takes 11.6 / 12.4 us (59 MB: 5.1 / 4.7 TB/s), 4096 x 14336
+// 11.5 / 13.2, 4096 x 4096 4.8 / 5.6, 28672 x 8192 34.6 / 43.3.  (As a tile of 16
+// rows of A by fp8_few_kernel: 12.4 / 17.3, 11.6 / 13.4, 5.3 / 7.0, 37 / 47; with
+// one row to a wavefront, four or eight, or fewer wavefronts to a row, up to 20%
+// slower.  Two rows of A are level with the tile.)
+constexpr int kVectorRows = 2, kVectorWaves = kThreads / kWaveLanes;
+
+// A as it is stored, or a row of bf16 that each workgroup quantizes for itself
+// (as fp8_rows_kernel does, bit for bit): that saves a launch before this one.
+template <int FMT>
+struct StoredRow {
+    static constexpr int kFormat = FMT;
+    const uint8_t *codes, *scales;
+    __device__ __forceinline__ u32x4 load(uint32_t at, bool there, uint32_t group, uint32_t &byte) const
+    {
+        byte = 0u;
+        if (!there) return u32x4{0u, 0u, 0u, 0u};
+        byte = scales[group];
+        return *reinterpret_cast<const u32x4 *>(codes + at);
+    }
+};
+struct RawRow {
+    static constexpr int kFormat = kE4M3;
+    const uint8_t *data;
+    int64_t cols;
+    __device__ __forceinline__ u32x4 load(uint32_t at, bool, uint32_t, uint32_t &byte) const
+    {
+        const uint8_t *p = data + at * 2u;
+        const int count = static_cast<int>(cols) - static_cast<int>(at);
+        const Eight<false> lo = load8<false, false>(p, count), hi = load8<false, false>(p + 16, count - 8);
+        Eight<false> top{};
+        raise(top, lo);
+        raise(top, hi);
+        uint32_t t = largest(top);               // over the eight lanes of a group
+        t = umax32(t, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(t), 0xB1, 0xF, 0xF, true)));
+        t = umax32(t, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(t), 0x4E, 0xF, 0xF, true)));
+        t = umax32(t, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(t), 0x141, 0xF, 0xF, true)));
+        const uint32_t scale = fp8_scale<kE4M3>(t);
+        const u32x2 a = row_codes<false, kE4M3>(lo, scale), b = row_codes<false, kE4M3>(hi, scale);
+        byte = t >= kInfinite ? kNanByte : scale >> 23;
+        return t >= kInfinite ? u32x4{0u, 0u, 0u, 0u} : u32x4{a.x, a.y, b.x, b.y};
+    }
+};
+
+template <typename A>
+__global__ void __launch_bounds__(kThreads)
+fp8_vector_kernel(A a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restrict__ out, bool out_fp32)
 {
-    const u32x4 a = *reinterpret_cast<const u32x4 *>(p), b = *reinterpret_cast<const u32x4 *>(p + 16);
-    return i32x8{static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
-                 static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+    constexpr int R = kVectorRows;
+    __shared__ float s_sum[2][kVectorWaves][R];
+    const int lane = threadIdx.x & (kWaveLanes - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
+    const int pieces = static_cast<int>((kp + 1023) / 1024), last = static_cast<int>(b.rows) - 1;
+    const uint32_t groups = (static_cast<uint32_t>(b.rows) + R - 1) / R;
+    int turn = 0;
+    for (uint32_t group = blockIdx.x; group < groups; group += gridDim.x, turn ^= 1) {
+        const uint8_t *codes[R], *scales[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = static_cast<int>(group * R) + r < last ? static_cast<int>(group * R) + r : last;
+            codes[r] = b.codes + row * kp;
+            scales[r] = b.scales + row * stride;
+        }
+        float acc[R] = {};
+        // (unrolled twice, 30% slower where a wavefront has one piece)
+#pragma unroll 1
+        for (int c = wave; c < pieces; c += kVectorWaves) {
+            const uint32_t at = static_cast<uint32_t>(c) * 1024u + lane * 16u, of = at / 128u;
+            const bool there = at < static_cast<uint32_t>(kp);
+            u32x4 wb[R];
+            uint32_t eb[R], ea;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                wb[r] = u32x4{0u, 0u, 0u, 0u};
+                eb[r] = 0u;
+                if (there) {
+                    wb[r] = *reinterpret_cast<const u32x4 *>(codes[r] + at);
+                    eb[r] = scales[r][of];
+                }
+            }
+            const u32x4 wa = a.load(at, there, of, ea);
+            float part[R] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float va[4], vb[4];
+                values4<A::kFormat>(wa[q], va);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    values4<kE4M3>(wb[r][q], vb);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part[r] = __builtin_fmaf(va[i], vb[i], part[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                acc[r] += ea == kNanByte || eb[r] == kNanByte
+                              ? __uint_as_float(0x7FC00000u)
+                              : __builtin_amdgcn_ldexpf(part[r], static_cast<int>(ea + eb[r]) - 254);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float x = wave_sum(acc[r]);
+            if (lane == 0) s_sum[turn][wave][r] = x;
+        }
+        __syncthreads();
+        const uint32_t n = group * R + threadIdx.x;
+        if (threadIdx.x < R && n <= static_cast<uint32_t>(last)) {
+            float x = s_sum[turn][0][threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < kVectorWaves; ++w) x += s_sum[turn][w][threadIdx.x];
+            if (out_fp32) reinterpret_cast<float *>(out)[n] = x;
+            else reinterpret_cast<uint16_t *>(out)[n] = bf16_rne(x);
+        }
+    }
 }
 
-// Few rows of A: the time is B's, read once, so nothing is staged.  A workgroup
-// takes 16 NT rows of B and 16 MT of A; its wavefronts take groups of 128
-// elements of K in turn and add their sums at the end, in wavefront order.
-// Within a step a lane holds 32 consecutive bytes of its row; any assignment of
-// them to the instruction's K slots is the same sum, the scale being the
-// row's for the whole step.
-constexpr int kSkinnyWaves = 8;
+// Few rows of A, or few tiles: a workgroup takes 16 NT rows of B and 16 MT of A;
+// its wavefronts take steps of 128 elements of K, four in succession, and add
+// their sums at the end, in wavefront order.  Each copies its own steps to LDS
+// of its own by the DMA, up to three ahead, and waits for nobody.  Scales go to
+// LDS 128 steps at a time.  LDS holds rows as the tiles below do.
+//
+// What bounds it is how much a CU has under way: 48 x 4096 x 14336 takes 14.3 us
+// with the weight in cache and 19.6 with weights in turn that no cache holds
+// (59 MB: 4.1 and 3.0 TB/s), 16 x 14336 x 4096 12.4 and 17.3, 256 x 4096 x 14336
+// 25.6 and 34.5.  (Loaded by the lanes that use them, operands take sixteen
+// rows' half lines an instruction, where the copies take eight rows' whole
+// ones, and the first of these 34 us, or 30 with four steps' loads at once.)
+constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWaveLanes;
 
-template <bool F32, int FMT, int MT, int NT>
-__global__ void __launch_bounds__(kSkinnyWaves *kWaveLanes)
-fp8_skinny_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restrict__ out, int64_t row_bytes)
+template <int MT, int NT>
+struct Few {
+    static constexpr int kRows = 16 * (MT + NT), kBytes = kRows * 128, kCopies = kRows / 8;
+    static constexpr int kStages = kFewWaves * kBytes * 4 <= 144 * 1024 - kRows * 144 ? 4 : 2;
+    static constexpr int kBlock = 128, kPitch = 144;       // steps whose scales LDS holds, and bytes of a row of them
+};
+
+template <int N>
+__device__ __forceinline__ void wait_vm()
 {
-    __shared__ f32x4 s_acc[kSkinnyWaves][NT][MT][kWaveLanes];
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+template <int FMT, int MT, int NT>
+__global__ void __launch_bounds__(kFewThreads)
+fp8_few_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restrict__ out, bool out_fp32,
+               int64_t row_bytes)
+{
+    using T = Few<MT, NT>;
+    constexpr int kWaves = kFewWaves, kStages = T::kStages;
+    __shared__ __align__(128) uint8_t s_buf[kWaves][kStages][T::kBytes];
+    __shared__ __align__(16) uint8_t s_scales[T::kRows][T::kPitch];
     const int lane = threadIdx.x & (kWaveLanes - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes);
     const int l16 = lane & 15, g = lane >> 4;
     const int64_t tiles_n = (b.rows + 16 * NT - 1) / (16 * NT), tiles_m = (a.rows + 16 * MT - 1) / (16 * MT);
-    const int steps = static_cast<int>(kp / 128);
+    const int all_steps = static_cast<int>(kp / 128);
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;   // of rows 0 to 7 of 16: bit 2 turned for the others
+    const uint32_t lds_to = lds_offset(s_buf[wave]);
     for (int64_t tile = blockIdx.x; tile < tiles_n * tiles_m; tile += gridDim.x) {
         const int64_t n0 = tile % tiles_n * (16 * NT), m0 = tile / tiles_n * (16 * MT);
-        const uint8_t *bp[NT], *bs[NT], *ap[MT], *as[MT];
+        const int n_last = static_cast<int>(b.rows - n0 < 16 * NT ? b.rows - n0 : 16 * NT) - 1;
+        const int m_last = static_cast<int>(a.rows - m0 < 16 * MT ? a.rows - m0 : 16 * MT) - 1;
+        // rows of B, then of A; past the end the last one again, unstored
+        uint32_t src[T::kCopies];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            int64_t r = n0 + 16 * t + l16;
-            if (r >= b.rows) r = b.rows - 1;     // read, never stored
-            bp[t] = b.codes + r * kp + g * 32;
-            bs[t] = b.scales + r * stride;
+        for (int i = 0; i < T::kCopies; ++i) {
+            const int r = (i < 2 * NT ? i : i - 2 * NT) * 8 + (lane >> 3), last = i < 2 * NT ? n_last : m_last;
+            src[i] = __umul24(r < last ? r : last, static_cast<uint32_t>(kp)) + (chunk ^ ((i & 1) * 64u));
         }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            int64_t r = m0 + 16 * t + l16;
-            if (r >= a.rows) r = a.rows - 1;
-            ap[t] = a.codes + r * kp + g * 32;
-            as[t] = a.scales + r * stride;
-        }
+        const uint8_t *b_codes = b.codes + n0 * kp, *a_codes = a.codes + m0 * kp;
         f32x4 acc[NT][MT];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = wave; k < steps; k += kSkinnyWaves) {
-            i32x8 vb[NT], va[MT];
-            uint32_t sb[NT], sa[MT];
+        for (int first = 0; first < all_steps; first += T::kBlock) {
+            const int count = all_steps - first < T::kBlock ? all_steps - first : T::kBlock;
+            // this wavefront's steps t = 0, 1, ...: fours of them in turn with the other wavefronts'
+            const int fours = (count + 3) / 4, mine = (fours - wave + kWaves - 1) / kWaves;
+            const int tail = mine > 0 && ((mine - 1) * kWaves + wave) * 4 + 4 > count ? 4 - (count & 3) : 0;
+            const int steps = 4 * mine - tail;
+            auto issue = [&](int t, int stage) {
+                const int64_t at = static_cast<int64_t>(first + ((t >> 2) * kWaves + wave) * 4 + (t & 3)) * 128;
+                const uint32_t to = lds_to + stage * T::kBytes;
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                vb[i] = load32(bp[i] + static_cast<int64_t>(k) * 128);
-                sb[i] = bs[i][k];
+                for (int i = 0; i < T::kCopies; ++i)
+                    load_to_lds((i < 2 * NT ? b_codes : a_codes) + at, src[i], to + i * 1024);
+            };
+#pragma unroll
+            for (int t = 0; t < kStages - 1; ++t)
+                if (t < steps) issue(t, t);
+            for (int u = threadIdx.x; u < T::kRows * 8; u += kFewThreads) {
+                const int r = u >> 3, at = first + (u & 7) * 16;
+                const bool of_b = r < 16 * NT;
+                const int row = of_b ? r : r - 16 * NT, last = of_b ? n_last : m_last;
+                const uint8_t *p = (of_b ? b.scales + n0 * stride : a.scales + m0 * stride) +
+                                   static_cast<int64_t>(row < last ? row : last) * stride;
+                if (at < stride)
+                    *reinterpret_cast<u32x4 *>(&s_scales[r][(u & 7) * 16]) = *reinterpret_cast<const u32x4 *>(p + at);
             }
+            __syncthreads();
+            for (int q = 0; q < mine; ++q) {
+                uint32_t sb[NT], sa[MT];
+                const int word = (q * kWaves + wave) * 4;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                va[j] = load32(ap[j] + static_cast<int64_t>(k) * 128);
-                sa[j] = as[j][k];
+                for (int i = 0; i < NT; ++i) sb[i] = *reinterpret_cast<const uint32_t *>(&s_scales[16 * i + l16][word]);
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    sa[j] = *reinterpret_cast<const uint32_t *>(&s_scales[16 * (NT + j) + l16][word]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int t = 4 * q + u, left = steps - 1 - t;
+                    if (left < 0) break;
+                    // the last step's reads are done: its buffer is the next copy's
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    if (left >= kStages - 1) {
+                        issue(t + kStages - 1, (u + kStages - 1) % kStages);
+                        wait_vm<(kStages - 1) * T::kCopies>();
+                    } else if (left == 2) {
+                        wait_vm<(kStages > 2 ? 2 : 0) * T::kCopies>();
+                    } else if (left == 1) {
+                        wait_vm<(kStages > 2 ? 1 : 0) * T::kCopies>();
+                    } else {
+                        wait_vm<0>();
+                    }
+                    const uint8_t *buf = s_buf[wave][u % kStages];
+                    auto operand = [&](int tile16) {
+                        const uint8_t *row = buf + tile16 * 2048 + l16 * 128;
+                        const uint32_t x = (g ^ ((l16 >> 1) & 7)) * 16;
+                        const u32x4 lo = *reinterpret_cast<const u32x4 *>(row + x);
+                        const u32x4 hi = *reinterpret_cast<const u32x4 *>(row + (x ^ 64));
+                        return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z),
+                                     static_cast<int>(lo.w), static_cast<int>(hi.x), static_cast<int>(hi.y),
+                                     static_cast<int>(hi.z), static_cast<int>(hi.w)};
+                    };
+                    i32x8 vb[NT], va[MT];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) vb[i] = operand(i);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) va[j] = operand(NT + j);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int j = 0; j < MT; ++j)
+                            acc[i][j] = mfma16<FMT>(vb[i], va[j], acc[i][j], sb[i] >> (8 * u), sa[j] >> (8 * u));
+                }
             }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < MT; ++j) acc[i][j] = mfma16<FMT>(vb[i], va[j], acc[i][j], sb[i], sa[j]);
+            __syncthreads();                     // every wavefront's reads of the scales and its copies are done
         }
+        f32x4(*s_acc)[NT][MT][kWaveLanes] = reinterpret_cast<f32x4(*)[NT][MT][kWaveLanes]>(&s_buf[0][0][0]);
+        static_assert(kWaves * NT * MT * kWaveLanes * 16 <= kWaves * kStages * T::kBytes, "sums");
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < MT; ++j) s_acc[wave][i][j][lane] = acc[i][j];
         __syncthreads();
-        for (int i = wave; i < NT * MT; i += kSkinnyWaves) {
+        for (int i = wave; i < NT * MT; i += kWaves) {
             f32x4 v = s_acc[0][i / MT][i % MT][lane];
 #pragma unroll
-            for (int w = 1; w < kSkinnyWaves; ++w) {
+            for (int w = 1; w < kWaves; ++w) {
                 const f32x4 u = s_acc[w][i / MT][i % MT][lane];
                 v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
             }
             const int64_t m = m0 + 16 * (i % MT) + l16, n = n0 + 16 * (i / MT) + 4 * g;
-            if (m < a.rows) store4<F32>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
+            if (m >= a.rows) continue;
+            if (out_fp32) store4<true>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
+            else store4<false>(out, row_bytes, m, n, b.rows, v.x, v.y, v.z, v.w);
         }
         __syncthreads();
     }
@@ -743,13 +951,28 @@ hipError_t quantize_type(const MxMatrix &x, bool block, const Fp8Out &q, hipStre
     return hipGetLastError();
 }
 
-template <bool F32, int FMT, int MT, int NT>
-hipError_t skinny(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_t row_bytes, hipStream_t st)
+template <typename A>
+hipError_t vector(const A &a, const Fp8In &b, int64_t k, uint8_t *out, bool out_fp32, hipStream_t st)
 {
-    const int64_t tiles = ((b.rows + 16 * NT - 1) / (16 * NT)) * ((a.rows + 16 * MT - 1) / (16 * MT));
+    const int64_t groups = (b.rows + kVectorRows - 1) / kVectorRows;
+    hipLaunchKernelGGL((fp8_vector_kernel<A>), dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : (1 << 20))),
+                       dim3(kThreads), 0, st, a, b, mx_padded(k), fp8_scale_stride(k), out, out_fp32);
+    return hipGetLastError();
+}
+
+int64_t few_tiles(const Fp8In &a, const Fp8In &b, int mt, int nt)
+{
+    return ((a.rows + 16 * mt - 1) / (16 * mt)) * ((b.rows + 16 * nt - 1) / (16 * nt));
+}
+
+template <int FMT, int MT, int NT>
+hipError_t few(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, bool out_fp32, int64_t row_bytes,
+               hipStream_t st)
+{
+    const int64_t tiles = few_tiles(a, b, MT, NT);
     const unsigned grid = static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20));
-    hipLaunchKernelGGL((fp8_skinny_kernel<F32, FMT, MT, NT>), dim3(grid), dim3(kSkinnyWaves * kWaveLanes), 0, st, a,
-                       b, mx_padded(k), fp8_scale_stride(k), out, row_bytes);
+    hipLaunchKernelGGL((fp8_few_kernel<FMT, MT, NT>), dim3(grid), dim3(kFewThreads), 0, st, a, b, mx_padded(k),
+                       fp8_scale_stride(k), out, out_fp32, row_bytes);
     return hipGetLastError();
 }
 
@@ -769,18 +992,54 @@ hipError_t tiles(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_
     return hipGetLastError();
 }
 
-template <bool F32, int FMT>
-hipError_t product_type(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_t row_bytes, hipStream_t st)
+// Elements of K from which 64 x 64 tiles, one or less to a CU, go to
+// fp8_few_kernel, whose wavefronts split K, instead of fp8_tile_kernel.  M x N x
+// K in us, there / here: 1024 x 1000 x 1000 6.0 / 7.1, 200 x 4096 x 2048 7.9 /
+// 7.7, 512 x 2048 x 2048 8.0 / 7.8, 256 x 4096 x 4096 12.3 / 11.0, 256 x 4096 x
+// 14336 54.7 / 25.6.
+constexpr int64_t kFewInner = 2048;
+
+template <int FMT>
+hipError_t product_format(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, bool out_fp32, int64_t row_bytes,
+                          hipStream_t st)
 {
-    if (a.rows <= 16) return skinny<F32, FMT, 1, 1>(a, b, k, out, row_bytes, st);
-    const int64_t m32 = (a.rows + 31) / 32;
-    if (m32 * ((b.rows + 15) / 16) <= kCus) return skinny<F32, FMT, 2, 1>(a, b, k, out, row_bytes, st);
-    if (m32 * ((b.rows + 31) / 32) <= kCus) return skinny<F32, FMT, 2, 2>(a, b, k, out, row_bytes, st);
+    if (a.rows == 1) return vector(StoredRow<FMT>{a.codes, a.scales}, b, k, out, out_fp32, st);
+    // The smallest tiles of which a CU gets one at most: a larger one reads A and
+    // B less often, a smaller one leaves fewer CUs idle.  M x N x K in us, tiles
+    // of 16 MT x 16 NT: 48 x 4096 x 14336 2 x 2 (256 tiles) 14.3, 3 x 2 17.1, 2 x 4
+    // 18.1, 2 x 1 22.4; 48 x 14336 x 4096 3 x 4 (224) 14.1, 3 x 2 16.2, 2 x 2 25.2;
+    // 24 x 6144 x 4096 2 x 2 (192) 7.8, 2 x 1 11.0; 64 x 2048 x 5632 2 x 1 (256)
+    // 6.2, 2 x 2 6.6, 4 x 1 7.3; 128 x 4096 x 14336 4 x 2 (256) 19.9, 4 x 4 24.6, 2
+    // x 2 27.1.
+    const int64_t m16 = (a.rows + 15) / 16;
+    auto fits = [&](int mt, int nt) { return mt <= m16 && few_tiles(a, b, mt, nt) <= kCus; };
+    if (fits(1, 1)) return few<FMT, 1, 1>(a, b, k, out, out_fp32, row_bytes, st);
+    if (fits(2, 1)) return few<FMT, 2, 1>(a, b, k, out, out_fp32, row_bytes, st);
+    if (m16 == 1 && fits(1, 2)) return few<FMT, 1, 2>(a, b, k, out, out_fp32, row_bytes, st);
+    if (fits(2, 2)) return few<FMT, 2, 2>(a, b, k, out, out_fp32, row_bytes, st);
+    // One tile of A's rows, and B of more rows than that: 16 x 14336 x 4096 1 x 4
+    // (224) 12.4, 1 x 1 14.0; 16 x 28672 x 8192 1 x 4 (448) 39.5, 1 x 1 (several to a
+    // CU at once) 38.4, from memory 59.7 and 54.0; 32 x 28672 x 8192 2 x 4 40.3, 2 x 1
+    // 54.1; 64 x 14336 x 4096 4 x 4 15.0, 64 x 64 tiles below 19.0.
+    if (m16 == 1)
+        return fits(1, 4) ? few<FMT, 1, 4>(a, b, k, out, out_fp32, row_bytes, st)
+                          : few<FMT, 1, 1>(a, b, k, out, out_fp32, row_bytes, st);
+    if (m16 == 3 && fits(3, 2)) return few<FMT, 3, 2>(a, b, k, out, out_fp32, row_bytes, st);
+    if (m16 == 2) return few<FMT, 2, 4>(a, b, k, out, out_fp32, row_bytes, st);
+    if (fits(4, 2)) return few<FMT, 4, 2>(a, b, k, out, out_fp32, row_bytes, st);
+    if (m16 == 3) return few<FMT, 3, 4>(a, b, k, out, out_fp32, row_bytes, st);
+    if (m16 == 4 || (fits(4, 4) && k >= kFewInner)) return few<FMT, 4, 4>(a, b, k, out, out_fp32, row_bytes, st);
+    // The largest tile of which there are enough for the 256 CUs, as above.  M x N
+    // x K in us, tiles of 256 / 128: BIGMID; of 128 / 64: MIDSMALL.
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
-    if (big >= 160) return tiles<F32, FMT, 256, 256, 4, 2>(a, b, k, out, row_bytes, st);
-    if (mid >= 160) return tiles<F32, FMT, 128, 128, 2, 2>(a, b, k, out, row_bytes, st);
-    return tiles<F32, FMT, 64, 64, 2, 2>(a, b, k, out, row_bytes, st);
+    auto in_tiles = [&](auto fp32) {
+        constexpr bool F32 = decltype(fp32)::value;
+        if (big >= 160) return tiles<F32, FMT, 256, 256, 4, 2>(a, b, k, out, row_bytes, st);
+        if (mid >= 160) return tiles<F32, FMT, 128, 128, 2, 2>(a, b, k, out, row_bytes, st);
+        return tiles<F32, FMT, 64, 64, 2, 2>(a, b, k, out, row_bytes, st);
+    };
+    return out_fp32 ? in_tiles(std::true_type{}) : in_tiles(std::false_type{});
 }
 
 }  // namespace
@@ -832,11 +1091,17 @@ hipError_t launch_fp8_product(const uint8_t *a_codes, const uint8_t *a_scales, i
         else hipLaunchKernelGGL(zero_kernel<false>, grid, dim3(kThreads), 0, st, out.rows, out.cols, p, row_bytes);
         return hipGetLastError();
     }
-    if (a_format == kE5M2)
-        return out.fp32 ? product_type<true, kE5M2>(a, b, inner, p, row_bytes, st)
-                        : product_type<false, kE5M2>(a, b, inner, p, row_bytes, st);
-    return out.fp32 ? product_type<true, kE4M3>(a, b, inner, p, row_bytes, st)
-                    : product_type<false, kE4M3>(a, b, inner, p, row_bytes, st);
+    return a_format == kE5M2 ? product_format<kE5M2>(a, b, inner, p, out.fp32, row_bytes, st)
+                             : product_format<kE4M3>(a, b, inner, p, out.fp32, row_bytes, st);
+}
+
+bool fp8_linear_direct(const MxMatrix &x) { return x.rows == 1 && !x.fp32 && x.cols > 0; }
+
+hipError_t launch_fp8_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
+                                    const MxMatrix &out, hipStream_t st)
+{
+    return vector(RawRow{static_cast<const uint8_t *>(x.data), x.cols}, Fp8In{w_codes, w_scales, out.cols}, x.cols,
+                  static_cast<uint8_t *>(out.data), out.fp32, st);
 }
 
 }  // namespace flashopt

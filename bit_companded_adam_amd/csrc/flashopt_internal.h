@@ -219,6 +219,12 @@ hipError_t launch_fp8_dequantize(const uint8_t *codes, const uint8_t *scales, in
 hipError_t launch_fp8_product(const uint8_t *a_codes, const uint8_t *a_scales, int a_format, const uint8_t *b_codes,
                               const uint8_t *b_scales, int64_t inner, const MxMatrix &out, hipStream_t stream);
 
+// x w^T in one launch, x quantized inside it: whether x (one row of bf16) allows
+// it, and the launch.
+bool fp8_linear_direct(const MxMatrix &x);
+hipError_t launch_fp8_linear_direct(const MxMatrix &x, const uint8_t *w_codes, const uint8_t *w_scales,
+                                    const MxMatrix &out, hipStream_t stream);
+
 // x, residual, h and y are of one size and type; what is not wanted is nullptr.
 struct NormCall {
     MxMatrix x, residual, h, y;

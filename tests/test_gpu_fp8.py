@@ -247,7 +247,16 @@ PRODUCTS = [(1, 1, 1), (1, 16, 128), (1, 17, 129), (3, 100, 1000), (15, 33, 255)
             (64, 2049, 500), (128, 2048, 700), (129, 2048, 700), (8192, 16, 300), (8193, 16, 300),
             # scales past the first sixteen of a row, every kind of end
             (300, 1100, 1920), (300, 1100, 2048), (300, 1101, 2176), (299, 1100, 2200), (300, 1100, 4096),
-            (300, 1100, 4224), (130, 5000, 12300), (1024, 1024, 6200), (2100, 2100, 2300), (4000, 3800, 4200)]
+            (300, 1100, 4224), (130, 5000, 12300), (1024, 1024, 6200), (2100, 2100, 2300), (4000, 3800, 4200),
+            # one row: pieces of 1024, shares of a few steps, more rows of B than one grid takes
+            (1, 300, 1), (1, 301, 1023), (1, 1, 1024), (1, 33, 1025), (1, 100, 4096), (1, 50, 5000), (1, 2200001, 128),
+            # few rows or tiles, each shape: ends of the fours of steps that a wavefront takes, of the 128 whose
+            # scales are held, and shares that are left without any
+            (2, 40, 128), (2, 40, 256), (3, 40, 384), (5, 40, 512), (16, 40, 640), (9, 700, 2048), (2, 30, 2176),
+            (7, 30, 16384), (7, 33, 16385), (16, 17, 16512), (11, 40, 33000), (20, 4096, 300), (33, 4096, 1000),
+            (33, 4097, 900), (16, 6000, 500), (15, 14336, 400), (2, 20000, 200), (40, 5000, 700), (48, 9000, 260),
+            (64, 9000, 260), (30, 9000, 260), (128, 4096, 520), (129, 4096, 520), (250, 4000, 2048), (250, 4000, 2047),
+            (64, 20000, 130), (33, 17000, 130)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
