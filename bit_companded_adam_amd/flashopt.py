@@ -16,6 +16,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 from array import array
 
@@ -200,8 +201,9 @@ def lib() -> ctypes.CDLL:
         L.flashopt_byte_dequantize.argtypes = [vp, vp, i, i64, i64, vp, i, i64, vp]
         L.flashopt_byte_product.argtypes = [vp, vp, i, vp, vp, i64, i64, i64, vp, i, i64, vp]
         L.flashopt_byte_linear.argtypes = [vp, i, i64, i64, i64, vp, vp, i64, vp, i, i64, vp, ctypes.c_size_t, vp]
-        L.flashopt_rms_norm.argtypes = [ctypes.POINTER(flashopt_norm_args), vp]
-        L.flashopt_rms_norm_backward.argtypes = [ctypes.POINTER(flashopt_norm_grad_args), vp]
+        # the structures by reference, or packed in bytes
+        L.flashopt_rms_norm.argtypes = [vp, vp]
+        L.flashopt_rms_norm_backward.argtypes = [vp, vp]
         L.flashopt_status_str.argtypes = [i]
         L.flashopt_status_str.restype = ctypes.c_char_p
         L.flashopt_abi_version.argtypes = []
@@ -232,7 +234,7 @@ def _check(status: int, where: str):
 
 def _stream(stream) -> int:
     if stream is None:      # torch.cuda.current_stream().cuda_stream, without the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -585,7 +587,7 @@ def _on(device, stream):
     """Allocations, torch operations and launches inside go to `device` and
     `stream` (None: the device's current stream)."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     elif stream.device != device:
@@ -1284,7 +1286,8 @@ class MXWeight:
 
 
 def _flat(x: torch.Tensor) -> torch.Tensor:
-    x = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
+    if x.dim() != 2:
+        x = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
     return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
 
 
@@ -1424,8 +1427,8 @@ class FP8Tensor:
     @staticmethod
     def empty(rows: int, cols: int, device, dtype=torch.float8_e4m3fn) -> "FP8Tensor":
         """Uninitialized, codes and then scales in one buffer."""
-        buffer = torch.empty(rows * sum(_fp8_widths(cols)), dtype=torch.uint8, device=device)
-        return FP8Tensor._over(buffer, rows, cols, dtype)
+        nbytes = rows * (FP8_BLOCK * ((cols + FP8_BLOCK - 1) // FP8_BLOCK) + 16 * ((cols + 2047) // 2048))
+        return FP8Tensor._over(torch.empty(nbytes, dtype=torch.uint8, device=device), rows, cols, dtype)
 
     @staticmethod
     def _over(buffer: torch.Tensor, rows: int, cols: int, dtype) -> "FP8Tensor":
@@ -1433,7 +1436,7 @@ class FP8Tensor:
         q.rows, q.cols, q.device, q._buffer, q._codes, q._scales = rows, cols, buffer.device, buffer, None, None
         q.dtype, q.format = dtype, FORMATS[dtype]
         q.code_ptr = buffer.data_ptr()
-        q.scale_ptr = q.code_ptr + rows * _fp8_widths(cols)[0]
+        q.scale_ptr = q.code_ptr + rows * FP8_BLOCK * ((cols + FP8_BLOCK - 1) // FP8_BLOCK)
         q.replayed = False
         return q
 
@@ -1482,8 +1485,19 @@ def _fp8_targets(out, layout, rows, cols, device, dtype):
     first, second = out if layout == "both" and out is not None else (out, out)
     q = None if layout == "cols" else _fp8_target(first, rows, cols, device, dtype)
     t = None if layout == "rows" else _fp8_target(second, cols, rows, device, dtype)
-    pointers = [p for one in (q, t) for p in ((one.code_ptr, one.scale_ptr) if one else (None, None))]
+    pointers = [p for one in (q, t) for p in ((one.code_ptr, one.scale_ptr) if one else (0, 0))]
     return q, t, *pointers
+
+
+def _target(out, rows, cols, dtype, device):
+    """(out, address, fp32 flag, row stride) of a matrix to write, made unless
+    given."""
+    if out is None and (dtype == torch.bfloat16 or dtype == torch.float32):
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        return out, out.data_ptr(), 1 if dtype == torch.float32 else 0, cols
+    out = _out_matrix(out, rows, cols, dtype, device)
+    ptr, wide, _, _, stride = _matrix(out, "out")
+    return out, ptr, wide, stride
 
 
 def flashopt_byte_quantize(x: torch.Tensor, layout: str = "rows", block: bool = False, dtype=torch.float8_e4m3fn,
@@ -1507,10 +1521,9 @@ def flashopt_byte_quantize(x: torch.Tensor, layout: str = "rows", block: bool = 
 def flashopt_byte_dequantize(q: FP8Tensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an FP8Tensor."""
     with _on(q.device, stream):
-        out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
-        ptr, wide, rows, cols, stride = _matrix(out, "out")
-        status = lib().flashopt_byte_dequantize(q.code_ptr, q.scale_ptr, q.format, rows, cols, ptr, wide, stride,
-                                               _stream(None))
+        out, ptr, wide, stride = _target(out, q.rows, q.cols, dtype, q.device)
+        status = lib().flashopt_byte_dequantize(q.code_ptr, q.scale_ptr, q.format, q.rows, q.cols, ptr, wide, stride,
+                                                _stream(None))
     _check(status, "flashopt_byte_dequantize")
     return out
 
@@ -1525,10 +1538,9 @@ def flashopt_byte_product(a: FP8Tensor, b: FP8Tensor, dtype=torch.bfloat16, out=
     dev = a.device
     _same_device(dev, b, "b")
     with _on(dev, stream):
-        out = _out_matrix(out, a.rows, b.rows, dtype, dev)
-        ptr, wide, m, n, stride = _matrix(out, "out")
-        status = lib().flashopt_byte_product(a.code_ptr, a.scale_ptr, a.format, b.code_ptr, b.scale_ptr, m, n, a.cols,
-                                            ptr, wide, stride, _stream(None))
+        out, ptr, wide, stride = _target(out, a.rows, b.rows, dtype, dev)
+        status = lib().flashopt_byte_product(a.code_ptr, a.scale_ptr, a.format, b.code_ptr, b.scale_ptr, a.rows, b.rows,
+                                             a.cols, ptr, wide, stride, _stream(None))
     _check(status, "flashopt_byte_product")
     return out
 
@@ -1549,15 +1561,16 @@ def flashopt_byte_linear(x: torch.Tensor, w: FP8Tensor, dtype=None, out=None, wo
     dev = x.device
     _same_device(dev, w, "w")
     with _on(dev, stream):
-        out = _out_matrix(out, m, w.rows, dtype or x.dtype, dev)
-        optr, owide, _, n, ostride = _matrix(out, "out")
+        out, optr, owide, ostride = _target(out, m, w.rows, dtype or x.dtype, dev)
         if workspace is None:
-            workspace = torch.empty(m * sum(_fp8_widths(k)), dtype=torch.uint8, device=dev)
+            nbytes = m * sum(_fp8_widths(k))
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            wptr = workspace.data_ptr()
         else:
             _same_device(dev, workspace, "workspace")
-        status = lib().flashopt_byte_linear(ptr, wide, m, k, stride, w.code_ptr, w.scale_ptr, n, optr, owide, ostride,
-                                           _dev(workspace, "workspace"),
-                                           workspace.numel() * workspace.element_size(), _stream(None))
+            wptr, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        status = lib().flashopt_byte_linear(ptr, wide, m, k, stride, w.code_ptr, w.scale_ptr, w.rows, optr, owide,
+                                            ostride, wptr, nbytes, _stream(None))
     _check(status, "flashopt_byte_linear")
     return out
 
@@ -1606,25 +1619,37 @@ def fp8_linear(x: torch.Tensor, weight, grad_dtype=torch.float8_e4m3fn) -> torch
 
 # --------------------------------------------------------------- norm
 
-def _vector(t: torch.Tensor, name: str, cols: int, device):
-    """(address, fp32 flag) of a contiguous bf16 or fp32 vector."""
+# The arguments' structures packed in one step (flashopt_norm_args and
+# flashopt_norm_grad_args, NULL as 0): a third of the time of a ctypes one.
+_NORM_ARGS = struct.Struct("10P6qd4i")
+_NORM_GRAD_ARGS = struct.Struct("8PN6q2i")
+
+
+def _vector(t: torch.Tensor, name: str, cols: int, device) -> int:
+    """The fp32 flag of a contiguous bf16 or fp32 vector."""
     if t.dtype != torch.bfloat16 and t.dtype != torch.float32:
         raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != cols:
         raise ValueError(f"{name} must be a vector of {cols}, got {tuple(t.shape)}")
-    _same_device(device, t, name)
-    return _dev(t, name), int(t.dtype == torch.float32)
+    if t.device != device:
+        _same_device(device, t, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return 1 if t.dtype == torch.float32 else 0
 
 
-def _alike(t: torch.Tensor, name: str, x: torch.Tensor):
-    """(address, row stride) of a matrix of x's size, type and device."""
+def _alike(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
+    """The row stride of a matrix of x's size, type and device."""
     if t.shape != x.shape:
         raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(t.shape)}")
     if t.dtype != x.dtype:
         raise ValueError(f"{name} must be {x.dtype}, got {t.dtype}")
-    ptr, _, _, _, stride = _matrix(t, name)
-    _same_device(x.device, t, name)
-    return ptr, stride
+    if t.device != x.device:
+        _same_device(x.device, t, name)
+    stride, inner = t.stride()
+    if inner != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return stride if t.shape[0] > 1 else t.shape[1]
 
 
 def flashopt_rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: float = 1e-6, output: str = "values",
@@ -1636,31 +1661,40 @@ def flashopt_rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: f
     which may be x or residual itself; rstd: an fp32 tensor for the rows' 1 / root,
     which flashopt_rms_norm_backward takes."""
     xp, wide, rows, cols, stride = _matrix(x, "x")
-    if output not in ("values", "rows", "cols", "both"):
+    dev = x.device
+    fmt = FORMATS.get(dtype)
+    if fmt is None or output not in ("values", "rows", "cols", "both"):
+        _format(dtype)
         raise ValueError("output must be 'values', 'rows', 'cols' or 'both'")
-    fmt, dev = _format(dtype), x.device
-    gp, gwide = _vector(gain, "gain", cols, dev)
-    rp, rstride = (None, 0) if residual is None else _alike(residual, "residual", x)
+    gwide = _vector(gain, "gain", cols, dev)
+    rstride = 0 if residual is None else _alike(residual, "residual", x)
     if h is not None and residual is None:
         raise ValueError("without a residual there is no sum to write to h")
     with _on(dev, stream):
-        hp, hstride, yp, ystride, q, t, c, sc, ct, sct = None, 0, None, 0, None, None, None, None, None, None
+        hp = hstride = yp = ystride = c = sc = ct = sct = 0
         if residual is not None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=dev) if h is None else h
-            hp, hstride = _alike(h, "h", x)
+            if h is None:
+                h, hstride = x.new_empty((rows, cols)), cols
+            else:
+                hstride = _alike(h, "h", x)
+            hp = h.data_ptr()
         if output == "values":
-            out = torch.empty((rows, cols), dtype=x.dtype, device=dev) if out is None else out
-            yp, ystride = _alike(out, "out", x)
+            if out is None:
+                out, ystride = x.new_empty((rows, cols)), cols
+            else:
+                ystride = _alike(out, "out", x)
+            yp = out.data_ptr()
         else:
             q, t, c, sc, ct, sct = _fp8_targets(out, output, rows, cols, dev, dtype)
             out = (q, t) if output == "both" else (q or t)
-        if rstd is None and t is not None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        args = flashopt_norm_args(xp, rp, gp, hp, yp, c, sc, ct, sct,
-                                  None if rstd is None else _buf(rstd, "rstd", dev, (4,), rows, float32=True),
-                                  rows, cols, stride, rstride, hstride, ystride, eps, wide, gwide, fmt, 0)
-        status = lib().flashopt_rms_norm(ctypes.byref(args), _stream(None))
-    _check(status, "flashopt_rms_norm")
+            if rstd is None and t is not None:
+                rstd = x.new_empty(rows, dtype=torch.float32)
+        status = lib().flashopt_rms_norm(
+            _NORM_ARGS.pack(xp, 0 if residual is None else residual.data_ptr(), gain.data_ptr(), hp, yp, c, sc, ct,
+                            sct, 0 if rstd is None else _buf(rstd, "rstd", dev, (4,), rows, float32=True), rows, cols,
+                            stride, rstride, hstride, ystride, eps, wide, gwide, fmt, 0), _stream(None))
+    if status:
+        _check(status, "flashopt_rms_norm")
     return out, x if residual is None else h
 
 
@@ -1676,30 +1710,36 @@ def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Te
     None for one that is not needed.  dx may be dy or dh itself."""
     hp, wide, rows, cols, hstride = _matrix(h, "h")
     dev = h.device
-    gp, gwide = _vector(gain, "gain", cols, dev)
-    yp, ystride = _alike(dy, "dy", h)
-    ep, estride = (None, 0) if dh is None else _alike(dh, "dh", h)
+    gwide = _vector(gain, "gain", cols, dev)
+    ystride, estride = _alike(dy, "dy", h), 0 if dh is None else _alike(dh, "dh", h)
     sp = _buf(rstd, "rstd", dev, (4,), rows, float32=True)
     with _on(dev, stream):
-        xp, xstride, dp, nbytes = None, 0, None, 0
+        xp = xstride = dp = wp = nbytes = 0
         if need_dx:
-            dx = torch.empty((rows, cols), dtype=h.dtype, device=dev) if dx is None else dx
-            xp, xstride = _alike(dx, "dx", h)
+            if dx is None:
+                dx, xstride = h.new_empty((rows, cols)), cols
+            else:
+                xstride = _alike(dx, "dx", h)
+            xp = dx.data_ptr()
         if need_dgain:
-            dgain = torch.empty(cols, dtype=gain.dtype, device=dev) if dgain is None else dgain
-            dp, dwide = _vector(dgain, "dgain", cols, dev)
-            if dwide != gwide:
+            if dgain is None:
+                dgain = gain.new_empty(cols)
+            elif _vector(dgain, "dgain", cols, dev) != gwide:
                 raise ValueError(f"dgain must be {gain.dtype}, got {dgain.dtype}")
+            dp = dgain.data_ptr()
             if workspace is None:
-                workspace = torch.empty(flashopt_rms_norm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
-                                        device=dev)
-            _same_device(dev, workspace, "workspace")
-            nbytes = workspace.numel() * workspace.element_size()
-        args = flashopt_norm_grad_args(yp, ep, hp, gp, sp, xp, dp,
-                                       _dev(workspace, "workspace") if need_dgain else None, nbytes, rows, cols,
-                                       ystride, estride, hstride, xstride, wide, gwide)
-        status = lib().flashopt_rms_norm_backward(ctypes.byref(args), _stream(None))
-    _check(status, "flashopt_rms_norm_backward")
+                nbytes = flashopt_rms_norm_backward_workspace_bytes(rows, cols)
+                workspace = h.new_empty(nbytes, dtype=torch.uint8)
+                wp = workspace.data_ptr()
+            else:
+                _same_device(dev, workspace, "workspace")
+                wp, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        status = lib().flashopt_rms_norm_backward(
+            _NORM_GRAD_ARGS.pack(dy.data_ptr(), 0 if dh is None else dh.data_ptr(), hp, gain.data_ptr(), sp, xp, dp,
+                                 wp, nbytes, rows, cols, ystride, estride, hstride, xstride, wide, gwide),
+            _stream(None))
+    if status:
+        _check(status, "flashopt_rms_norm_backward")
     return dx if need_dx else None, dgain if need_dgain else None
 
 
@@ -1711,14 +1751,18 @@ def _norm_operands(x, gain, residual):
                          f"{residual.dtype}")
 
 
-def _norm_backward(ctx, dy, dh, h, gain, rstd, need_dx, need_gain):
-    """(dx in x's shape, dgain) from the gradients of the norm's outputs, either
+def _as(t, shape):
+    return t if t.dim() == len(shape) else t.view(shape)
+
+
+def _norm_backward(dy, dh, h, gain, rstd, need_dx, need_gain):
+    """(dx in h's shape, dgain) from the gradients of the norm's outputs, either
     of which may be missing."""
     if dy is None:
         return dh if need_dx else None, None
     dx, dgain = flashopt_rms_norm_backward(dy, _flat(h), gain, rstd, None if dh is None else _flat(dh), need_dx,
                                            need_gain)
-    return None if dx is None else dx.view(ctx.x_shape), dgain
+    return None if dx is None else _as(dx, h.shape), dgain
 
 
 class _RMSNorm(torch.autograd.Function):
@@ -1726,24 +1770,23 @@ class _RMSNorm(torch.autograd.Function):
     def forward(ctx, x, gain, residual, eps):
         ctx.set_materialize_grads(False)
         flat = _flat(x)
-        rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        rstd = flat.new_empty(flat.shape[0], dtype=torch.float32)
         y, h = flashopt_rms_norm(flat, gain, None if residual is None else _flat(residual), eps, rstd=rstd)
-        ctx.x_shape = x.shape
-        y = y.view(x.shape)
+        y = _as(y, x.shape)
         if residual is None:
             ctx.save_for_backward(x, gain, rstd)
             return y
-        h = h.view(x.shape)
+        h = _as(h, x.shape)
         ctx.save_for_backward(h, gain, rstd)
         return y, h
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dh=None):
-        need_x, need_gain, need_residual = ctx.needs_input_grad[:3]
+        need_x, need_gain, need_residual, _ = ctx.needs_input_grad
         h, gain, rstd = ctx.saved_tensors
-        dx, dgain = _norm_backward(ctx, None if dy is None else _flat(dy), dh, h, gain, rstd,
-                                   need_x or need_residual, need_gain)
+        dx, dgain = _norm_backward(None if dy is None else _flat(dy), dh, h, gain, rstd, need_x or need_residual,
+                                   need_gain)
         return dx if need_x else None, dgain, dx if need_residual else None, None
 
 
@@ -1767,17 +1810,18 @@ class _FP8NormLinear(torch.autograd.Function):
         need_dy = need_x or need_gain or need_residual
         w_rows, w_cols, weight = _weight_copies(kind, w, weight, need_dy)
         flat = _flat(x)
-        rstd = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        rstd = flat.new_empty(flat.shape[0], dtype=torch.float32)
         q, h = flashopt_rms_norm(flat, gain, None if residual is None else _flat(residual), eps,
                                  "both" if need_w else "rows", rstd=rstd)
         rows, cols = q if need_w else (q, None)
         ctx.kind, ctx.weight, ctx.version = kind, weight, None if weight is None else weight.version
-        ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, w.dtype
-        h = x if residual is None else h.view(x.shape)
+        ctx.x_dtype, ctx.w_dtype = x.dtype, w.dtype
+        h = x if residual is None else _as(h, x.shape)
         kept = (cols, w_cols if need_dy else None)
         ctx.kept = [None if t is None else t._size() for t in kept]
         ctx.save_for_backward(h, gain, rstd, *[t._buffer for t in kept if t is not None])
-        y = kind.product(rows, w_rows, x.dtype).view(*x.shape[:-1], w.shape[0])
+        y = kind.product(rows, w_rows, x.dtype)
+        y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
         return y if residual is None else (y, h)
 
     @staticmethod
@@ -1789,18 +1833,19 @@ class _FP8NormLinear(torch.autograd.Function):
         cols, w_cols = [None if k is None else kind.tensor._over(saved.pop(0), *k) for k in ctx.kept]
         dn = dw = None
         if dy is not None:
-            layouts = [name for name, need in (("rows", need_dx or need_gain), ("cols", need_w)) if need]
-            if layouts[0] == "rows":
+            need_rows = need_dx or need_gain
+            if need_rows:
                 _check_fresh(ctx, kind)
-            layout = "both" if len(layouts) == 2 else layouts[0]
+            layout = "both" if need_rows and need_w else "rows" if need_rows else "cols"
             q = kind.quantize(_flat(dy), layout, grad=True)
             dy_rows, dy_cols = q if layout == "both" else (q, q)
-            if "rows" in layouts:
+            if need_rows:
                 dn = kind.product(dy_rows, w_cols, ctx.x_dtype)
-            if "cols" in layouts:
+            if need_w:
                 dw = kind.product(dy_cols, cols, ctx.w_dtype)
-        dx, dgain = (None, None) if not need_dx and not need_gain else _norm_backward(
-            ctx, dn, dh, h, gain, rstd, need_dx, need_gain)
+        dx = dgain = None
+        if need_dx or need_gain:
+            dx, dgain = _norm_backward(dn, dh, h, gain, rstd, need_dx, need_gain)
         return dx if need_x else None, dgain, dw, dx if need_residual else None, None, None, None, None
 
 
