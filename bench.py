@@ -19,7 +19,7 @@ codec ablation), --fp32-states (quantize_states=False), --optimizer sgd (the
 FlashSGD step: lr 1e-2, momentum 0.9, weight decay 0.01), --grad-release (one
 single-tensor launch per tensor, the gradient-release launch pattern).
 --codec times the codec and split entry points instead, --ops the gradient
-norm, clipping and MXFP4 entry points (one JSON line each).
+norm, clipping, MXFP4, 8-bit and row norm entry points (one JSON line each).
 
 Prints one JSON line: Gparam/s over the K timed steps, the roofline of the
 step kernel (algorithmic bytes per param of the configuration against
@@ -53,6 +53,7 @@ from bit_companded_adam_amd import workloads as W  # noqa: E402
 
 METRIC = "FlashAdamW step Gparam/s and % of HBM roofline (12.25 B/param), 1 GPU"
 PEAK_FP4_TFLOPS = 10066.0   # MI355X, dense
+PEAK_FP8_TFLOPS = 5033.0
 PEAK_HBM_GBS = 8000.0
 KERNEL_SRC = os.path.join(ROOT, "bit_companded_adam_amd", "csrc", "flashopt_kernels.hip")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "adamw_step_8b_traffic.json")
@@ -542,8 +543,8 @@ def bench_codec(n: int, reps: int, warmup: int):
 
 def bench_ops(workload: str, reps: int, warmup: int):
     """Times the gradient norm, clipping and the scaled step over a workload's
-    list, and the MXFP4 entry points at the 8.0B list's layer sizes (one JSON
-    line each).  Rates count each input read once and each output written
+    list, and the MXFP4, 8-bit and row norm entry points at the 8.0B list's
+    layer sizes (one JSON line each).  Rates count each input read once and each output written
     once; clipping reads and writes every gradient."""
     shapes = WORKLOADS[workload]()
     sizes = [W.numel(s) for _, s in shapes]
@@ -566,7 +567,14 @@ def bench_ops(workload: str, reps: int, warmup: int):
     w = F.flashopt_mx_quantize(torch.randn((f, k), generator=g, device="cuda").bfloat16() * 0.02)
     y = torch.empty((m, f), dtype=torch.bfloat16, device="cuda")
     rows, both = F.flashopt_mx_quantize(x), F.flashopt_mx_quantize(x, "both")
-    mx = 17 / 32                     # bytes of an MXFP4 element
+    mx, b8 = 17 / 32, 129 / 128      # bytes of an MXFP4 and of an 8-bit element
+    wide = torch.randn((f, k), generator=g, device="cuda").bfloat16() * 0.02
+    w8 = F.FP8Weight(wide)
+    rows8, both8 = F.flashopt_byte_quantize(x), F.flashopt_byte_quantize(x, "both")
+    gain = torch.ones(k, device="cuda")
+    h, dy, dx = (torch.randn((m, k), generator=g, device="cuda").bfloat16() for _ in range(3))
+    normed, rstd, dgain = torch.empty_like(x), torch.ones(m, device="cuda"), torch.empty_like(gain)
+    work = torch.empty(F.flashopt_rms_norm_backward_workspace_bytes(m, k), dtype=torch.uint8, device="cuda")
     cases = [
         ("flashopt_grad_norm", workload, 2 * n, 0, lambda: plan.norm(1.0, out=out)),
         ("flashopt_grad_clip", workload, 4 * n, 0, clip),
@@ -582,6 +590,23 @@ def bench_ops(workload: str, reps: int, warmup: int):
          lambda: F.flashopt_mx_product(rows, w, out=y)),
         ("flashopt_mx_linear", f"1 x {f} x {k}", 2 * k + mx * f * k + 2 * f, 2 * f * k,
          lambda: F.flashopt_mx_linear(x[:1], w, out=y[:1])),
+        ("flashopt_byte_quantize, rows", f"{m} x {k} bf16", (2 + b8) * m * k, 0,
+         lambda: F.flashopt_byte_quantize(x, out=rows8)),
+        ("flashopt_byte_quantize, both", f"{m} x {k} bf16", (2 + 2 * b8) * m * k, 0,
+         lambda: F.flashopt_byte_quantize(x, "both", out=both8)),
+        ("flashopt_byte_quantize, both, blocks", f"{f} x {k} bf16", (2 + 2 * b8) * f * k, 0, w8.refresh),
+        ("flashopt_byte_dequantize", f"{m} x {k} bf16", (2 + b8) * m * k, 0,
+         lambda: F.flashopt_byte_dequantize(rows8, out=normed)),
+        ("flashopt_byte_product", f"{m} x {f} x {k}", b8 * (m + f) * k + 2 * m * f, 2 * m * f * k,
+         lambda: F.flashopt_byte_product(rows8, w8.rows, out=y)),
+        ("flashopt_byte_linear", f"1 x {f} x {k}", 2 * k + b8 * f * k + 2 * f, 2 * f * k,
+         lambda: F.flashopt_byte_linear(x[:1], w8.rows, out=y[:1])),
+        ("flashopt_rms_norm", f"{m} x {k} bf16, residual", 8 * m * k, 0,
+         lambda: F.flashopt_rms_norm(x, gain, dy, out=normed, h=h, rstd=rstd)),
+        ("flashopt_rms_norm, rows in 8 bits", f"{m} x {k} bf16, residual", (6 + b8) * m * k, 0,
+         lambda: F.flashopt_rms_norm(x, gain, dy, output="rows", out=rows8, h=h, rstd=rstd)),
+        ("flashopt_rms_norm_backward", f"{m} x {k} bf16, dh", 8 * m * k, 0,
+         lambda: F.flashopt_rms_norm_backward(dy, h, gain, rstd, dh=x, dx=dx, dgain=dgain, workspace=work)),
     ]
     for op, size, nbytes, flops, fn in cases:
         for _ in range(warmup):
@@ -597,8 +622,9 @@ def bench_ops(workload: str, reps: int, warmup: int):
         ms = float(np.median([a.elapsed_time(b) for a, b in ev]))
         gbs, tflops = nbytes / (ms * 1e-3) / 1e9, flops / (ms * 1e-3) / 1e12
         # the bound whose peak rate takes longer
-        matrix = flops / PEAK_FP4_TFLOPS / 1e12 > nbytes / PEAK_HBM_GBS / 1e9
-        value, unit, peak = (tflops, "TFLOP/s", PEAK_FP4_TFLOPS) if matrix else (gbs, "GB/s", PEAK_HBM_GBS)
+        rate = PEAK_FP8_TFLOPS if op.startswith("flashopt_byte") else PEAK_FP4_TFLOPS
+        matrix = flops / rate / 1e12 > nbytes / PEAK_HBM_GBS / 1e9
+        value, unit, peak = (tflops, "TFLOP/s", rate) if matrix else (gbs, "GB/s", PEAK_HBM_GBS)
         line = {"metric": f"{op} ({size}) {unit}, 1 GPU", "value": value, "unit": unit, "n_gpus": 1,
                 "steps": reps, "warmup": warmup, "ms_per_step": ms, "higher_is_better": True,
                 "vs_baseline": None, "data": "synthetic", "config": {"op": op, "size": size},
@@ -654,7 +680,7 @@ def main():
     ap.add_argument("--codec-elems", type=int, default=1 << 29)
     ap.add_argument("--ops", action="store_true",
                     help="instead of the step, time the gradient norm, clipping, the scaled step and "
-                         "the MXFP4 entry points (one JSON line each)")
+                         "the MXFP4, 8-bit and row norm entry points (one JSON line each)")
     args = ap.parse_args()
 
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) != 1:
