@@ -1179,9 +1179,16 @@ def _out_matrix(out, rows, cols, dtype, device):
     return out
 
 
+def _quantized(kind, q, name: str):
+    """A matrix of another layout has too few bytes for the calls of this one."""
+    if not isinstance(q, kind):
+        raise ValueError(f"{name} must be an {kind.__name__}, got {type(q).__name__}")
+
+
 def _mx_target(q, rows, cols, device):
     if q is None:
         return MXTensor.empty(rows, cols, device)
+    _quantized(MXTensor, q, "out")
     if (q.rows, q.cols) != (rows, cols):
         raise ValueError(f"out is {q.rows} x {q.cols}, {rows} x {cols} needed")
     _same_device(device, q, "out")
@@ -1213,6 +1220,7 @@ def flashopt_mx_quantize(x: torch.Tensor, layout: str = "rows", out=None, stream
 
 def flashopt_mx_dequantize(q: MXTensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an MXTensor."""
+    _quantized(MXTensor, q, "q")
     with _on(q.device, stream):
         out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
         ptr, wide, rows, cols, stride = _matrix(out, "out")
@@ -1224,6 +1232,8 @@ def flashopt_mx_dequantize(q: MXTensor, dtype=torch.float32, out=None, stream=No
 
 def flashopt_mx_product(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """a b^T of two MXTensors with the same number of columns, in bf16 or fp32."""
+    _quantized(MXTensor, a, "a")
+    _quantized(MXTensor, b, "b")
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     dev = a.device
@@ -1245,6 +1255,7 @@ def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, works
     """x w^T of a bf16 or fp32 matrix, quantized on the way, and MXFP4 weights
     (no gradients: mx_linear has them); in x's dtype unless given.  out must
     not share elements with x."""
+    _quantized(MXTensor, w, "w")
     ptr, wide, m, k, stride = _matrix(x, "x")
     if k != w.cols:
         raise ValueError(f"x has {k} columns, w {w.cols}")
@@ -1364,6 +1375,8 @@ class _Linear(torch.autograd.Function):
 def _operands(x, weight, held_type):
     """(weight parameter, its holder or None) of a linear layer's call."""
     w, held = (weight.param, weight) if isinstance(weight, held_type) else (weight, None)
+    if not isinstance(w, torch.Tensor):
+        raise ValueError(f"weight must be a tensor or an {held_type.__name__}, got {type(w).__name__}")
     if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1]:
         raise ValueError(f"x {tuple(x.shape)} and weight {tuple(w.shape)} do not match")
     return w, held
@@ -1472,6 +1485,7 @@ def _format(dtype) -> int:
 def _fp8_target(q, rows, cols, device, dtype):
     if q is None:
         return FP8Tensor.empty(rows, cols, device, dtype)
+    _quantized(FP8Tensor, q, "out")
     if (q.rows, q.cols, q.dtype) != (rows, cols, dtype):
         raise ValueError(f"out is {q.rows} x {q.cols} of {q.dtype}, {rows} x {cols} of {dtype} needed")
     _same_device(device, q, "out")
@@ -1520,6 +1534,7 @@ def flashopt_byte_quantize(x: torch.Tensor, layout: str = "rows", block: bool = 
 
 def flashopt_byte_dequantize(q: FP8Tensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an FP8Tensor."""
+    _quantized(FP8Tensor, q, "q")
     with _on(q.device, stream):
         out, ptr, wide, stride = _target(out, q.rows, q.cols, dtype, q.device)
         status = lib().flashopt_byte_dequantize(q.code_ptr, q.scale_ptr, q.format, q.rows, q.cols, ptr, wide, stride,
@@ -1531,6 +1546,8 @@ def flashopt_byte_dequantize(q: FP8Tensor, dtype=torch.float32, out=None, stream
 def flashopt_byte_product(a: FP8Tensor, b: FP8Tensor, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """a b^T of two FP8Tensors with the same number of columns, b in E4M3, in
     bf16 or fp32."""
+    _quantized(FP8Tensor, a, "a")
+    _quantized(FP8Tensor, b, "b")
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     if b.format != 0:
@@ -1553,6 +1570,7 @@ def flashopt_byte_linear(x: torch.Tensor, w: FP8Tensor, dtype=None, out=None, wo
     """x w^T of a bf16 or fp32 matrix, quantized to E4M3 on the way, and 8-bit
     weights (no gradients: fp8_linear has them); in x's dtype unless given.  out
     must not share elements with x."""
+    _quantized(FP8Tensor, w, "w")
     ptr, wide, m, k, stride = _matrix(x, "x")
     if k != w.cols:
         raise ValueError(f"x has {k} columns, w {w.cols}")
@@ -1623,6 +1641,7 @@ def fp8_linear(x: torch.Tensor, weight, grad_dtype=torch.float8_e4m3fn) -> torch
 # flashopt_norm_grad_args, NULL as 0): a third of the time of a ctypes one.
 _NORM_ARGS = struct.Struct("10P6qd4i")
 _NORM_GRAD_ARGS = struct.Struct("8PN6q2i")
+NORM_GRAD_COLS = 32768           # most columns of the backward pass
 
 
 def _vector(t: torch.Tensor, name: str, cols: int, device) -> int:
@@ -1749,6 +1768,9 @@ def _norm_operands(x, gain, residual):
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError(f"residual must be {tuple(x.shape)} of {x.dtype}, got {tuple(residual.shape)} of "
                          f"{residual.dtype}")
+    if gain.shape[0] > NORM_GRAD_COLS and torch.is_grad_enabled() and (
+            x.requires_grad or gain.requires_grad or residual is not None and residual.requires_grad):
+        raise ValueError(f"{gain.shape[0]} columns: gradients have at most {NORM_GRAD_COLS}")
 
 
 def _as(t, shape):
@@ -1793,7 +1815,8 @@ class _RMSNorm(torch.autograd.Function):
 def rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: float = 1e-6):
     """(y, h) with gradients: h = x + residual (x itself without one), x [...,
     cols], and y the root-mean-square norm of h times gain [cols], in x's dtype.
-    Work goes to the current stream; graphs as for mx_linear."""
+    Gradients have at most 32768 columns.  Work goes to the current stream;
+    graphs as for mx_linear."""
     _norm_operands(x, gain, residual)
     if residual is None:
         return _RMSNorm.apply(x, gain, None, eps), x
@@ -1855,7 +1878,7 @@ def fp8_norm_linear(x: torch.Tensor, gain: torch.Tensor, weight, residual=None, 
     The norm writes its output in 8 bits, along rows for the product and along
     columns for the weight's gradient, and in no other form.  weight: a
     parameter [out, in] (several projections stacked share one norm) or an
-    FP8Weight."""
+    FP8Weight.  Otherwise as rms_norm and fp8_linear."""
     w, held = _operands(x, weight, FP8Weight)
     _norm_operands(x, gain, residual)
     args = (x, gain, w, residual, held, eps, torch.is_grad_enabled(), _FP8(grad_dtype))

@@ -599,8 +599,9 @@ flashopt_status flashopt_byte_dequantize(const void *codes, const void *scales, 
  * instructions and rounded once to out's type (bf16 to nearest even).  The
  * instructions form each sum of eight consecutive products to 2^-13 of the
  * largest one's binade (a relative 2e-5 of an output on normally distributed
- * operands, a hundredth of bf16's own rounding).  One launch.  A NaN scale makes its row's (or column's) outputs NaN.  k == 0
- * writes zeros.  A linear layer takes three of these, as for MXFP4.
+ * operands, a hundredth of bf16's own rounding).  One launch.  A NaN scale
+ * makes its row's (or column's) outputs NaN.  k == 0 writes zeros.  A linear
+ * layer takes three of these, as for MXFP4.
  * Errors: EINVAL (sizes, k above 2^24 - 128, out_fp32, a_format, row_stride <
  * n, NULL), EALIGN, EHIP. */
 flashopt_status flashopt_byte_product(const void *a_codes, const void *a_scales, int a_format,
@@ -610,7 +611,8 @@ flashopt_status flashopt_byte_product(const void *a_codes, const void *a_scales,
 
 /* y = quantize(x) w^T for serving: x [m, k] bf16 or fp32, quantized to E4M3
  * along its rows, w [n, k] laid out once.  The result is that of
- * flashopt_byte_quantize and flashopt_byte_product.
+ * flashopt_byte_quantize and flashopt_byte_product.  Two launches; one for a
+ * single row of bf16, which is quantized inside the product.
  *   workspace  DEVICE, 16-byte aligned, holds x's codes until the call has run
  *   out        may lie between x's columns (the same bytes from row to row),
  *              but shares no element with x

@@ -113,3 +113,42 @@ def test_buffers_are_released_with_the_graph(calls):
         y.sum().backward()
         gc.collect()
         assert all(k() is None for k in kept)
+
+
+def test_matrices_of_another_layout_are_refused():
+    """An 8-bit matrix has fewer bytes of scales than the 4-bit calls read, and
+    the reverse of codes."""
+    eight, four = F.FP8Tensor.empty(8, 4096, "cpu"), F.MXTensor.empty(8, 4096, "cpu")
+    x = torch.zeros(2, 4096)
+    for call in (lambda: F.flashopt_mx_product(eight, four), lambda: F.flashopt_mx_product(four, eight),
+                 lambda: F.flashopt_mx_dequantize(eight), lambda: F.flashopt_mx_linear(x, eight),
+                 lambda: F._mx_target(eight, 8, 4096, torch.device("cpu"))):
+        with pytest.raises(ValueError, match="must be an MXTensor, got FP8Tensor"):
+            call()
+    for call in (lambda: F.flashopt_byte_product(eight, four), lambda: F.flashopt_byte_product(four, eight),
+                 lambda: F.flashopt_byte_dequantize(four), lambda: F.flashopt_byte_linear(x, four),
+                 lambda: F._fp8_target(four, 8, 4096, torch.device("cpu"), torch.float8_e4m3fn)):
+        with pytest.raises(ValueError, match="must be an FP8Tensor, got MXTensor"):
+            call()
+    for call in (lambda: F.mx_linear(x, F.FP8Weight.__new__(F.FP8Weight)),
+                 lambda: F.fp8_linear(x, F.MXWeight.__new__(F.MXWeight))):
+        with pytest.raises(ValueError, match="weight must be"):
+            call()
+
+
+def test_gradients_of_too_many_columns_are_refused_in_the_forward_call(calls):
+    cols = F.NORM_GRAD_COLS + 1
+    plain = dict(x=torch.zeros(2, cols), gain=torch.ones(cols), residual=torch.zeros(2, cols))
+    w = torch.zeros(3, cols, requires_grad=True)
+    for name in plain:
+        args = {k: t.clone().requires_grad_(k == name) for k, t in plain.items()}
+        for call in (lambda: F.rms_norm(**args), lambda: F.fp8_norm_linear(weight=w, **args)):
+            with pytest.raises(ValueError, match="gradients have at most 32768"):
+                call()
+        with torch.no_grad():
+            F.rms_norm(**args), F.fp8_norm_linear(weight=w, **args)
+    F.rms_norm(**plain)
+    F.fp8_norm_linear(weight=w, **plain)[0].sum().backward()        # the weight's gradient has no such bound
+    assert w.grad.shape == w.shape and calls[-1] == "product"
+    x = torch.zeros(2, cols - 1, requires_grad=True)
+    F.rms_norm(x, torch.ones(cols - 1))[0].sum().backward()

@@ -554,3 +554,115 @@ def test_offsets_past_32_bits():
     dx, _ = F.flashopt_rms_norm_backward(y, x, gain, rstd, need_dgain=False)
     de, _ = F.flashopt_rms_norm_backward(ye, x[-last:], gain, tail, need_dgain=False)
     assert torch.equal(dx[-last:], de)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [40, 512, 1001, 4096, 8192, 16384, 20000, 32768])
+def test_backward_in_place(cols, dtype):
+    """dx over dy, over dh, and one gradient that is both; more rows than
+    workgroups take at once, so that the next row is loaded under this one."""
+    require_gpu()
+    h, gain = _random((1100, cols), 1, dtype), _random(cols, 2, dtype)
+    dy, dh = _random(h.shape, 3, dtype), _random(h.shape, 4, dtype)
+    rstd = torch.empty(1100, device="cuda")
+    F.flashopt_rms_norm(h, gain, rstd=rstd)
+    want, want_gain = F.flashopt_rms_norm_backward(dy, h, gain, rstd, dh)
+    for over in (0, 1):
+        d = [dy.clone(), dh.clone()]
+        dx, dgain = F.flashopt_rms_norm_backward(d[0], h, gain, rstd, d[1], dx=d[over])
+        assert dx is d[over] and torch.equal(dx, want) and torch.equal(dgain, want_gain)
+        assert torch.equal(d[1 - over], (dh, dy)[over])
+    want, _ = F.flashopt_rms_norm_backward(dy, h, gain, rstd, dy.clone())
+    both = dy.clone()
+    F.flashopt_rms_norm_backward(both, h, gain, rstd, both, dx=both)
+    assert torch.equal(both, want)
+
+
+@pytest.mark.parametrize("shape", [(6, 300), (2, 3, 512)])
+def test_broadcast_and_transposed_operands(shape):
+    """Gradients of a plain sum (stride 0 throughout), rows and residuals that
+    repeat one row, transposed inputs, and x as its own residual: as with copies
+    in rows."""
+    require_gpu()
+    cols, w = shape[-1], _random((200, shape[-1]), 1, BF16)
+    gain = _random(cols, 2, F32)
+
+    def norm(x, residual, g, _):
+        return F.rms_norm(x, g, residual)
+
+    def linear(x, residual, g, weight):
+        return F.fp8_norm_linear(x, g, weight, residual)
+
+    def product(x, residual, g, weight):
+        return (F.fp8_linear(x, weight),)
+    x = _random(shape, 3, BF16)
+    row = _random((cols,), 4, BF16).expand(shape)
+    turned = _random((*shape[:-2], cols, shape[-2]), 5, BF16).transpose(-1, -2)
+    for call in (norm, linear, product):
+        for residual in (None, row, turned) if call is not product else (None,):
+            got = call(x, residual, gain, w)
+            want = call(x, None if residual is None else residual.contiguous(), gain, w)
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for first in (row, turned):
+            assert all(torch.equal(a, b) for a, b in zip(call(first, x if call is not product else None, gain, w),
+                                                         call(first.contiguous(), x if call is not product else None,
+                                                              gain, w)))
+        # the gradient of a sum against that of the same ones in memory
+        for residual in (None, turned) if call is not product else (None,):
+            results = []
+            for dense in (False, True):
+                leaf = x.clone().requires_grad_()
+                outs = [o for o in call(leaf, residual, gain.clone().requires_grad_(), w.clone().requires_grad_())]
+                if dense:
+                    torch.autograd.backward(outs, [torch.ones_like(o).contiguous() for o in outs])
+                else:
+                    sum(o.sum() for o in outs).backward()
+                results.append(leaf.grad)
+            assert torch.equal(*results)
+    for call in (norm, linear):
+        a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+        other = x.clone().requires_grad_()
+        one, two = call(a, a, gain, w), call(b, other, gain, w)
+        assert all(torch.equal(p, q) for p, q in zip(one, two))
+        one[0].sum().backward()
+        two[0].sum().backward()
+        assert torch.equal(b.grad, other.grad) and torch.equal(a.grad, b.grad + other.grad)
+
+
+def test_two_captured_graphs_replayed_in_turn():
+    """Graphs of forward and backward calls share no workspace: replayed in turn
+    and on two streams at once, with eager work between, each gives what its
+    eager call gave."""
+    require_gpu()
+    cases = []
+    for i, (rows, cols, n) in enumerate([(300, 1001, 130), (40, 4096, 512), (1, 2048, 300)]):
+        x, res = _random((rows, cols), 2 * i, BF16), _random((rows, cols), 2 * i + 1, BF16)
+        gain, dy = _random(cols, 10 + i, F32), _random((rows, cols), 20 + i, BF16)
+        w = F.flashopt_byte_quantize(_random((n, cols), 30 + i, BF16))
+        rstd = torch.empty(rows, device="cuda")
+
+        def run(x=x, res=res, gain=gain, dy=dy, w=w, rstd=rstd):
+            (q, t), h = F.flashopt_rms_norm(x, gain, res, output="both", rstd=rstd)
+            dx, dgain = F.flashopt_rms_norm_backward(dy, h, gain, rstd, res)
+            return (h, q.codes.view(torch.uint8), t.codes.view(torch.uint8), t.scales, dx, dgain,
+                    F.flashopt_byte_product(q, w), F.flashopt_byte_linear(x, w))
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run()
+        cases.append((graph, got, want, run))        # run: keeps the inputs, which replays read
+    streams = [torch.cuda.Stream() for _ in cases]
+    for turn in range(4):
+        for _, got, _, _ in cases:
+            for t in got:
+                t.zero_()
+        torch.cuda.synchronize()
+        for (graph, *_), stream in zip(cases, streams):
+            with torch.cuda.stream(stream if turn % 2 else torch.cuda.current_stream()):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, got, want, _ in cases:
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+        F.flashopt_rms_norm_backward(*[_random((50, 700), 1, BF16)] * 2, _random(700, 2, F32),
+                                     torch.ones(50, device="cuda"))
