@@ -1332,6 +1332,17 @@ def _check_fresh(ctx, kind):
         raise RuntimeError(f"the {kind.name} was refreshed between the forward and the backward pass")
 
 
+def _once(backward):
+    """once_differentiable, gone into only where a graph of the backward pass is
+    made: elsewhere gradients are off, and its own time would be a tenth of a
+    small call's."""
+    checked = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return checked(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return run
+
+
 class _Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T with straight-through gradients: dx = Q(dy) Q'(w) and
     dw = Q'(dy)^T Q'(x), Q along rows and Q' along columns (the axis each
@@ -1356,7 +1367,7 @@ class _Linear(torch.autograd.Function):
         return y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy):
         kind, (need_x, need_w) = ctx.kind, ctx.needs_input_grad[:2]
         if need_x:                                   # only the input's gradient reads the weight's copies
@@ -1803,7 +1814,7 @@ class _RMSNorm(torch.autograd.Function):
         return y, h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy, dh=None):
         need_x, need_gain, need_residual, _ = ctx.needs_input_grad
         h, gain, rstd = ctx.saved_tensors
@@ -1848,7 +1859,7 @@ class _FP8NormLinear(torch.autograd.Function):
         return y if residual is None else (y, h)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy, dh=None):
         kind, (need_x, need_gain, need_w, need_residual) = ctx.kind, ctx.needs_input_grad[:4]
         need_dx = need_x or need_residual

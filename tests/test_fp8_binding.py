@@ -152,3 +152,14 @@ def test_gradients_of_too_many_columns_are_refused_in_the_forward_call(calls):
     assert w.grad.shape == w.shape and calls[-1] == "product"
     x = torch.zeros(2, cols - 1, requires_grad=True)
     F.rms_norm(x, torch.ones(cols - 1))[0].sum().backward()
+
+
+def test_a_second_derivative_is_refused(calls):
+    x, w, gain = (torch.ones(*s, requires_grad=True) for s in ((4, 64), (3, 64), (64,)))
+    for out in (F.fp8_linear(x, w), F.rms_norm(x, gain)[0], F.fp8_norm_linear(x, gain, w)[0]):
+        loss = out.square().sum()                 # whose gradient depends on out
+        g, = torch.autograd.grad(loss, x, create_graph=True, retain_graph=False)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            g.sum().backward()
+        with pytest.raises(RuntimeError, match="second time"):      # the first graph was used up
+            loss.backward()
