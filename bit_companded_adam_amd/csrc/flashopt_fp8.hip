@@ -649,15 +649,17 @@ __host__ __device__ constexpr int stage_bytes(bool f32, int tn) { return stage_r
 // a register to LDS; a lane fetches a word, four steps' worth, of each of its
 // rows and shifts it by a byte a step.
 //
-// What bounds it: 8192^3 takes 408 us (2.7 PFLOP/s) with random operands, where
-// the bare instruction on registers reaches 4.05 (4.95 on zeros): the card's
-// power.  The matrix units are busy 71% of the cycles at a clock that is held
-// to 1.9 GHz; without the copies, or without the reads of LDS, a copy of the
-// kernel keeps the same cycles' share at 2.0 and 2.3 GHz.  Two groups of
-// wavefronts in turn, one reading while the other multiplies, are busy 79% at
-// 1.78 GHz and 3% faster on 8192^3, 5% slower over short K; four wavefronts of
-// 128 x 128, a third fewer reads, 5% faster on 8192^3 and as much slower on
-// 8192 x 14336 x 4096.
+// What bounds it: 8192^3 takes 403-422 us (2.6-2.7 PFLOP/s) with random
+// operands, 8192 x 14336 x 4096 365-399, where the bare instruction on registers
+// reaches 4.05 PFLOP/s (4.95 on zeros): the card's power.  The matrix units are
+// busy 71% of the cycles (61% of the second's) at a clock that is held to 1.9
+// GHz; without the copies, or without the reads of LDS, a copy of the kernel
+// keeps the same cycles' share at 2.0 and 2.3 GHz, and without its stores the
+// second takes 5% less.  Two groups of wavefronts in turn, one reading while the
+// other multiplies, are busy 79% at 1.78 GHz and 3% faster on 8192^3, 5% slower
+// over short K; four wavefronts of 128 x 128, a third fewer reads, 5% faster on
+// 8192^3 and as much slower on 8192 x 14336 x 4096; workgroups that start one
+// after another, so that their stores fall apart, 1% slower.
 template <int BN, int BM, int WN, int WM>
 struct Tile {
     static constexpr int kWaves = WN * WM;
