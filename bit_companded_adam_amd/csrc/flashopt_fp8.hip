@@ -666,15 +666,17 @@ struct Tile {
     static constexpr int kTileThreads = kWaves * kWaveLanes;
     static constexpr int kRows = BN + BM;                  // rows of B, then of A
     static constexpr int kBytes = kRows * 128;             // one buffer
-    static constexpr int kCopies = kRows / 8 / kWaves;     // DMA instructions of a wavefront and step
+    // half of the wavefronts copy B, half A: DMA instructions of one and step
+    static constexpr int kCopiesB = BN / 4 / kWaves, kCopiesA = BM / 4 / kWaves;
+    static constexpr int kCopies = kCopiesB > kCopiesA ? kCopiesB : kCopiesA;
     static constexpr int kTN = BN / WN / 32, kTM = BM / WM / 32;
     static constexpr int kWavesPerSimd = BN * BM >= 128 * 128 ? 2 : 4;
     // A's operands of a step in their order, the ring that holds them, and how
     // far ahead of its products one is fetched
-    static constexpr int kSeq = 2 * kTM, kRing = kSeq < 4 ? kSeq : 4, kAhead = kRing - 1;
+    static constexpr int kSeq = 2 * kTM, kRing = kSeq < 4 ? kSeq : kSeq % 4 == 0 ? 4 : 3, kAhead = kRing - 1;
     static constexpr int kLds(bool f32) { return 2 * kBytes + 2 * kRows * 16 + kWaves * stage_bytes(f32, kTN); }
-    static_assert(kRows % (8 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 && kSeq % kRing == 0 &&
-                      kRows <= kTileThreads && BN % (8 * kCopies) == 0 && BN % kWaveLanes == 0, "tile");
+    static_assert(BN % (4 * kWaves) == 0 && BM % (4 * kWaves) == 0 && BN % (32 * WN) == 0 && BM % (32 * WM) == 0 &&
+                      kSeq % kRing == 0 && kRows <= kTileThreads && BN % kWaveLanes == 0, "tile");
 };
 
 template <bool F32, int FMT, int BN, int BM, int WN, int WM>
@@ -703,7 +705,8 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
     // last one, unstored.
     uint32_t pt = blockIdx.x;
     int pk = 0;
-    const bool copy_b = wave * (8 * T::kCopies) < BN, scale_b = wave * kWaveLanes < BN;
+    const bool copy_b = wave < T::kWaves / 2, scale_b = wave * kWaveLanes < BN;
+    const int first_copy = copy_b ? wave * T::kCopiesB : (wave - T::kWaves / 2) * T::kCopiesA;
     const uint8_t *copy_base = nullptr, *scale_base = nullptr;
     uint32_t src[T::kCopies], scale_src = 0;
     // slot s of row r holds chunk s ^ ((r / 2) & 7): for rows 0 to 7 of 16
@@ -718,7 +721,7 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
         copy_base = copy_b ? b.codes + n0 * code_stride : a.codes + m0 * code_stride;
         scale_base = scale_b ? b.scales + n0 * scale_stride : a.scales + m0 * scale_stride;
         const int copy_last = copy_b ? n_last : m_last, scale_last = scale_b ? n_last : m_last;
-        const int first = wave * (8 * T::kCopies) - (copy_b ? 0 : BN) + (lane >> 3);
+        const int first = first_copy * 8 + (lane >> 3);
 #pragma unroll
         for (int i = 0; i < T::kCopies; ++i) {
             const int r = first + 8 * i;
@@ -727,8 +730,12 @@ fp8_tile_kernel(Fp8In a, Fp8In b, int64_t kp, int64_t stride, uint32_t tiles_n, 
         const int r = thread - (scale_b ? 0 : BN);
         scale_src = __umul24(r < scale_last ? r : scale_last, scale_stride);
     };
-    const uint32_t lds_to = lds_offset(s_buf) + wave * (T::kCopies * 1024);
-    auto copy = [&](int i, int buf) { load_to_lds(copy_base, src[i], lds_to + buf * T::kBytes + i * 1024); };
+    const uint32_t lds_to = lds_offset(s_buf) + (copy_b ? 0 : BN * 128) + first_copy * 1024;
+    auto copy = [&](int i, int buf) {
+        if (i >= T::kCopiesB && copy_b) return;
+        if (i >= T::kCopiesA && !copy_b) return;
+        load_to_lds(copy_base, src[i], lds_to + buf * T::kBytes + i * 1024);
+    };
 
     // Quarter q of a lane's row: its chunk 2 q + g; a product takes two.
     const uint32_t off = (lane & 31) * 128 + ((g ^ ((lane >> 1) & 7)) << 4);
@@ -1048,8 +1055,17 @@ hipError_t product_format(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *ou
     // 1000 (208) 9.1 / 10.8, 2048 x 2048 x 2048 (256) 13.3 / 16.8.
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
+    // Of the two largest, 256 x 192 where that takes less of the turns that the
+    // CUs take together, by three quarters of the work a turn.  256 x 256 / 256 x
+    // 192: 5632 x 2048 x 8192 (176 tiles, 240) 96 / 88, 3328 x 3328 x 4096 (169, 234)
+    // 47.3 / 42.5, 2560 x 4096 x 4096 (160, 224) 48 / 43.3, 4096 x 4608 x 4096
+    // (288, 396) 93 / 75, 5632 x 6144 x 2048 (528, 720) 78 / 66.  With fewer tiles, 128
+    // x 128 are ahead: 2048 x 4096 x 4096 (128, 176) 34.5 against 38.3.
+    const int64_t low = ((a.rows + 191) / 192) * ((b.rows + 255) / 256);
+    const bool lower = (low + kCus - 1) / kCus * 3 < (big + kCus - 1) / kCus * 4;
     auto in_tiles = [&](auto fp32) {
         constexpr bool F32 = decltype(fp32)::value;
+        if (big >= 160 && lower) return tiles<F32, FMT, 256, 192, 4, 2>(a, b, k, out, row_bytes, st);
         if (big >= 160) return tiles<F32, FMT, 256, 256, 4, 2>(a, b, k, out, row_bytes, st);
         if (mid >= 160) return tiles<F32, FMT, 128, 128, 2, 2>(a, b, k, out, row_bytes, st);
         return tiles<F32, FMT, 64, 64, 2, 2>(a, b, k, out, row_bytes, st);
