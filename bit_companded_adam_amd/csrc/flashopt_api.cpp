@@ -1390,10 +1390,12 @@ flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, 
     const flashopt_norm_grad_args &p = *args;
     flashopt_status cs = check_norm_sizes(p.rows, p.cols, p.fp32, p.gain_fp32);
     if (cs != FLASHOPT_OK) return cs;
+    if ((p.dy_fp32 != 0 && p.dy_fp32 != 1) || p.reserved != 0) return FLASHOPT_EINVAL;
     if (p.cols > flashopt::kNormGradCols || (!p.dx && !p.dgain)) return FLASHOPT_EINVAL;
     if (p.cols == 0 || (p.rows == 0 && !p.dgain)) return FLASHOPT_OK;
     const bool wide = p.fp32 != 0;
-    const flashopt::NormGradCall n{{const_cast<void *>(p.dy), p.rows, p.cols, p.dy_stride, wide},
+    const bool wide_dy = wide || p.dy_fp32 != 0;
+    const flashopt::NormGradCall n{{const_cast<void *>(p.dy), p.rows, p.cols, p.dy_stride, wide_dy},
                                    {const_cast<void *>(p.dh), p.rows, p.cols, p.dh_stride, wide},
                                    {const_cast<void *>(p.h), p.rows, p.cols, p.h_stride, wide},
                                    {p.dx, p.rows, p.cols, p.dx_stride, wide},
@@ -1404,7 +1406,7 @@ flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, 
                                    static_cast<float *>(p.workspace)};
     if (!aligned(p.dgain, p.gain_fp32 ? 4 : 2)) return FLASHOPT_EALIGN;
     if (p.rows > 0) {
-        if ((cs = check_matrix(n.dy, p.fp32, false)) != FLASHOPT_OK) return cs;
+        if ((cs = check_matrix(n.dy, wide_dy, false)) != FLASHOPT_OK) return cs;
         if ((cs = check_matrix(n.h, p.fp32, false)) != FLASHOPT_OK) return cs;
         if (!p.rstd) return FLASHOPT_EINVAL;
         if ((cs = check_vectors(p.gain, p.gain_fp32, p.rstd)) != FLASHOPT_OK) return cs;
@@ -1421,7 +1423,8 @@ flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, 
             for (int j = i + 1; j < 3; ++j)
                 if (shared(written[i], written[j])) return FLASHOPT_EINVAL;
             for (int j = 0; j < 5; ++j)
-                if (shared(written[i], read[j]) && !(i == 0 && j < 2 && same(written[i], read[j])))
+                if (shared(written[i], read[j]) &&
+                    !(i == 0 && (j == 1 || (j == 0 && wide_dy == wide)) && same(written[i], read[j])))
                     return FLASHOPT_EINVAL;
         }
     }

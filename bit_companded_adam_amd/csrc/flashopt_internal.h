@@ -242,7 +242,7 @@ constexpr int64_t kNormGradCols = 32768;
 // Workgroups of a backward pass that sums dgain, one partial row each.
 constexpr unsigned kNormPartials = 512;
 struct NormGradCall {
-    MxMatrix dy, dh, h, dx;
+    MxMatrix dy, dh, h, dx;                 // dy: of h's type, or fp32
     const void *gain;
     bool gain_fp32;
     const float *rstd;

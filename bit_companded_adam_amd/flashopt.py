@@ -124,7 +124,8 @@ class flashopt_norm_grad_args(ctypes.Structure):
                ("workspace_bytes", ctypes.c_size_t)] + [
                (name, ctypes.c_int64) for name in ("rows", "cols", "dy_stride", "dh_stride", "h_stride",
                                                    "dx_stride")] + [
-               ("fp32", ctypes.c_int32), ("gain_fp32", ctypes.c_int32)]
+               ("fp32", ctypes.c_int32), ("gain_fp32", ctypes.c_int32), ("dy_fp32", ctypes.c_int32),
+               ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -1651,7 +1652,7 @@ def fp8_linear(x: torch.Tensor, weight, grad_dtype=torch.float8_e4m3fn) -> torch
 # The arguments' structures packed in one step (flashopt_norm_args and
 # flashopt_norm_grad_args, NULL as 0): a third of the time of a ctypes one.
 _NORM_ARGS = struct.Struct("10P6qd4i")
-_NORM_GRAD_ARGS = struct.Struct("8PN6q2i")
+_NORM_GRAD_ARGS = struct.Struct("8PN6q4i")
 NORM_GRAD_COLS = 32768           # most columns of the backward pass
 
 
@@ -1668,11 +1669,11 @@ def _vector(t: torch.Tensor, name: str, cols: int, device) -> int:
     return 1 if t.dtype == torch.float32 else 0
 
 
-def _alike(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
-    """The row stride of a matrix of x's size, type and device."""
+def _alike(t: torch.Tensor, name: str, x: torch.Tensor, wide: bool = False) -> int:
+    """The row stride of a matrix of x's size, type (wide: or fp32) and device."""
     if t.shape != x.shape:
         raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(t.shape)}")
-    if t.dtype != x.dtype:
+    if t.dtype != x.dtype and not (wide and t.dtype == torch.float32):
         raise ValueError(f"{name} must be {x.dtype}, got {t.dtype}")
     if t.device != x.device:
         _same_device(x.device, t, name)
@@ -1737,11 +1738,12 @@ def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Te
                                stream=None):
     """(dx, dgain) of flashopt_rms_norm from its h and rstd: dx, in h's dtype, is
     the gradient of x and of the residual, with dh, h's own gradient, added;
-    None for one that is not needed.  dx may be dy or dh itself."""
+    None for one that is not needed.  dy is of h's dtype, or fp32.  dx may be dh,
+    or a dy of its dtype, itself."""
     hp, wide, rows, cols, hstride = _matrix(h, "h")
     dev = h.device
     gwide = _vector(gain, "gain", cols, dev)
-    ystride, estride = _alike(dy, "dy", h), 0 if dh is None else _alike(dh, "dh", h)
+    ystride, estride = _alike(dy, "dy", h, wide=True), 0 if dh is None else _alike(dh, "dh", h)
     sp = _buf(rstd, "rstd", dev, (4,), rows, float32=True)
     with _on(dev, stream):
         xp = xstride = dp = wp = nbytes = 0
@@ -1766,8 +1768,8 @@ def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Te
                 wp, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
         status = lib().flashopt_rms_norm_backward(
             _NORM_GRAD_ARGS.pack(dy.data_ptr(), 0 if dh is None else dh.data_ptr(), hp, gain.data_ptr(), sp, xp, dp,
-                                 wp, nbytes, rows, cols, ystride, estride, hstride, xstride, wide, gwide),
-            _stream(None))
+                                 wp, nbytes, rows, cols, ystride, estride, hstride, xstride, wide, gwide,
+                                 1 if dy.dtype == torch.float32 else 0, 0), _stream(None))
     if status:
         _check(status, "flashopt_rms_norm_backward")
     return dx if need_dx else None, dgain if need_dgain else None
@@ -1835,10 +1837,11 @@ def rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: float = 1e
 
 
 class _FP8NormLinear(torch.autograd.Function):
-    """rms_norm, then _Linear on its output, which exists in 8 bits only."""
+    """rms_norm, then _Linear on its output, which exists in 8 bits only.  The
+    gradient of that output goes from the product to the norm in `between`."""
 
     @staticmethod
-    def forward(ctx, x, gain, w, residual, weight, eps, grad, kind):
+    def forward(ctx, x, gain, w, residual, weight, eps, grad, kind, between):
         ctx.set_materialize_grads(False)
         need_x, need_gain, need_w, need_residual = [need and grad for need in ctx.needs_input_grad[:4]]
         need_dy = need_x or need_gain or need_residual
@@ -1849,7 +1852,7 @@ class _FP8NormLinear(torch.autograd.Function):
                                  "both" if need_w else "rows", rstd=rstd)
         rows, cols = q if need_w else (q, None)
         ctx.kind, ctx.weight, ctx.version = kind, weight, None if weight is None else weight.version
-        ctx.x_dtype, ctx.w_dtype = x.dtype, w.dtype
+        ctx.w_dtype, ctx.between = w.dtype, between
         h = x if residual is None else _as(h, x.shape)
         kept = (cols, w_cols if need_dy else None)
         ctx.kept = [None if t is None else t._size() for t in kept]
@@ -1874,23 +1877,31 @@ class _FP8NormLinear(torch.autograd.Function):
             q = kind.quantize(_flat(dy), layout, grad=True)
             dy_rows, dy_cols = q if layout == "both" else (q, q)
             if need_rows:
-                dn = kind.product(dy_rows, w_cols, ctx.x_dtype)
+                dn = kind.product(dy_rows, w_cols, ctx.between)
             if need_w:
                 dw = kind.product(dy_cols, cols, ctx.w_dtype)
         dx = dgain = None
         if need_dx or need_gain:
             dx, dgain = _norm_backward(dn, dh, h, gain, rstd, need_dx, need_gain)
-        return dx if need_x else None, dgain, dw, dx if need_residual else None, None, None, None, None
+        return dx if need_x else None, dgain, dw, dx if need_residual else None, None, None, None, None, None
 
 
 def fp8_norm_linear(x: torch.Tensor, gain: torch.Tensor, weight, residual=None, eps: float = 1e-6,
-                    grad_dtype=torch.float8_e4m3fn):
+                    grad_dtype=torch.float8_e4m3fn, norm_grad_dtype=None):
     """(out, h): rms_norm and fp8_linear on its output in one, with gradients.
     The norm writes its output in 8 bits, along rows for the product and along
     columns for the weight's gradient, and in no other form.  weight: a
     parameter [out, in] (several projections stacked share one norm) or an
-    FP8Weight.  Otherwise as rms_norm and fp8_linear."""
+    FP8Weight.  norm_grad_dtype: the type in which the gradient of the norm's
+    output goes from the product to the norm's backward pass.  x's unless given,
+    as between two layers: with bf16 the gradients of x and gain then carry two
+    roundings to it, 1.4 times the error of the one at their end; torch.float32
+    saves the inner one and moves 4 more bytes an element.  Otherwise as rms_norm
+    and fp8_linear."""
+    between = norm_grad_dtype or x.dtype
+    if between not in (x.dtype, torch.float32):
+        raise ValueError(f"norm_grad_dtype must be {x.dtype} or torch.float32, got {between}")
     w, held = _operands(x, weight, FP8Weight)
     _norm_operands(x, gain, residual)
-    args = (x, gain, w, residual, held, eps, torch.is_grad_enabled(), _FP8(grad_dtype))
+    args = (x, gain, w, residual, held, eps, torch.is_grad_enabled(), _FP8(grad_dtype), between)
     return (_FP8NormLinear.apply(*args), x) if residual is None else _FP8NormLinear.apply(*args)

@@ -56,7 +56,7 @@
 extern "C" {
 #endif
 
-#define FLASHOPT_ABI_VERSION 10
+#define FLASHOPT_ABI_VERSION 11
 
 typedef enum {
     FLASHOPT_OK = 0,
@@ -662,10 +662,11 @@ flashopt_status flashopt_rms_norm(const flashopt_norm_args *args, void *stream);
  *   dx    = r (u - t c) + dh  fp32, rounded to the type of h: the gradient of
  *                             x and of the residual
  *   dgain = sum over rows of dy t, in an order that depends only on the sizes
- * What is written shares no memory with what is read, but for dx, which may be
- * dy or dh itself. */
+ * dy may be fp32 beside a bf16 h (dy_fp32), as the fp32 output of a product that
+ * went without a rounding to bf16.  What is written shares no memory with what
+ * is read, but for dx, which may be dh, or a dy of its own type, itself. */
 typedef struct {
-    const void *dy;           /* [rows, cols], of h's type                    */
+    const void *dy;           /* [rows, cols], of h's type, or fp32 (dy_fp32) */
     const void *dh;           /* h's own gradient, or NULL                    */
     const void *h;            /* [rows, cols] bf16 or fp32                    */
     const void *gain;         /* [cols]                                       */
@@ -676,10 +677,12 @@ typedef struct {
     size_t workspace_bytes;
     int64_t rows, cols;       /* cols at most 32768                           */
     int64_t dy_stride, dh_stride, h_stride, dx_stride;
-    int32_t fp32, gain_fp32;
+    int32_t fp32, gain_fp32;  /* 0: bf16, 1: fp32                             */
+    int32_t dy_fp32;          /* 0: dy is of h's type, 1: it is fp32          */
+    int32_t reserved;         /* 0                                            */
 } flashopt_norm_grad_args;
-/* Errors: as flashopt_rms_norm (EINVAL also for neither dx nor dgain and for
- * more than 32768 columns); EWORKSPACE.  No rows: dgain is zeros. */
+/* Errors: as flashopt_rms_norm (EINVAL also for a dy_fp32 not 0 or 1, for
+ * neither dx nor dgain and for more than 32768 columns); EWORKSPACE.  No rows: dgain is zeros. */
 size_t flashopt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
 flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, void *stream);
 
