@@ -1303,6 +1303,12 @@ def _flat(x: torch.Tensor) -> torch.Tensor:
     return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
 
 
+def _output(t: torch.Tensor, shape) -> torch.Tensor:
+    """A forward pass's fresh result in its shape.  No view of it: autograd
+    forbids in-place work on a custom function's outputs that are views."""
+    return t if t.dim() == len(shape) else torch.ops.aten._unsafe_view(t, shape)
+
+
 class _MX:
     """MXFP4 as a linear layer uses it."""
     name, tensor = "MXWeight", MXTensor
@@ -1365,7 +1371,7 @@ class _Linear(torch.autograd.Function):
         ctx.kept = [None if t is None else t._size() for t in kept]
         ctx.save_for_backward(*[t._buffer for t in kept if t is not None])
         y = kind.product(x_rows, w_rows, x.dtype)
-        return y.view(*x.shape[:-1], w.shape[0])
+        return _output(y, (*x.shape[:-1], w.shape[0]))
 
     @staticmethod
     @_once
@@ -1807,11 +1813,11 @@ class _RMSNorm(torch.autograd.Function):
         flat = _flat(x)
         rstd = flat.new_empty(flat.shape[0], dtype=torch.float32)
         y, h = flashopt_rms_norm(flat, gain, None if residual is None else _flat(residual), eps, rstd=rstd)
-        y = _as(y, x.shape)
+        y = _output(y, x.shape)
         if residual is None:
             ctx.save_for_backward(x, gain, rstd)
             return y
-        h = _as(h, x.shape)
+        h = _output(h, x.shape)
         ctx.save_for_backward(h, gain, rstd)
         return y, h
 
@@ -1853,12 +1859,12 @@ class _FP8NormLinear(torch.autograd.Function):
         rows, cols = q if need_w else (q, None)
         ctx.kind, ctx.weight, ctx.version = kind, weight, None if weight is None else weight.version
         ctx.w_dtype, ctx.between = w.dtype, between
-        h = x if residual is None else _as(h, x.shape)
+        h = x if residual is None else _output(h, x.shape)
         kept = (cols, w_cols if need_dy else None)
         ctx.kept = [None if t is None else t._size() for t in kept]
         ctx.save_for_backward(h, gain, rstd, *[t._buffer for t in kept if t is not None])
         y = kind.product(rows, w_rows, x.dtype)
-        y = y if x.dim() == 2 else y.view(*x.shape[:-1], w.shape[0])
+        y = _output(y, (*x.shape[:-1], w.shape[0]))
         return y if residual is None else (y, h)
 
     @staticmethod
