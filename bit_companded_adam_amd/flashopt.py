@@ -1180,6 +1180,15 @@ def _out_matrix(out, rows, cols, dtype, device):
     return out
 
 
+def _changed(*tensors):
+    """Tell autograd that tensors of the caller's (None: the call made its own)
+    have been written, as an in-place operation does: a backward pass that has
+    kept one refuses.  Those made in inference mode have no versions."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _quantized(kind, q, name: str):
     """A matrix of another layout has too few bytes for the calls of this one."""
     if not isinstance(q, kind):
@@ -1222,12 +1231,14 @@ def flashopt_mx_quantize(x: torch.Tensor, layout: str = "rows", out=None, stream
 def flashopt_mx_dequantize(q: MXTensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an MXTensor."""
     _quantized(MXTensor, q, "q")
+    given = out
     with _on(q.device, stream):
         out = _out_matrix(out, q.rows, q.cols, dtype, q.device)
         ptr, wide, rows, cols, stride = _matrix(out, "out")
         status = lib().flashopt_mx_dequantize(q.code_ptr, q.scale_ptr, rows, cols, ptr, wide, stride,
                                               _stream(None))
     _check(status, "flashopt_mx_dequantize")
+    _changed(given)
     return out
 
 
@@ -1239,12 +1250,14 @@ def flashopt_mx_product(a: MXTensor, b: MXTensor, dtype=torch.bfloat16, out=None
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     dev = a.device
     _same_device(dev, b, "b")
+    given = out
     with _on(dev, stream):
         out = _out_matrix(out, a.rows, b.rows, dtype, dev)
         ptr, wide, m, n, stride = _matrix(out, "out")
         status = lib().flashopt_mx_product(a.code_ptr, a.scale_ptr, b.code_ptr, b.scale_ptr, m, n, a.cols, ptr,
                                            wide, stride, _stream(None))
     _check(status, "flashopt_mx_product")
+    _changed(given)
     return out
 
 
@@ -1262,6 +1275,7 @@ def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, works
         raise ValueError(f"x has {k} columns, w {w.cols}")
     dev = x.device
     _same_device(dev, w, "w")
+    given = out
     with _on(dev, stream):
         out = _out_matrix(out, m, w.rows, dtype or x.dtype, dev)
         optr, owide, _, n, ostride = _matrix(out, "out")
@@ -1274,6 +1288,7 @@ def flashopt_mx_linear(x: torch.Tensor, w: MXTensor, dtype=None, out=None, works
                                           ostride, _dev(workspace, "workspace"),
                                           workspace.numel() * workspace.element_size(), _stream(None))
     _check(status, "flashopt_mx_linear")
+    _changed(given)
     return out
 
 
@@ -1553,11 +1568,13 @@ def flashopt_byte_quantize(x: torch.Tensor, layout: str = "rows", block: bool = 
 def flashopt_byte_dequantize(q: FP8Tensor, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """The bf16 or fp32 values of an FP8Tensor."""
     _quantized(FP8Tensor, q, "q")
+    given = out
     with _on(q.device, stream):
         out, ptr, wide, stride = _target(out, q.rows, q.cols, dtype, q.device)
         status = lib().flashopt_byte_dequantize(q.code_ptr, q.scale_ptr, q.format, q.rows, q.cols, ptr, wide, stride,
                                                 _stream(None))
     _check(status, "flashopt_byte_dequantize")
+    _changed(given)
     return out
 
 
@@ -1572,11 +1589,13 @@ def flashopt_byte_product(a: FP8Tensor, b: FP8Tensor, dtype=torch.bfloat16, out=
         raise ValueError("b must be float8_e4m3fn")
     dev = a.device
     _same_device(dev, b, "b")
+    given = out
     with _on(dev, stream):
         out, ptr, wide, stride = _target(out, a.rows, b.rows, dtype, dev)
         status = lib().flashopt_byte_product(a.code_ptr, a.scale_ptr, a.format, b.code_ptr, b.scale_ptr, a.rows, b.rows,
                                              a.cols, ptr, wide, stride, _stream(None))
     _check(status, "flashopt_byte_product")
+    _changed(given)
     return out
 
 
@@ -1596,6 +1615,7 @@ def flashopt_byte_linear(x: torch.Tensor, w: FP8Tensor, dtype=None, out=None, wo
         raise ValueError("w must be float8_e4m3fn")
     dev = x.device
     _same_device(dev, w, "w")
+    given = out
     with _on(dev, stream):
         out, optr, owide, ostride = _target(out, m, w.rows, dtype or x.dtype, dev)
         if workspace is None:
@@ -1608,6 +1628,7 @@ def flashopt_byte_linear(x: torch.Tensor, w: FP8Tensor, dtype=None, out=None, wo
         status = lib().flashopt_byte_linear(ptr, wide, m, k, stride, w.code_ptr, w.scale_ptr, w.rows, optr, owide,
                                             ostride, wptr, nbytes, _stream(None))
     _check(status, "flashopt_byte_linear")
+    _changed(given)
     return out
 
 
@@ -1707,6 +1728,7 @@ def flashopt_rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: f
     rstride = 0 if residual is None else _alike(residual, "residual", x)
     if h is not None and residual is None:
         raise ValueError("without a residual there is no sum to write to h")
+    given = (h, out if output == "values" else None, rstd)
     with _on(dev, stream):
         hp = hstride = yp = ystride = c = sc = ct = sct = 0
         if residual is not None:
@@ -1732,6 +1754,7 @@ def flashopt_rms_norm(x: torch.Tensor, gain: torch.Tensor, residual=None, eps: f
                             stride, rstride, hstride, ystride, eps, wide, gwide, fmt, 0), _stream(None))
     if status:
         _check(status, "flashopt_rms_norm")
+    _changed(*given)
     return out, x if residual is None else h
 
 
@@ -1751,6 +1774,7 @@ def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Te
     gwide = _vector(gain, "gain", cols, dev)
     ystride, estride = _alike(dy, "dy", h, wide=True), 0 if dh is None else _alike(dh, "dh", h)
     sp = _buf(rstd, "rstd", dev, (4,), rows, float32=True)
+    given = (dx if need_dx else None, dgain if need_dgain else None)
     with _on(dev, stream):
         xp = xstride = dp = wp = nbytes = 0
         if need_dx:
@@ -1778,6 +1802,7 @@ def flashopt_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, gain: torch.Te
                                  1 if dy.dtype == torch.float32 else 0, 0), _stream(None))
     if status:
         _check(status, "flashopt_rms_norm_backward")
+    _changed(*given)
     return dx if need_dx else None, dgain if need_dgain else None
 
 
