@@ -222,13 +222,14 @@ struct GradIn {
 
 // A workgroup takes rows in turn, as the forward pass does, and keeps its
 // threads' columns of dgain in registers over all of them; partial[workgroup]
-// is added up in order by norm_gain_kernel.  While a row waits for its sum, the
+// is added up in order by norm_gain_kernel.  dx is no __restrict__ pointer: it
+// may be dy or dh itself.  While a row waits for its sum, the
 // next one's loads are under way (kAhead, where registers allow).  DY32: dy is
 // fp32, whatever the other matrices are: 8192 x 2048 beside bf16 29.5 us for
 // 25.6 with a bf16 dy, 8192 x 4096 63 for 44.
 template <bool F32, bool DY32, int TPR, int NV>
 __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads)
-rms_norm_backward_kernel(GradIn in, uint8_t *__restrict__ dx, int64_t dx_bytes, float *__restrict__ partial)
+rms_norm_backward_kernel(GradIn in, uint8_t *dx, int64_t dx_bytes, float *__restrict__ partial)
 {
     constexpr int kGroup = TPR > kThreads ? TPR : kThreads, kRowsAtOnce = TPR > kWaveLanes ? 1 : kGroup / TPR;
     constexpr int kEsz = F32 ? 4 : 2, kDyEsz = DY32 ? 4 : 2;
