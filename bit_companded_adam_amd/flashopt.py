@@ -1822,10 +1822,8 @@ def _as(t, shape):
 
 
 def _norm_backward(dy, dh, h, gain, rstd, need_dx, need_gain):
-    """(dx in h's shape, dgain) from the gradients of the norm's outputs, either
-    of which may be missing."""
-    if dy is None:
-        return dh if need_dx else None, None
+    """(dx in h's shape, dgain) from the gradients of the norm's output and, where
+    there is one, of the sum."""
     dx, dgain = flashopt_rms_norm_backward(dy, _flat(h), gain, rstd, None if dh is None else _flat(dh), need_dx,
                                            need_gain)
     return None if dx is None else _as(dx, h.shape), dgain
@@ -1850,9 +1848,10 @@ class _RMSNorm(torch.autograd.Function):
     @_once
     def backward(ctx, dy, dh=None):
         need_x, need_gain, need_residual, _ = ctx.needs_input_grad
-        h, gain, rstd = ctx.saved_tensors
-        dx, dgain = _norm_backward(None if dy is None else _flat(dy), dh, h, gain, rstd, need_x or need_residual,
-                                   need_gain)
+        if dy is None:                               # the sum alone was used: nothing kept is read
+            dx, dgain = dh, None
+        else:
+            dx, dgain = _norm_backward(_flat(dy), dh, *ctx.saved_tensors, need_x or need_residual, need_gain)
         return dx if need_x else None, dgain, dx if need_residual else None, None
 
 
@@ -1887,7 +1886,8 @@ class _FP8NormLinear(torch.autograd.Function):
         h = x if residual is None else _output(h, x.shape)
         kept = (cols, w_cols if need_dy else None)
         ctx.kept = [None if t is None else t._size() for t in kept]
-        ctx.save_for_backward(h, gain, rstd, *[t._buffer for t in kept if t is not None])
+        norm = (h, gain, rstd) if need_dy else ()
+        ctx.save_for_backward(*[t._buffer for t in kept if t is not None], *norm)
         y = kind.product(rows, w_rows, x.dtype)
         y = _output(y, (*x.shape[:-1], w.shape[0]))
         return y if residual is None else (y, h)
@@ -1897,23 +1897,19 @@ class _FP8NormLinear(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         kind, (need_x, need_gain, need_w, need_residual) = ctx.kind, ctx.needs_input_grad[:4]
         need_dx = need_x or need_residual
-        h, gain, rstd, *saved = ctx.saved_tensors
+        if dy is None:                               # the sum alone was used: nothing kept is read
+            return dh if need_x else None, None, None, dh if need_residual else None, None, None, None, None, None
+        need_rows = need_dx or need_gain
+        if need_rows:
+            _check_fresh(ctx, kind)
+        saved = list(ctx.saved_tensors)
         cols, w_cols = [None if k is None else kind.tensor._over(saved.pop(0), *k) for k in ctx.kept]
-        dn = dw = None
-        if dy is not None:
-            need_rows = need_dx or need_gain
-            if need_rows:
-                _check_fresh(ctx, kind)
-            layout = "both" if need_rows and need_w else "rows" if need_rows else "cols"
-            q = kind.quantize(_flat(dy), layout, grad=True)
-            dy_rows, dy_cols = q if layout == "both" else (q, q)
-            if need_rows:
-                dn = kind.product(dy_rows, w_cols, ctx.between)
-            if need_w:
-                dw = kind.product(dy_cols, cols, ctx.w_dtype)
-        dx = dgain = None
-        if need_dx or need_gain:
-            dx, dgain = _norm_backward(dn, dh, h, gain, rstd, need_dx, need_gain)
+        layout = "both" if need_rows and need_w else "rows" if need_rows else "cols"
+        q = kind.quantize(_flat(dy), layout, grad=True)
+        dy_rows, dy_cols = q if layout == "both" else (q, q)
+        dn = kind.product(dy_rows, w_cols, ctx.between) if need_rows else None
+        dw = kind.product(dy_cols, cols, ctx.w_dtype) if need_w else None
+        dx, dgain = _norm_backward(dn, dh, *saved, need_dx, need_gain) if need_rows else (None, None)
         return dx if need_x else None, dgain, dw, dx if need_residual else None, None, None, None, None, None
 
 
