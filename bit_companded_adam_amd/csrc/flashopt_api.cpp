@@ -1381,7 +1381,7 @@ flashopt_status flashopt_rms_norm(const flashopt_norm_args *args, void *stream)
 size_t flashopt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0 || check_size(rows, cols) != FLASHOPT_OK) return 0;
-    return static_cast<size_t>(cols) * flashopt::kNormPartials * sizeof(float);
+    return static_cast<size_t>(flashopt::norm_grad_partials(rows, cols)) * sizeof(float);
 }
 
 flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, void *stream)
@@ -1416,7 +1416,11 @@ flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, 
         if (need > 0 && (!p.workspace || p.workspace_bytes < need)) return FLASHOPT_EWORKSPACE;
         if (need > 0 && !aligned(p.workspace, 16)) return FLASHOPT_EALIGN;
         const size_t gain_bytes = static_cast<size_t>(p.cols) * (p.gain_fp32 ? 4 : 2);
-        const Region written[3] = {region(n.dx), flat(p.dgain, gain_bytes), flat(p.workspace, need)};
+        // the workspace counts up to what so many columns take with any number of
+        // rows: whether memory is shared does not hang on them
+        const size_t most = need > 0 ? flashopt_rms_norm_backward_workspace_bytes(INT32_MAX, p.cols) : 0;
+        const Region written[3] = {region(n.dx), flat(p.dgain, gain_bytes),
+                                   flat(p.workspace, most < p.workspace_bytes ? most : p.workspace_bytes)};
         const Region read[5] = {region(n.dy), region(n.dh), region(n.h), flat(p.gain, gain_bytes),
                                 flat(p.rstd, static_cast<size_t>(p.rows) * 4)};
         for (int i = 0; i < 3; ++i) {

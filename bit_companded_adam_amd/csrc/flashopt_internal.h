@@ -239,15 +239,17 @@ hipError_t launch_rms_norm(const NormCall &n, hipStream_t stream);
 
 // Most columns of a backward pass: a row stays in registers.
 constexpr int64_t kNormGradCols = 32768;
-// Workgroups of a backward pass that sums dgain, one partial row each.
-constexpr unsigned kNormPartials = 512;
+// Elements of the workspace of a backward pass that sums dgain: a partial row for
+// each of its workgroups.  It falls neither with rows nor with cols: what is
+// made for the largest pass serves them all.
+int64_t norm_grad_partials(int64_t rows, int64_t cols);
 struct NormGradCall {
     MxMatrix dy, dh, h, dx;                 // dy: of h's type, or fp32
     const void *gain;
     bool gain_fp32;
     const float *rstd;
     void *dgain;
-    float *partial;          // [kNormPartials][cols]
+    float *partial;          // norm_grad_partials(rows, cols) of them
 };
 hipError_t launch_rms_norm_backward(const NormGradCall &n, hipStream_t stream);
 

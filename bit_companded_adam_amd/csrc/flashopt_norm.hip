@@ -395,6 +395,16 @@ unsigned row_groups(int64_t rows)
     return static_cast<unsigned>(TPR > kWaveLanes ? rows : (rows + kThreads / TPR - 1) / (kThreads / TPR));
 }
 
+// Workgroups of a backward pass: two to a CU, one of 512 threads or more (with
+// two, 8192 x 8192 takes 50.0 us instead of 45.2, for the partial rows).
+template <int TPR>
+unsigned backward_groups(int64_t rows)
+{
+    constexpr unsigned kMost = TPR >= 512 ? kCus : 2 * kCus;
+    const unsigned groups = row_groups<TPR>(rows);
+    return groups < kMost ? groups : kMost;
+}
+
 template <bool F32>
 hipError_t norm_type(const NormIn &in, const NormOut &out, hipStream_t st)
 {
@@ -416,12 +426,7 @@ hipError_t backward_type(const GradIn &in, uint8_t *dx, int64_t dx_bytes, uint8_
         if constexpr (NV == 0) {
             return hipErrorInvalidValue;
         } else {
-            const unsigned groups = row_groups<TPR>(in.rows);
-            // two workgroups to a CU, one of 512 threads or more: with two, 8192 x
-            // 8192 takes 50.0 us instead of 45.2, for the partial rows
-            constexpr unsigned kMost = TPR >= 512 ? kCus : 2 * kCus;
-            static_assert(kMost <= kNormPartials, "partial rows");
-            const unsigned grid = groups < kMost ? groups : kMost;
+            const unsigned grid = backward_groups<TPR>(in.rows);
             if (grid > 0) {
                 hipLaunchKernelGGL((rms_norm_backward_kernel<F32, DY32, TPR, NV>), dim3(grid),
                                    dim3(TPR > kThreads ? TPR : kThreads), 0, st, in, dx, dx_bytes, partial);
@@ -437,6 +442,23 @@ hipError_t backward_type(const GradIn &in, uint8_t *dx, int64_t dx_bytes, uint8_
 }
 
 }  // namespace
+
+int64_t norm_grad_partials(int64_t rows, int64_t cols)
+{
+    int64_t most = 0;
+    auto with = [&](int64_t c) {
+        (void)by_columns(c, [&](auto tpr, auto) {
+            const int64_t size = backward_groups<decltype(tpr)::value>(rows) * c;
+            most = size > most ? size : most;
+            return hipSuccess;
+        });
+    };
+    // a narrower pass may have more workgroups: the widest of each of by_columns'
+    for (int64_t c : {512, 1024, 2048, 4096, 8192, 16384, 32768})
+        if (c < cols) with(c);
+    with(cols);
+    return most;
+}
 
 hipError_t launch_rms_norm(const NormCall &n, hipStream_t st)
 {

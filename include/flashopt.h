@@ -682,7 +682,10 @@ typedef struct {
     int32_t reserved;         /* 0                                            */
 } flashopt_norm_grad_args;
 /* Errors: as flashopt_rms_norm (EINVAL also for a dy_fp32 not 0 or 1, for
- * neither dx nor dgain and for more than 32768 columns); EWORKSPACE.  No rows: dgain is zeros. */
+ * neither dx nor dgain and for more than 32768 columns); EWORKSPACE.  No rows:
+ * dgain is zeros.  The workspace's bytes fall neither with rows nor with cols: a
+ * buffer made for the largest pass serves all.  What so many columns take with
+ * any number of rows counts as written, as far as the buffer reaches. */
 size_t flashopt_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
 flashopt_status flashopt_rms_norm_backward(const flashopt_norm_grad_args *args, void *stream);
 
