@@ -350,9 +350,9 @@ __device__ __forceinline__ f32x4 mfma16(i32x8 b, i32x8 a, f32x4 c, uint32_t sb, 
 // fp32 unscaled and then scaled by both scales' exponents together.
 //
 // Bound by memory: with the weight in cache / with weights in turn that no cache
-// holds 14336 x 4096 takes 11.6 / 12.4 us (59 MB: 5.1 / 4.7 TB/s), 4096 x 14336
-// 11.5 / 13.2, 4096 x 4096 4.8 / 5.6, 28672 x 8192 34.6 / 43.3.  (As a tile of 16
-// rows of A by fp8_few_kernel: 12.4 / 17.3, 11.6 / 13.4, 5.3 / 7.0, 37 / 47; with
+// holds 14336 x 4096 takes 11.5 / 12.3 us (59 MB: 5.1 / 4.8 TB/s), 4096 x 14336
+// 11.8 / 14.0, 4096 x 4096 4.5 / 5.9, 28672 x 8192 36.8 / 45.  (As a tile of 16
+// rows of A by fp8_few_kernel: 12.4 / 17.2, 11.7 / 13.7, 5.0 / 7.0, 38 / 47; with
 // one row to a wavefront, four or eight, or fewer wavefronts to a row, up to 20%
 // slower.  Two rows of A are level with the tile.)
 constexpr int kVectorRows = 2, kVectorWaves = kThreads / kWaveLanes;
@@ -472,10 +472,10 @@ fp8_vector_kernel(A a, Fp8In b, int64_t kp, int64_t stride, uint8_t *__restrict_
 // of its own by the DMA, up to three ahead, and waits for nobody.  Scales go to
 // LDS 128 steps at a time.  LDS holds rows as the tiles below do.
 //
-// What bounds it is how much a CU has under way: 48 x 4096 x 14336 takes 14.3 us
-// with the weight in cache and 19.6 with weights in turn that no cache holds
-// (59 MB: 4.1 and 3.0 TB/s), 16 x 14336 x 4096 12.4 and 17.3, 256 x 4096 x 14336
-// 25.6 and 34.5.  (Loaded by the lanes that use them, operands take sixteen
+// What bounds it is how much a CU has under way: 48 x 4096 x 14336 takes 14.6 us
+// with the weight in cache and 20-22 with weights in turn that no cache holds
+// (59 MB: 4.0 and 2.8 TB/s), 16 x 14336 x 4096 12.7 and 18-19, 256 x 4096 x 14336
+// 25.5 and 34.  (Loaded by the lanes that use them, operands take sixteen
 // rows' half lines an instruction, where the copies take eight rows' whole
 // ones, and the first of these 34 us, or 30 with four steps' loads at once.)
 constexpr int kFewWaves = 4, kFewThreads = kFewWaves * kWaveLanes;
@@ -649,8 +649,9 @@ __host__ __device__ constexpr int stage_bytes(bool f32, int tn) { return stage_r
 // a register to LDS; a lane fetches a word, four steps' worth, of each of its
 // rows and shifts it by a byte a step.
 //
-// What bounds it: 8192^3 takes 403-422 us (2.6-2.7 PFLOP/s) with random
-// operands, 8192 x 14336 x 4096 365-399, where the bare instruction on registers
+// What bounds it: 8192^3 takes 401-422 us (2.6-2.7 PFLOP/s) with random
+// operands, 8192 x 14336 x 4096 365-399 (of fp32 outputs, twice their bytes, 438
+// and 421), where the bare instruction on registers
 // reaches 4.05 PFLOP/s (4.95 on zeros): the card's power.  The matrix units are
 // busy 71% of the cycles (61% of the second's) at a clock that is held to 1.9
 // GHz; without the copies, or without the reads of LDS, a copy of the kernel
@@ -1012,9 +1013,9 @@ hipError_t tiles(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *out, int64_
 
 // Elements of K from which 64 x 64 tiles, one or less to a CU, go to
 // fp8_few_kernel, whose wavefronts split K, instead of fp8_tile_kernel.  M x N x
-// K in us, there / here: 1024 x 1000 x 1000 6.0 / 7.1, 200 x 4096 x 2048 7.9 /
-// 7.7, 512 x 2048 x 2048 8.0 / 7.8, 256 x 4096 x 4096 12.3 / 11.0, 256 x 4096 x
-// 14336 54.7 / 25.6.
+// K in us, by its tiles / by fp8_few_kernel: 1024 x 1000 x 1000 5.9 / 7.2, 200 x
+// 4096 x 2048 7.8 / 7.7, 512 x 2048 x 2048 7.9 / 7.8, 256 x 4096 x 4096 12.4 / 11.2,
+// 256 x 4096 x 14336 55.5 / 26.
 constexpr int64_t kFewInner = 2048;
 
 template <int FMT>
@@ -1024,11 +1025,11 @@ hipError_t product_format(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *ou
     if (a.rows == 1) return vector(StoredRow<FMT>{a.codes, a.scales}, b, k, out, out_fp32, st);
     // The smallest tiles of which a CU gets one at most: a larger one reads A and
     // B less often, a smaller one leaves fewer CUs idle.  M x N x K in us, tiles
-    // of 16 MT x 16 NT: 48 x 4096 x 14336 2 x 2 (256 tiles) 14.3, 3 x 2 17.1, 2 x 4
-    // 18.1, 2 x 1 22.4; 48 x 14336 x 4096 3 x 4 (224) 14.1, 3 x 2 16.2, 2 x 2 25.2;
-    // 24 x 6144 x 4096 2 x 2 (192) 7.8, 2 x 1 11.0; 64 x 2048 x 5632 2 x 1 (256)
-    // 6.2, 2 x 2 6.6, 4 x 1 7.3; 128 x 4096 x 14336 4 x 2 (256) 19.9, 4 x 4 24.6, 2
-    // x 2 27.1.
+    // of 16 MT x 16 NT: 48 x 4096 x 14336 2 x 2 (256 tiles) 14.6, 3 x 2 17.4, 2 x 4
+    // 18.4, 2 x 1 22.6; 48 x 14336 x 4096 3 x 4 (224) 14.5, 3 x 2 19.8, 2 x 2 27.9;
+    // 24 x 6144 x 4096 2 x 2 (192) 7.0, 2 x 1 10.1; 64 x 2048 x 5632 2 x 1 (256)
+    // 6.5, 2 x 2 6.8, 4 x 1 7.5; 128 x 4096 x 14336 4 x 2 (256) 20.7, 4 x 4 25.2, 2
+    // x 2 27.5.
     const int64_t m16 = (a.rows + 15) / 16;
     auto fits = [&](int mt, int nt) { return mt <= m16 && few_tiles(a, b, mt, nt) <= kCus; };
     if (fits(1, 1)) return few<FMT, 1, 1>(a, b, k, out, out_fp32, row_bytes, st);
@@ -1036,9 +1037,9 @@ hipError_t product_format(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *ou
     if (m16 == 1 && fits(1, 2)) return few<FMT, 1, 2>(a, b, k, out, out_fp32, row_bytes, st);
     if (fits(2, 2)) return few<FMT, 2, 2>(a, b, k, out, out_fp32, row_bytes, st);
     // One tile of A's rows, and B of more rows than that: 16 x 14336 x 4096 1 x 4
-    // (224) 12.4, 1 x 1 14.0; 16 x 28672 x 8192 1 x 4 (448) 39.5, 1 x 1 (several to a
-    // CU at once) 38.4, from memory 59.7 and 54.0; 32 x 28672 x 8192 2 x 4 40.3, 2 x 1
-    // 54.1; 64 x 14336 x 4096 4 x 4 15.0, 64 x 64 tiles below 19.0.
+    // (224) 12.7, 1 x 1 15.1; 16 x 28672 x 8192 1 x 4 (448) 39.8, 1 x 1 (several to a
+    // CU at once) 38.4, from memory 60.9 and 55.1; 32 x 28672 x 8192 2 x 4 41.5, 2 x 1
+    // 53.0; 64 x 14336 x 4096 4 x 4 15.3, 64 x 64 tiles below 19.2.
     if (m16 == 1)
         return fits(1, 4) ? few<FMT, 1, 4>(a, b, k, out, out_fp32, row_bytes, st)
                           : few<FMT, 1, 1>(a, b, k, out, out_fp32, row_bytes, st);
@@ -1049,18 +1050,19 @@ hipError_t product_format(const Fp8In &a, const Fp8In &b, int64_t k, uint8_t *ou
     if (m16 == 4 || (fits(4, 4) && k >= kFewInner)) return few<FMT, 4, 4>(a, b, k, out, out_fp32, row_bytes, st);
     // The largest tile of which 160 are there for the 256 CUs: it reads A and B the
     // least often.  M x N x K in us, tiles of 256 / 128: 2048 x 4096 x 4096 (128 of
-    // 256) 49.5 / 39.3, 2048 x 5120 x 4096 (160) 47.8 / 51.0, 2048 x 5120 x 1024 18.5 /
-    // 17.5, 3328 x 3328 x 4096 (169) 47.3 / 50.0; tiles of 128 / 64: 1024 x 2048 x 2048
-    // (128 of 128) 12.6 / 10.6, 1280 x 2048 x 2048 (160) 13.1 / 13.2, 1024 x 3328 x
-    // 1000 (208) 9.1 / 10.8, 2048 x 2048 x 2048 (256) 13.3 / 16.8.
+    // 256) 50.7 / 35.9, 2048 x 5120 x 4096 (160) 48.1 / 50.3, 2048 x 5120 x 1024 18.5 /
+    // 18.5, 3328 x 3328 x 4096 (169) 48.7 / 51.3; tiles of 128 / 64: 1024 x 2048 x 2048
+    // (128 of 128) 11.6 / 9.3, 1280 x 2048 x 2048 (160) 12.3 / 12.1, 1024 x 3328 x
+    // 1000 (208) 8.9 / 10.3, 2048 x 2048 x 2048 (256) 13.3 / 16.7.
     const int64_t big = ((a.rows + 255) / 256) * ((b.rows + 255) / 256);
     const int64_t mid = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
     // Of the two largest, 256 x 192 where that takes less of the turns that the
     // CUs take together, by three quarters of the work a turn.  256 x 256 / 256 x
-    // 192: 5632 x 2048 x 8192 (176 tiles, 240) 96 / 88, 3328 x 3328 x 4096 (169, 234)
-    // 47.3 / 42.5, 2560 x 4096 x 4096 (160, 224) 48 / 43.3, 4096 x 4608 x 4096
-    // (288, 396) 93 / 75, 5632 x 6144 x 2048 (528, 720) 78 / 66.  With fewer tiles, 128
-    // x 128 are ahead: 2048 x 4096 x 4096 (128, 176) 34.5 against 38.3.
+    // 192: 5632 x 2048 x 8192 (176 tiles, 240) 90 / 80, 3328 x 3328 x 4096 (169, 234)
+    // 48.7 / 43.7, 2560 x 4096 x 4096 (160, 224) 47.5 / 42.2, 2048 x 5120 x 1024 (160,
+    // 220) 18.5 / 16.4, 4096 x 4608 x 4096 (288, 396) 94 / 78, 5632 x 6144 x 2048 (528,
+    // 720) 79 / 70.  With fewer tiles, 128 x 128 are ahead: 2048 x 4096 x 4096 (128,
+    // 176) 35.9 against 40.6.
     const int64_t low = ((a.rows + 191) / 192) * ((b.rows + 255) / 256);
     const bool lower = (low + kCus - 1) / kCus * 3 < (big + kCus - 1) / kCus * 4;
     auto in_tiles = [&](auto fp32) {

@@ -16,7 +16,9 @@
 // registers between the sum and the output.  With a residual, bf16, 8192 x 4096
 // takes 41-44 us to 8 bits (235 MB: 5.5 TB/s) and 42 to bf16 (268 MB: 6.4), its
 // backward pass with dh 44 (268 MB: 6.1); 8192 x 2048 23 and 26; one row of 4096
-// 3.9 and 5.7, which is latency.  (Sums over a wavefront by LDS permutations
+// 3.8 and 5.7, which is latency.  Beyond 16384 columns a backward thread holds
+// four vectors of three matrices and spills: 2048 x 16384 takes 59 us (4.6 TB/s),
+// 2048 x 20000 101 (3.2).  (Sums over a wavefront by LDS permutations
 // instead of DPP, and the gain loaded after the sum, cost the first of these 15
 // us; without the next row's loads under way the backward pass takes 58.)
 
