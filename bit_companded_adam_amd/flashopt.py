@@ -1159,7 +1159,7 @@ def _matrix(x: torch.Tensor, name: str):
         raise ValueError(f"{name} must be bf16 or fp32, got {x.dtype}")
     rows, cols = x.shape
     stride, inner = x.stride()
-    if inner != 1 and cols > 1:
+    if inner != 1 and cols > 1 and rows > 0:      # (without rows, strides are whatever they were)
         raise ValueError(f"{name}'s rows must be contiguous")
     return x.data_ptr(), int(x.dtype == torch.float32), rows, cols, stride if rows > 1 else cols
 
@@ -1705,7 +1705,7 @@ def _alike(t: torch.Tensor, name: str, x: torch.Tensor, wide: bool = False) -> i
     if t.device != x.device:
         _same_device(x.device, t, name)
     stride, inner = t.stride()
-    if inner != 1 and t.shape[1] > 1:
+    if inner != 1 and t.shape[1] > 1 and t.shape[0] > 0:
         raise ValueError(f"{name}'s rows must be contiguous")
     return stride if t.shape[0] > 1 else t.shape[1]
 
